@@ -2,7 +2,10 @@
  * moe_capi.h — C ABI of the B200 (sm_100a) DeepSeekMoE layer: the forward,
  * the bias controller, node-limited routing, the sequence-wise balance
  * statistics, the FP8 backward of the expert path, and the layer with its
- * routed experts sharded over several GPUs (expert parallelism).
+ * routed experts sharded over several GPUs (expert parallelism). Beside the
+ * layer: products grouped by expert in 16 bits with their gradients, the
+ * norms before and after the layer's block with its gate and residual, and
+ * the global gradient norm with clipping.
  *
  * The layer (sources: "DeepSeek-V3: Auxiliary-Loss-Free MoE Load Balancing,
  * Multi-Token Prediction, and FP8 Training at 671B Scale", trishampatil.com,
@@ -395,6 +398,135 @@ int moe_expert_down_bf16(int32_t H, int32_t I, int32_t n_groups, const int32_t* 
                          const int32_t* group_start, int64_t rows, const uint8_t* h_q,
                          const float* h_s, const uint8_t* w2, const float* s2, void* y_rows,
                          uint32_t* status_ws, void* stream);
+
+/* Element types of the 16-bit grouped products, the block norms and the
+ * gradient lists. */
+typedef enum { MOE_BF16 = 0, MOE_FP16 = 1, MOE_FP32 = 2 } moe_type;
+
+/*
+ * Products grouped by expert in 16 bits (the grouped expert GEMMs above are
+ * FP8): per-expert linear maps for weights kept in bf16 or fp16, over ragged
+ * groups. Group g (0 <= g < n_groups, n_groups <= 1025) owns rows
+ * [group_start[g], group_start[g] + group_rows[g]) of the row buffers, at any
+ * alignment (packed rows, or the 128-aligned starts of the forward's
+ * workspace). group_rows and group_start are DEVICE int32 arrays [n_groups];
+ * non-empty groups must ascend without overlap inside [0, rows). A group that
+ * does not is treated as empty and sets the bounds bit of status_ws.
+ *
+ * moe_grouped_matmul:
+ *   trans_b != 0: out[r, n] = sum_k a[r, k] b[g, n, k]   b [n_groups, N, K]
+ *   trans_b == 0: out[r, n] = sum_k a[r, k] b[g, k, n]   b [n_groups, K, N]
+ *   The second form with the forward's weights gives the input gradient
+ *   (a = dy) without a transposed copy of them.
+ *   a [rows, K], out [rows, N]. Rows outside every group are neither read
+ *   into a result nor written.
+ * moe_grouped_wgrad: dw[g, n, k] = sum over the group's rows dy[r, n] x[r, k],
+ *   added to what dw holds when accumulate != 0. dy [rows, N], x [rows, K],
+ *   dw [n_groups, N, K]. An empty group's dw is zero (accumulating: unchanged).
+ *
+ * type: MOE_BF16 or MOE_FP16 (a and b, or dy and x, alike); out_type: the
+ * same, or MOE_FP32. Sums are fp32, rounded once to out_type; their order is
+ * fixed, so results are reproducible. An infinity or NaN stays in the output
+ * rows (for the weight gradient: in the group) it belongs to. N and K are
+ * multiples of 8 up to 2^20; pointers 16-byte aligned; rows < 2^31 - 256
+ * (rows = 0: the row buffers may be NULL). out and dw must not overlap the
+ * inputs. status_ws: a device uint32 status word, or NULL (may be the forward
+ * workspace); read by moe_get_status.
+ */
+int moe_grouped_matmul(int32_t type, int32_t out_type, int32_t n_groups, const int32_t* group_rows,
+                       const int32_t* group_start, int64_t rows, int32_t K, int32_t N,
+                       const void* a, const void* b, int32_t trans_b, void* out,
+                       uint32_t* status_ws, void* stream);
+
+int moe_grouped_wgrad(int32_t type, int32_t out_type, int32_t n_groups, const int32_t* group_rows,
+                      const int32_t* group_start, int64_t rows, int32_t N, int32_t K,
+                      const void* dy, const void* x, void* dw, int32_t accumulate,
+                      uint32_t* status_ws, void* stream);
+
+/*
+ * Norms before and after a block, with its gate and residual scale (the
+ * Transformer block around the layer: "DeepSeek-V3: Auxiliary-Loss-Free MoE
+ * Load Balancing, ..."). With N(v; w) = v rsqrt(mean(v^2) + eps) w,
+ * row by row:
+ *   r = x + alpha * scale * gate * N(z; post)
+ *   u = N(r; pre)
+ * The forms: z NULL: r is x and only u is made (the norm before the block,
+ * pre required). z given, pre NULL: only r is made (after it). Both: r and
+ * the next block's input u in one pass. post NULL: z itself in place of its
+ * norm. scale: [H] or NULL (1). gate_kind 0: none, 1: float [T], one per row,
+ * 2: [T, H] of act_type.
+ *   x, r: [T, H] of res_type (the residual stream); z, u: [T, H] of act_type;
+ *   pre, post, scale: [H] of w_type.
+ * act_type: any moe_type; res_type and w_type: act_type or MOE_FP32. Sums and
+ * all arithmetic in fp32; u comes from the unrounded r. r may be x, and u may
+ * be z; no other overlap. H: 1 to MOE_BLOCK_NORM_MAX_H. Any alignment of the
+ * elements' own size; 16-byte aligned rows (H a multiple of 8) are faster.
+ * T = 0 is a no-op.
+ *
+ * moe_block_norm_backward, for the upstream gradients dr and du of r and u:
+ *   r    the forward's r (its x where z was NULL), z, gate and weights as given
+ *        to the forward
+ *   dr   [T, H] of res_type or NULL (zero; only with pre); du [T, H] of
+ *        act_type, required with pre
+ *   dx   [T, H] of res_type, the gradient of x: required with pre; without
+ *        pre it equals dr and is not written
+ *   dz   [T, H] of act_type (with z); dgate: like gate, float [T] or [T, H]
+ *   dpre, dpost, dscale: float [H], for those weights that are given
+ *   ws: moe_block_norm_backward_workspace_size(H) bytes, 256-byte aligned; no
+ *        other call that may run at the same time can use it.
+ * Both statistics are recomputed from r and z. Column sums run in an order
+ * that depends on T and H alone: results are reproducible. dx may be dr, and
+ * dz may be z or du; no other overlap. T = 0: dpre, dpost and dscale are zero.
+ */
+#define MOE_BLOCK_NORM_MAX_H 16384
+int moe_block_norm(int64_t T, int32_t H, int32_t res_type, int32_t act_type, int32_t w_type,
+                   int32_t gate_kind, float alpha, float eps, const void* x, const void* z,
+                   const void* gate, const void* pre, const void* post, const void* scale, void* r,
+                   void* u, void* stream);
+
+size_t moe_block_norm_backward_workspace_size(int32_t H);
+
+int moe_block_norm_backward(int64_t T, int32_t H, int32_t res_type, int32_t act_type,
+                            int32_t w_type, int32_t gate_kind, float alpha, float eps,
+                            const void* r, const void* z, const void* gate, const void* pre,
+                            const void* post, const void* scale, const void* dr, const void* du,
+                            void* dx, void* dz, void* dgate, float* dpre, float* dpost,
+                            float* dscale, void* ws, size_t ws_bytes, void* stream);
+
+/*
+ * Global gradient norm and clipping over many tensors (the weight gradients
+ * of moe_backward and moe_grouped_wgrad, the router's, the norms'):
+ *   norm = sqrt(sum of all squares),  c = min(1, max_norm / (norm + 1e-6)),
+ *   out = g * c
+ * A list holds n tensors as HOST arrays of device pointers: grads[i] with
+ * sizes[i] contiguous elements of moe_type types[i]; out[i] of the same size
+ * and type, or out NULL to scale in place. The arrays are read during the
+ * call only. Elements of their own size's alignment; tensors may be empty and
+ * may differ in type. Outputs must not overlap one another, nor another
+ * tensor's gradients.
+ *
+ * moe_grad_sumsq leaves MOE_GRAD_PARTIALS partial sums of squares (double);
+ *   their sum is the squared norm. With the experts sharded over several GPUs
+ *   the ranks add their arrays element by element (an all-reduce of 8 KiB)
+ *   before they clip.
+ * moe_grad_clip adds the partials, writes the norm (float [1]) and scales.
+ *   max_norm >= 0, infinity allowed. In place nothing is touched when c = 1.
+ * Squares are summed in fp64, in a fixed order. A NaN in any gradient makes
+ * the norm and every gradient NaN; an infinity makes the norm infinite, the
+ * infinite gradients NaN and the others zero.
+ */
+typedef struct {
+  int32_t n;
+  const void* const* grads;
+  void* const* out;
+  const int64_t* sizes;
+  const int32_t* types;
+} moe_grad_list;
+#define MOE_GRAD_PARTIALS 1024
+int moe_grad_sumsq(const moe_grad_list* list, double* partials, void* stream);
+
+int moe_grad_clip(const moe_grad_list* list, const double* partials, float max_norm, float* norm,
+                  void* stream);
 
 /*
  * Expert parallelism ("DeepSeek-V3: Auxiliary-Loss-Free MoE Load Balancing,

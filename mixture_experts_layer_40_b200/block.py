@@ -1,0 +1,145 @@
+"""The Transformer block around an MoE layer, per-expert linear maps in 16
+bits, and gradient clipping: thin holders of device memory over the C ABI, as
+layer.MoELayer is. All compute is in the CUDA library.
+"""
+from __future__ import annotations
+
+import torch
+
+from . import capi
+from .layer import MoELayer
+
+
+class MoEBlock:
+    """r = x + alpha * scale * gate * N(layer(N(x; pre_weight)); post_weight):
+    the norm before the MoE layer, the layer, and the norm after it with its
+    gate and residual. post_weight, scale (weights [H], bf16 or float32 alike)
+    and gate (float32 [T], or bf16 [T, H]) are optional. x is bf16 or float32;
+    the layer runs on bf16. The block keeps the last forward's x, u and the
+    layer's output for the backward."""
+
+    def __init__(self, layer: MoELayer, pre_weight: torch.Tensor,
+                 post_weight: torch.Tensor | None = None, scale: torch.Tensor | None = None,
+                 alpha: float = 1.0, eps: float = 1e-6):
+        self.layer, self.alpha, self.eps = layer, alpha, eps
+        self.pre_weight, self.post_weight, self.scale = pre_weight, post_weight, scale
+        shape = (layer.T, layer.H)
+        self.u = torch.empty(shape, dtype=torch.bfloat16, device=layer.device)
+        self.z = torch.empty(shape, dtype=torch.bfloat16, device=layer.device)
+        self.x = self.gate = self._ws = None
+
+    def forward(self, x: torch.Tensor, bias: torch.Tensor, gate: torch.Tensor | None = None,
+                r: torch.Tensor | None = None, next_weight: torch.Tensor | None = None,
+                stream=None):
+        """r [T, H] like x; with next_weight also u = N(r; next_weight), the
+        next block's input, from the same pass: (r, u)."""
+        with torch.cuda.stream(stream):  # None: the current one
+            capi.moe_block_norm(x, self.eps, pre_weight=self.pre_weight, u=self.u, stream=stream)
+            self.layer.forward(self.u, bias, self.z, stream)
+            if r is None:
+                r = torch.empty_like(x)
+            u = None if next_weight is None else torch.empty_like(self.z)
+            capi.moe_block_norm(x, self.eps, pre_weight=next_weight, u=u, z=self.z,
+                                post_weight=self.post_weight, gate=gate, scale=self.scale,
+                                alpha=self.alpha, r=r, stream=stream)
+            self.x, self.gate = x, gate
+            return r if next_weight is None else (r, u)
+
+    def backward(self, dr: torch.Tensor, weights: bool = True, stream=None) -> dict:
+        """Gradients of the last forward for the upstream gradient dr of r, with
+        the routing held fixed: a dict of dx (through the residual and the
+        experts), gates (the layer's gate gradients, [T, K]), pre_weight, and
+        as they were given post_weight, scale and gate; with `weights` also w13
+        and w2."""
+        if self.x is None:
+            raise ValueError("backward needs a forward before it")
+        with torch.cuda.stream(stream):  # None: the current one
+            dev, H = self.layer.device, self.layer.H
+            if self._ws is None:
+                nbytes = capi.moe_block_norm_backward_workspace_size(H)
+                self._ws = torch.empty(nbytes, dtype=torch.uint8, device=dev)
+
+            def column(w):
+                return None if w is None else torch.empty(H, dtype=torch.float32, device=dev)
+
+            out = {"pre_weight": column(self.pre_weight), "post_weight": column(self.post_weight),
+                   "scale": column(self.scale),
+                   "gate": None if self.gate is None else torch.empty_like(self.gate)}
+            dz = torch.empty_like(self.z)
+            # r itself is only read with a norm of r, which this half has not
+            capi.moe_block_norm_backward(dr, self.eps, self._ws, dr=dr, z=self.z,
+                                         post_weight=self.post_weight, gate=self.gate,
+                                         scale=self.scale, alpha=self.alpha, dz=dz,
+                                         dgate=out["gate"], dscale=out["scale"],
+                                         dpost=out["post_weight"], stream=stream)
+            grads = self.layer.backward(dz, self.u if weights else None, stream)
+            dx = torch.empty_like(self.x)
+            capi.moe_block_norm_backward(self.x, self.eps, self._ws, dr=dr, du=grads[0],
+                                         pre_weight=self.pre_weight, dx=dx, dpre=out["pre_weight"],
+                                         stream=stream)
+            out.update(dx=dx, gates=grads[1])
+            if weights:
+                out.update(w13=grads[2], w2=grads[3])
+            return {k: v for k, v in out.items() if v is not None}
+
+
+class GroupedLinear:
+    """y[r] = x[r] W_g^T for the rows of each expert's group: weight [G, N, K],
+    bf16 or fp16. The groups are device arrays (rows and first row of each),
+    packed or with gaps, as MoELayer's workspace views "group_rows" and
+    "row_start" hold them after a forward."""
+
+    def __init__(self, weight: torch.Tensor):
+        if weight.dim() != 3:
+            raise ValueError("weight must be [groups, N, K]")
+        self.weight = weight
+
+    def forward(self, x, group_rows, group_start, y=None, status=None, stream=None):
+        """y [R, N] like x; rows outside the groups stay as they are (zero in a
+        new y)."""
+        with torch.cuda.stream(stream):  # None: the current one
+            if y is None:
+                y = torch.zeros((x.shape[0], self.weight.shape[1]), dtype=x.dtype, device=x.device)
+            capi.moe_grouped_matmul(x, self.weight, group_rows, group_start, y, True, status, stream)
+            return y
+
+    def backward(self, dy, x, group_rows, group_start, dw=None, accumulate=False, dx=None,
+                 status=None, stream=None):
+        """(dx [R, K] like dy, dw [G, N, K] float32); with accumulate the weight
+        gradient is added to the dw given."""
+        if accumulate and dw is None:
+            raise ValueError("accumulate needs the dw to add to")
+        with torch.cuda.stream(stream):  # None: the current one
+            if dx is None:
+                dx = torch.zeros((dy.shape[0], self.weight.shape[2]), dtype=dy.dtype, device=dy.device)
+            if dw is None:
+                dw = torch.empty(self.weight.shape, dtype=torch.float32, device=dy.device)
+            capi.moe_grouped_matmul(dy, self.weight, group_rows, group_start, dx, False, status, stream)
+            capi.moe_grouped_wgrad(dy, x, group_rows, group_start, dw, accumulate, status, stream)
+            return dx, dw
+
+
+class GradClip:
+    """Clips a fixed set of gradient tensors by their global norm:
+
+        clip = GradClip([grads["w13"], grads["w2"], ...])
+        norm = clip(max_norm=1.0)
+
+    In place, or into `out`. With the experts sharded over several GPUs the
+    ranks' sums of squares have to meet first: call capi.moe_grad_sumsq and
+    moe_grad_clip with an all-reduce of the partials between them."""
+
+    def __init__(self, grads, out=None):
+        self.list = capi.make_grad_list(grads, out)
+        if self.list.device is None:
+            raise ValueError("no gradients")
+        dev = self.list.device
+        self.partials = torch.empty(capi.GRAD_PARTIALS, dtype=torch.float64, device=dev)
+        self.norm = torch.empty(1, dtype=torch.float32, device=dev)
+
+    def __call__(self, max_norm: float, stream=None) -> torch.Tensor:
+        """The norm before clipping, float32 [1] on the device (overwritten by
+        the next call)."""
+        capi.moe_grad_sumsq(self.list, self.partials, stream)
+        capi.moe_grad_clip(self.list, self.partials, max_norm, self.norm, stream)
+        return self.norm

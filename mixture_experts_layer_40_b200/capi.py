@@ -8,6 +8,7 @@ missing, importing this module raises.
 """
 from __future__ import annotations
 
+import bisect
 import ctypes
 import os
 
@@ -37,6 +38,12 @@ class moe_shape(ctypes.Structure):
 class moe_weights(ctypes.Structure):
     _fields_ = [("gate_w", ctypes.c_void_p), ("w13", ctypes.c_void_p), ("s13", ctypes.c_void_p),
                 ("w2", ctypes.c_void_p), ("s2", ctypes.c_void_p), ("gate_split", ctypes.c_void_p)]
+
+
+class moe_grad_list(ctypes.Structure):
+    _fields_ = [("n", ctypes.c_int32), ("grads", ctypes.POINTER(ctypes.c_void_p)),
+                ("out", ctypes.POINTER(ctypes.c_void_p)), ("sizes", ctypes.POINTER(ctypes.c_int64)),
+                ("types", ctypes.POINTER(ctypes.c_int32))]
 
 
 _LAYOUT_FIELDS = ["status", "counts", "offsets", "group_rows", "row_start", "row_token",
@@ -77,6 +84,18 @@ SIGNATURES = {
     "moe_expert_down": (ctypes.c_int, [_I32, _I32, _I32, _P, _P, _I64, _P, _P, _P, _P, _P, _P, _P]),
     "moe_expert_down_bf16": (ctypes.c_int, [_I32, _I32, _I32, _P, _P, _I64, _P, _P, _P, _P, _P, _P,
                                             _P]),
+    "moe_grouped_matmul": (ctypes.c_int, [_I32, _I32, _I32, _P, _P, _I64, _I32, _I32, _P, _P, _I32,
+                                          _P, _P, _P]),
+    "moe_grouped_wgrad": (ctypes.c_int, [_I32, _I32, _I32, _P, _P, _I64, _I32, _I32, _P, _P, _P,
+                                         _I32, _P, _P]),
+    "moe_block_norm": (ctypes.c_int, [_I64, _I32, _I32, _I32, _I32, _I32, _F32, _F32, _P, _P, _P,
+                                      _P, _P, _P, _P, _P, _P]),
+    "moe_block_norm_backward_workspace_size": (_SZ, [_I32]),
+    "moe_block_norm_backward": (ctypes.c_int, [_I64, _I32, _I32, _I32, _I32, _I32, _F32, _F32, _P,
+                                               _P, _P, _P, _P, _P, _P, _P, _P, _P, _P, _P, _P, _P,
+                                               _P, _SZ, _P]),
+    "moe_grad_sumsq": (ctypes.c_int, [ctypes.POINTER(moe_grad_list), _P, _P]),
+    "moe_grad_clip": (ctypes.c_int, [ctypes.POINTER(moe_grad_list), _P, _F32, _P, _P]),
     "moe_ep_row_bytes": (_I64, [moe_shape]),
     "moe_ep_dispatch_workspace_size": (_SZ, [moe_shape, _I32]),
     "moe_ep_dispatch": (ctypes.c_int, [moe_shape, _I32, _P, _P, _P, _P, _P, _P, _P, _P, _I64, _P,
@@ -294,6 +313,266 @@ def moe_expert_down_bf16(H, I, n_groups, group_rows, group_start, rows, h_q, h_s
         H, I, n_groups, _ptr(group_rows, torch.int32), _ptr(group_start, torch.int32), rows,
         _ptr(h_q, torch.uint8), _ptr(h_s, torch.float32), _ptr(w2, torch.uint8),
         _ptr(s2, torch.float32), _ptr(y_rows, torch.bfloat16), _ptr(status), _stream(stream)))
+
+
+# ------------------------------------------------- operators beside the layer
+#
+# These check sizes as well, since they are given no shape struct, and run on
+# the device that holds their tensors: its current stream, or `stream` of it.
+TYPES = {torch.bfloat16: 0, torch.float16: 1, torch.float32: 2}
+
+
+def _type(t: torch.Tensor, name: str) -> int:
+    if t.dtype not in TYPES:
+        raise ValueError(f"{name} must be bfloat16, float16 or float32, got {t.dtype}")
+    return TYPES[t.dtype]
+
+
+def _need(t: torch.Tensor | None, dtype: torch.dtype, shape: tuple, device: torch.device,
+          name: str):
+    """_ptr of a tensor (or None) that must have this type, shape and device."""
+    if t is None:
+        return None
+    p = _ptr(t, dtype, name)
+    if t.shape != shape:
+        raise ValueError(f"{name} must be {list(shape)}, got {list(t.shape)}")
+    if t.device != device:
+        raise ValueError(f"{name} must be on {device}, got {t.device}")
+    return p
+
+
+def _run(name: str, device: torch.device, stream, *args) -> None:
+    if stream is not None and stream.device != device:
+        raise ValueError(f"{name}: the stream is on {stream.device}, the tensors on {device}")
+    fn = getattr(LIB, name)
+    if device.index == torch.cuda.current_device():
+        code = fn(*args, _stream(stream))
+    else:
+        with torch.cuda.device(device):
+            code = fn(*args, _stream(stream))
+    _check(name, code)
+
+
+def _sums_type(t: torch.Tensor, of: torch.Tensor, name: str) -> int:
+    if t.dtype not in (of.dtype, torch.float32):
+        raise ValueError(f"{name} must be {of.dtype} or float32, got {t.dtype}")
+    return _type(t, name)
+
+
+def _groups(group_rows, group_start, n_groups: int, device, status):
+    if status is not None:
+        if status.device != device:
+            raise ValueError(f"status must be on {device}, got {status.device}")
+        if status.numel() * status.element_size() < 4:
+            raise ValueError("status must hold the 4 bytes of a status word")
+    return (_need(group_rows, torch.int32, (n_groups,), device, "group_rows"),
+            _need(group_start, torch.int32, (n_groups,), device, "group_start"),
+            _ptr(status, None, "status"))
+
+
+def moe_grouped_matmul(a, b, group_rows, group_start, out, trans_b: bool = True, status=None,
+                       stream=None):
+    """out[r] = a[r] @ b[g]^T (trans_b; b [G, N, K]) or a[r] @ b[g] (b [G, K, N])
+    for the rows r of each group g: group_rows[g] rows from group_start[g], any
+    alignment. a [R, K] and b bf16 or fp16 alike; out [R, N] of their type or
+    float32. Rows of out outside every group are left as they are."""
+    if a.dim() != 2 or b.dim() != 3:
+        raise ValueError("a must be [rows, K] and b three-dimensional")
+    rows, K = a.shape
+    G, N = b.shape[0], b.shape[1 if trans_b else 2]
+    dev = a.device
+    t = _type(a, "a")
+    ap = _need(a, a.dtype, (rows, K), dev, "a")
+    bp = _need(b, a.dtype, (G, N, K) if trans_b else (G, K, N), dev, "b")
+    op = _need(out, out.dtype, (rows, N), dev, "out")
+    gr, gs, st = _groups(group_rows, group_start, G, dev, status)
+    _run("moe_grouped_matmul", dev, stream, t, _sums_type(out, a, "out"), G, gr, gs, rows, K, N, ap, bp,
+         1 if trans_b else 0, op, st)
+
+
+def moe_grouped_wgrad(dy, x, group_rows, group_start, dw, accumulate: bool = False, status=None,
+                      stream=None):
+    """dw[g] = dy_g^T @ x_g over the rows of each group g (added to dw with
+    accumulate). dy [R, N] and x [R, K] bf16 or fp16 alike; dw [G, N, K] of
+    their type or float32."""
+    if dy.dim() != 2 or x.dim() != 2 or dw.dim() != 3:
+        raise ValueError("dy and x must be [rows, N] and [rows, K], dw three-dimensional")
+    rows, N = dy.shape
+    K, G = x.shape[1], dw.shape[0]
+    dev = dy.device
+    t = _type(dy, "dy")
+    yp = _need(dy, dy.dtype, (rows, N), dev, "dy")
+    xp = _need(x, dy.dtype, (rows, K), dev, "x")
+    wp = _need(dw, dw.dtype, (G, N, K), dev, "dw")
+    gr, gs, st = _groups(group_rows, group_start, G, dev, status)
+    _run("moe_grouped_wgrad", dev, stream, t, _sums_type(dw, dy, "dw"), G, gr, gs, rows, N, K, yp, xp, wp,
+         1 if accumulate else 0, st)
+
+
+def _norm_common(x, act, z, gate, weights):
+    """(T, H, device, res type, act type, weight type, gate kind, pointers of
+    z, gate, pre, post, scale) of a block norm's common arguments; `act`: a
+    tensor of the block's type."""
+    if x.dim() != 2:
+        raise ValueError("the rows must be two-dimensional")
+    T, H = x.shape
+    dev = x.device
+    zp = _need(z, act.dtype, (T, H), dev, "z")
+    kind, gp = 0, None
+    if gate is not None:
+        if gate.dim() == 1:
+            kind, gp = 1, _need(gate, torch.float32, (T,), dev, "gate")
+        else:
+            kind, gp = 2, _need(gate, act.dtype, (T, H), dev, "gate")
+    given = [(n, w) for n, w in weights if w is not None]
+    wtype = given[0][1].dtype if given else act.dtype
+    wp = [_need(w, wtype, (H,), dev, n) for n, w in weights]
+    wt = _type(given[0][1], given[0][0]) if given else _type(act, "z")
+    return T, H, dev, _type(x, "x"), _type(act, "z"), wt, kind, [zp, gp] + wp
+
+
+def moe_block_norm(x, eps: float, pre_weight=None, u=None, z=None, post_weight=None, gate=None,
+                   scale=None, alpha: float = 1.0, r=None, stream=None):
+    """r = x + alpha * scale * gate * N(z; post_weight) and u = N(r; pre_weight),
+    N(v; w) = v * rsqrt(mean(v^2) + eps) * w by row. Without z only u (of x);
+    without pre_weight only r. x, r [T, H] bf16, fp16 or float32; z, u of the
+    same type or, with x float32, any; gate float32 [T] or [T, H] of z's type;
+    weights and scale [H] of z's type or float32. r may be x and u may be z."""
+    if (z is None) != (r is None) or (pre_weight is None) != (u is None):
+        raise ValueError("r goes with z, and u with pre_weight")
+    act = z if z is not None else u
+    if act is None:
+        raise ValueError("nothing to compute: give z and r, pre_weight and u, or both")
+    T, H, dev, rt, at, wt, kind, (zp, gp, pre, post, sc) = _norm_common(
+        x, act, z, gate, [("pre_weight", pre_weight), ("post_weight", post_weight),
+                          ("scale", scale)])
+    xp = _need(x, x.dtype, (T, H), dev, "x")
+    _run("moe_block_norm", dev, stream, T, H, rt, at, wt, kind, float(alpha), float(eps), xp, zp,
+         gp, pre, post, sc, _need(r, x.dtype, (T, H), dev, "r"),
+         _need(u, act.dtype, (T, H), dev, "u"))
+
+
+def moe_block_norm_backward_workspace_size(H: int) -> int:
+    return int(LIB.moe_block_norm_backward_workspace_size(H))
+
+
+def moe_block_norm_backward(r, eps: float, ws, dr=None, du=None, pre_weight=None, z=None,
+                            post_weight=None, gate=None, scale=None, alpha: float = 1.0, dx=None,
+                            dz=None, dgate=None, dscale=None, dpost=None, dpre=None, stream=None):
+    """Gradients of moe_block_norm for the upstream dr (of r; None: zero) and du
+    (of u). r: the forward's r, or its x where it had no z. dx like r (with
+    pre_weight; without it the gradient of x is dr itself), dz like z, dgate
+    like gate, dpre, dpost and dscale float32 [H]. ws: uint8, at least
+    moe_block_norm_backward_workspace_size(H) bytes."""
+    for a, b, what in ((z, dz, "dz goes with z"), (gate, dgate, "dgate with gate"),
+                       (scale, dscale, "dscale with scale"), (pre_weight, dpre, "dpre with pre_weight"),
+                       (post_weight, dpost, "dpost with post_weight"), (pre_weight, dx, "dx with pre_weight"),
+                       (pre_weight, du, "du with pre_weight")):
+        if (a is None) != (b is None):
+            raise ValueError(what)
+    act = z if z is not None else du
+    if act is None:
+        raise ValueError("nothing to compute: give z, du or both")
+    T, H, dev, rt, at, wt, kind, (zp, gp, pre, post, sc) = _norm_common(
+        r, act, z, gate, [("pre_weight", pre_weight), ("post_weight", post_weight),
+                          ("scale", scale)])
+    f32 = torch.float32
+    gate_t, gate_s = (None, None) if gate is None else (gate.dtype, tuple(gate.shape))
+    rp = _need(r, r.dtype, (T, H), dev, "r")
+    wsp = _ptr(ws, torch.uint8, "ws")
+    if ws.device != dev:
+        raise ValueError(f"ws must be on {dev}, got {ws.device}")
+    _run("moe_block_norm_backward", dev, stream, T, H, rt, at, wt, kind, float(alpha), float(eps),
+         rp, zp, gp, pre, post, sc, _need(dr, r.dtype, (T, H), dev, "dr"),
+         _need(du, act.dtype, (T, H), dev, "du"), _need(dx, r.dtype, (T, H), dev, "dx"),
+         _need(dz, act.dtype, (T, H), dev, "dz"), _need(dgate, gate_t, gate_s, dev, "dgate"),
+         _need(dpre, f32, (H,), dev, "dpre"), _need(dpost, f32, (H,), dev, "dpost"),
+         _need(dscale, f32, (H,), dev, "dscale"), wsp, ws.numel())
+
+
+GRAD_PARTIALS = 1024
+
+
+class GradList:
+    """A moe_grad_list over a program's gradient tensors, made once by
+    make_grad_list and used in every step that writes new gradients into
+    them; it keeps the tensors."""
+
+    def __init__(self, grads, out):
+        self.grads, self.out = list(grads), None if out is None else list(out)
+        n = len(self.grads)
+        if self.out is not None and len(self.out) != n:
+            raise ValueError(f"{n} gradients and {len(self.out)} outputs")
+        self.device = self.grads[0].device if n else None
+        gp = [_need(g, g.dtype, g.shape, self.device, f"grads[{i}]")
+              for i, g in enumerate(self.grads)]
+        op = None
+        if self.out is not None:
+            op = [_need(o, g.dtype, g.shape, self.device, f"out[{i}]")
+                  for i, (o, g) in enumerate(zip(self.out, self.grads))]
+        sizes = [g.numel() for g in self.grads]
+        self._refuse_overlap(gp, op, [g.numel() * g.element_size() for g in self.grads])
+        ptrs = ctypes.c_void_p * n
+        self._arrays = (ptrs(*gp), None if op is None else ptrs(*op),
+                        (ctypes.c_int64 * n)(*sizes),
+                        (ctypes.c_int32 * n)(*[_type(g, f"grads[{i}]")
+                                               for i, g in enumerate(self.grads)]))
+        g, o, s, t = self._arrays
+        cast = ctypes.cast
+        vpp = ctypes.POINTER(ctypes.c_void_p)
+        self.struct = moe_grad_list(n, cast(g, vpp), None if o is None else cast(o, vpp),
+                                    cast(s, ctypes.POINTER(ctypes.c_int64)),
+                                    cast(t, ctypes.POINTER(ctypes.c_int32)))
+
+    @staticmethod
+    def _refuse_overlap(grads, out, nbytes):
+        """Raises ValueError where an output lies on another output or, unless
+        it is the tensor itself, on gradients (addresses and sizes)."""
+        written = grads if out is None else out
+        spans = sorted((p, p + b, i) for i, (p, b) in enumerate(zip(written, nbytes)) if b)
+        for (_, end, i), (begin, _, j) in zip(spans, spans[1:]):
+            if begin < end:
+                raise ValueError(f"tensors {i} and {j} overlap where they are written")
+        if out is None:
+            return
+        ends = [end for _, end, _ in spans]
+        for j, (p, b) in enumerate(zip(grads, nbytes)):
+            for begin, end, i in spans[bisect.bisect_right(ends, p):]:
+                if not b or begin >= p + b:
+                    break
+                if i != j or begin != p:
+                    raise ValueError(f"the output of tensor {i} overlaps gradient {j}")
+
+
+def make_grad_list(grads, out=None) -> GradList:
+    """grads: contiguous bf16, fp16 or float32 tensors on one device (types may
+    differ); out: tensors of the same shapes and types for the clipped
+    gradients, or None to scale in place. Outputs must not overlap one another
+    or another tensor's gradients (ValueError)."""
+    return GradList(grads, out)
+
+
+def _partials(gl: GradList, partials):
+    p = _need(partials, torch.float64, (GRAD_PARTIALS,), partials.device, "partials")
+    if gl.device is not None and partials.device != gl.device:
+        raise ValueError(f"partials must be on {gl.device}, got {partials.device}")
+    return p
+
+
+def moe_grad_sumsq(gl: GradList, partials, stream=None):
+    """Partial sums of squares of all gradients of the list: partials float64
+    [GRAD_PARTIALS]; their sum is the squared global norm. With sharded
+    experts, add the ranks' partials (an all-reduce) before moe_grad_clip."""
+    _run("moe_grad_sumsq", partials.device, stream, ctypes.byref(gl.struct),
+         _partials(gl, partials))
+
+
+def moe_grad_clip(gl: GradList, partials, max_norm: float, norm, stream=None):
+    """norm (float32 [1]) = sqrt(sum of partials); every gradient times
+    min(1, max_norm / (norm + 1e-6)) into the list's outputs (or in place)."""
+    _run("moe_grad_clip", partials.device, stream, ctypes.byref(gl.struct),
+         _partials(gl, partials), float(max_norm),
+         _need(norm, torch.float32, (1,), partials.device, "norm"))
 
 
 def moe_ep_row_bytes(sh: moe_shape) -> int:

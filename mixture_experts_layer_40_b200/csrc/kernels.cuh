@@ -31,6 +31,11 @@ cudaError_t make_tmap_f32(CUtensorMap* map, const void* base, int64_t inner, int
 cudaError_t make_tmap_bf16(CUtensorMap* map, const void* base, int64_t inner, int64_t rows,
                            int64_t depth, int box_inner, int box_rows, int box_depth = 1);
 
+// 16-bit tensor map over [depth, rows, inner], always three-dimensional, with
+// 128-byte swizzle and a box of box_inner x box_rows x 1 (host side).
+cudaError_t make_tmap_16b_3d(CUtensorMap* map, const void* base, int64_t inner, int64_t rows,
+                             int64_t depth, int box_inner, int box_rows);
+
 // The sizes every entry point accepts (see moe_shape in moe_capi.h).
 bool shape_ok(const moe_shape& s);
 
@@ -149,5 +154,20 @@ cudaError_t launch_combine(const float* y_rows, const int32_t* ids, const float*
 
 cudaError_t launch_update_bias(float* bias, const int32_t* counts, int N, int T, int K,
                                float gamma, cudaStream_t stream);
+
+// Products grouped by expert in 16 bits over ragged groups (grouped16.cu).
+struct Groups16 {
+  int32_t n_groups;
+  const int32_t* group_rows;   // device [n_groups]
+  const int32_t* group_start;  // device [n_groups]
+  int64_t rows;                // rows of the row buffers
+  uint32_t* status;
+};
+cudaError_t launch_grouped_matmul(const Groups16& gr, bool f16, int out_type, int K, int N,
+                                  const void* a, const void* b, bool trans_b, void* out,
+                                  cudaStream_t stream, int sm_count);
+cudaError_t launch_grouped_wgrad(const Groups16& gr, bool f16, int out_type, int N, int K,
+                                 const void* dy, const void* x, void* dw, bool accumulate,
+                                 cudaStream_t stream, int sm_count);
 
 }  // namespace moe

@@ -1,0 +1,320 @@
+"""Products grouped by expert in 16 bits, and their gradients, against float64.
+
+Tolerance of one output element, before any run: the 16-bit products are exact
+in fp32; each tensor-core step adds 16 of them to the fp32 total and is off by
+at most 2^-22 of the largest partial sum, which S = sum |a||b| bounds, so K/16
+steps are off by (K/16 + 2) 2^-22 S; the rounding to the output's type adds
+half a step, finfo.eps / 2 of the value (or half the smallest subnormal)."""
+import numpy as np
+import pytest
+import torch
+
+pytestmark = pytest.mark.gpu
+
+BF16, FP16, FP32 = torch.bfloat16, torch.float16, torch.float32
+
+
+@pytest.fixture(scope="module", autouse=True)
+def capi():
+    from __graft_entry__ import build
+    build()
+    assert torch.cuda.is_available()
+    from mixture_experts_layer_40_b200 import capi as c
+    return c
+
+
+def layout(counts, align=1, lead=0, tail=0):
+    """Device group arrays for these counts, starts rounded up to `align`."""
+    starts, at = [], lead
+    for c in counts:
+        at = -(-at // align) * align
+        starts.append(at)
+        at += c
+    dev = [torch.tensor(v, dtype=torch.int32, device="cuda") for v in (counts, starts)]
+    return dev[0], dev[1], starts, at + tail
+
+
+def close(got, ref, mag, terms, what):
+    """Every element within the tolerance of the module's docstring."""
+    info = torch.finfo(got.dtype)
+    acc = (terms / 16 + 2) * 2.0 ** -22 * mag
+    tol = acc + (info.eps / 2) * (ref.abs() + acc) + info.smallest_normal * info.eps / 2
+    err = (got.double() - ref).abs()
+    bad = ~(err <= tol)
+    assert not bad.any(), (what, int(bad.sum()), float((err / tol).max()))
+
+
+def randn(gen, *shape, dtype=BF16, std=1.0):
+    return (torch.randn(*shape, generator=gen, device="cuda") * std).to(dtype)
+
+
+def check_matmul(capi, counts, K, N, dtype=BF16, out_dtype=None, trans=True, align=1, lead=0,
+                 tail=0, seed=0, poison=True):
+    gen = torch.Generator(device="cuda").manual_seed(seed)
+    gr, gs, starts, rows = layout(counts, align, lead, tail)
+    G = len(counts)
+    a = randn(gen, max(rows, 1), K, dtype=dtype)[:rows]
+    b = randn(gen, G, N, K, dtype=dtype, std=K ** -0.5)
+    b_arg = b if trans else b.transpose(1, 2).contiguous()
+    inside = torch.zeros(rows, dtype=torch.bool, device="cuda")
+    for s, c in zip(starts, counts):
+        inside[s:s + c] = True
+    if poison:  # rows of no group hold anything at all
+        a[~inside] = float("nan")
+    out = torch.full((rows, N), 7.0, dtype=out_dtype or dtype, device="cuda")
+    status = torch.zeros(4, dtype=torch.int32, device="cuda")
+    capi.moe_grouped_matmul(a, b_arg, gr, gs, out, trans_b=trans, status=status)
+    assert capi.moe_get_status(status) == 0
+    assert (out[~inside] == 7.0).all()
+    for g, (s, c) in enumerate(zip(starts, counts)):
+        if c:
+            x, w = a[s:s + c].double(), b[g].double()
+            close(out[s:s + c], x @ w.T, x.abs() @ w.abs().T, K, (g, counts))
+    return a, b_arg, gr, gs, out
+
+
+def check_wgrad(capi, counts, N, K, dtype=BF16, out_dtype=FP32, align=1, lead=0, tail=0, seed=0,
+                accumulate=False):
+    gen = torch.Generator(device="cuda").manual_seed(seed)
+    gr, gs, starts, rows = layout(counts, align, lead, tail)
+    dy = randn(gen, max(rows, 1), N, dtype=dtype)[:rows]
+    x = randn(gen, max(rows, 1), K, dtype=dtype)[:rows]
+    inside = torch.zeros(rows, dtype=torch.bool, device="cuda")
+    for s, c in zip(starts, counts):
+        inside[s:s + c] = True
+    dy[~inside] = float("nan")
+    x[~inside] = float("inf")
+    base = randn(gen, len(counts), N, K, dtype=out_dtype)
+    dw = base.clone() if accumulate else torch.full_like(base, 7.0)
+    status = torch.zeros(4, dtype=torch.int32, device="cuda")
+    capi.moe_grouped_wgrad(dy, x, gr, gs, dw, accumulate=accumulate, status=status)
+    assert capi.moe_get_status(status) == 0
+    for g, (s, c) in enumerate(zip(starts, counts)):
+        p, q = dy[s:s + c].double(), x[s:s + c].double()
+        ref, mag = p.T @ q, p.abs().T @ q.abs()
+        if accumulate:
+            ref = ref + base[g].double()
+            mag = mag + base[g].double().abs()
+        if c == 0:
+            assert torch.equal(dw[g], base[g] if accumulate else torch.zeros_like(base[g]))
+        else:
+            close(dw[g], ref, mag, c, (g, counts))
+    return dy, x, gr, gs, dw
+
+
+COUNTS = [[1], [0, 3, 0], [128, 128], [127, 129, 1, 0, 64], [33, 0, 0, 300, 5, 96, 97], [0, 0]]
+
+
+@pytest.mark.parametrize("counts", COUNTS)
+@pytest.mark.parametrize("trans", [True, False])
+@pytest.mark.parametrize("dtype,out", [(BF16, None), (FP16, None), (BF16, FP32), (FP16, FP32)])
+def test_matmul_ragged(capi, counts, trans, dtype, out):
+    check_matmul(capi, counts, 200, 136, dtype, out, trans)
+
+
+@pytest.mark.parametrize("K,N", [(8, 8), (64, 64), (72, 264), (128, 256), (1000, 40), (16, 520)])
+@pytest.mark.parametrize("trans", [True, False])
+def test_matmul_sizes(capi, K, N, trans):
+    check_matmul(capi, [5, 0, 140, 31], K, N, trans=trans, seed=K + N)
+
+
+@pytest.mark.parametrize("trans", [True, False])
+def test_matmul_gaps_and_ends(capi, trans):
+    check_matmul(capi, [100, 0, 7, 260], 136, 72, trans=trans, align=128, tail=60)
+    check_matmul(capi, [100, 1, 7, 26], 136, 72, trans=trans, align=5, lead=3, tail=1)
+
+
+@pytest.mark.parametrize("trans", [True, False])
+def test_matmul_wide_tiles(capi, trans):
+    # enough tiles for the 128- and the 256-wide variants
+    check_matmul(capi, [300] * 40, 264, 1304, trans=trans)
+    check_matmul(capi, [1] * 130, 136, 648, trans=trans)
+    check_matmul(capi, [257, 1000, 3, 4000, 129, 640] * 3, 456, 1800, trans=trans)
+
+
+def test_matmul_many_groups(capi):
+    counts = [(g * 7) % 5 for g in range(1025)]
+    check_matmul(capi, counts, 64, 24)
+
+
+@pytest.mark.parametrize("counts", COUNTS + [[16], [17, 15, 47, 49], [63, 65, 191]])
+@pytest.mark.parametrize("dtype,out", [(BF16, FP32), (FP16, FP32), (BF16, BF16), (FP16, FP16)])
+def test_wgrad_ragged(capi, counts, dtype, out):
+    check_wgrad(capi, counts, 136, 200, dtype, out)
+
+
+@pytest.mark.parametrize("N,K", [(8, 8), (64, 64), (264, 72), (128, 256), (40, 1000), (520, 16)])
+def test_wgrad_sizes(capi, N, K):
+    check_wgrad(capi, [5, 0, 140, 31], N, K, seed=K + N)
+
+
+@pytest.mark.parametrize("out", [FP32, BF16])
+def test_wgrad_accumulates(capi, out):
+    check_wgrad(capi, [5, 0, 140, 31], 136, 264, out_dtype=out, accumulate=True)
+
+
+def test_wgrad_gaps_and_wide_tiles(capi):
+    check_wgrad(capi, [100, 0, 7, 260], 136, 72, align=128, tail=60)
+    check_wgrad(capi, [100, 1, 7, 26], 136, 72, align=5, lead=3, tail=1)
+    check_wgrad(capi, [300, 0, 257, 1, 64] * 4, 520, 1304)
+
+
+def test_no_rows(capi):
+    gr, gs = torch.zeros(2, 3, dtype=torch.int32, device="cuda")
+    w = torch.ones(3, 16, 24, dtype=BF16, device="cuda")
+    out = torch.empty(0, 16, dtype=BF16, device="cuda")
+    capi.moe_grouped_matmul(torch.empty(0, 24, dtype=BF16, device="cuda"), w, gr, gs, out)
+    dw = torch.ones(3, 16, 24, device="cuda")
+    e = torch.empty(0, 16, dtype=BF16, device="cuda"), torch.empty(0, 24, dtype=BF16, device="cuda")
+    capi.moe_grouped_wgrad(*e, gr, gs, dw, accumulate=True)
+    assert (dw == 1).all()
+    capi.moe_grouped_wgrad(*e, gr, gs, dw)
+    assert (dw == 0).all()
+
+
+def test_special_values_stay_in_their_rows(capi):
+    gen = torch.Generator(device="cuda").manual_seed(1)
+    a, b = randn(gen, 70, 64), randn(gen, 2, 48, 64)
+    gr, gs, starts, _ = layout([40, 30])
+    a[3, 5], a[45, 7] = float("inf"), float("nan")
+    out = torch.zeros(70, 48, dtype=BF16, device="cuda")
+    capi.moe_grouped_matmul(a, b, gr, gs, out)
+    fine = torch.isfinite(out).all(1)
+    assert not fine[3] and not fine[45] and int(fine.sum()) == 68
+    dw = torch.zeros(2, 48, 64, device="cuda")
+    dy = randn(gen, 70, 48)
+    capi.moe_grouped_wgrad(dy, a, gr, gs, dw)
+    cols = torch.isfinite(dw).all(1)  # [G, K]
+    assert not cols[0, 5] and not cols[1, 7] and int(cols.sum()) == 126
+
+
+def test_bad_groups_are_flagged_and_skipped(capi):
+    """Group tables that fail the kernel's checks set the bounds status, and
+    only the groups that pass are computed."""
+    gen = torch.Generator(device="cuda").manual_seed(2)
+    a, b = randn(gen, 50, 64), randn(gen, 4, 32, 64)
+    for rows, start, good in [([10, -1, 10, 10], [0, 10, 20, 30], [0, 2, 3]),
+                              ([10, 10, 10, 10], [0, 5, 20, 30], [0, 2, 3]),
+                              ([10, 10, 10, 21], [0, 10, 20, 30], [0, 1, 2]),
+                              ([10, 10, 10, 10], [-3, 10, 20, 30], [1, 2, 3]),
+                              ([10, 10, 2 ** 31 - 1, 10], [0, 10, 2 ** 31 - 1, 30], [0, 1, 3]),
+                              ([10, 10, 10, 10], [30, 20, 10, 0], [0])]:
+        gr = torch.tensor(rows, dtype=torch.int32, device="cuda")
+        gs = torch.tensor(start, dtype=torch.int32, device="cuda")
+        out = torch.full((50, 32), 7.0, dtype=FP32, device="cuda")
+        status = torch.zeros(4, dtype=torch.int32, device="cuda")
+        capi.moe_grouped_matmul(a, b, gr, gs, out, status=status)
+        assert capi.moe_get_status(status) == -5  # MOE_ERR_BOUNDS
+        done = torch.zeros(50, dtype=torch.bool, device="cuda")
+        for g in good:
+            s, c = start[g], rows[g]
+            done[s:s + c] = True
+            x, w = a[s:s + c].double(), b[g].double()
+            close(out[s:s + c], x @ w.T, x.abs() @ w.abs().T, 64, (g, rows))
+        assert (out[~done] == 7.0).all()
+        dw = torch.full((4, 32, 64), 7.0, device="cuda")
+        dy = randn(gen, 50, 32)
+        capi.moe_grouped_wgrad(dy, a, gr, gs, dw, status=status)
+        assert capi.moe_get_status(status) == -5
+        for g in range(4):
+            assert good.count(g) or (dw[g] == 0).all()
+
+
+def test_gradients_against_differences(capi):
+    """L = sum dout * out is linear in a and in b: central differences of L, in
+    float64 over fp32 outputs, give the gradients up to the outputs' error."""
+    gen = torch.Generator(device="cuda").manual_seed(4)
+    counts, K, N = [9, 0, 70, 130], 72, 104
+    gr, gs, _, rows = layout(counts)
+    a, b, dout = randn(gen, rows, K), randn(gen, 4, N, K), randn(gen, rows, N)
+
+    def forward(a, b):
+        out = torch.zeros(rows, N, device="cuda")
+        capi.moe_grouped_matmul(a, b, gr, gs, out)
+        return out.double()
+
+    da, dw = torch.zeros(rows, K, device="cuda"), torch.zeros(4, N, K, device="cuda")
+    capi.moe_grouped_matmul(dout, b, gr, gs, da, trans_b=False)
+    capi.moe_grouped_wgrad(dout, a, gr, gs, dw)
+    for t, grad in ((a, da), (b, dw)):
+        step = torch.sign(randn(gen, *t.shape))
+        # t +- step must be exact in bf16: round the base to multiples of 1/8
+        base = (t.float().clamp(-3, 3) * 8).round() / 8
+        plus, minus = (base + step.float()).to(BF16), (base - step.float()).to(BF16)
+        args = lambda v: (v, b) if t is a else (a, v)  # noqa: E731
+        diff = ((forward(*args(plus)) - forward(*args(minus))) * dout.double()).sum() / 2
+        want = (grad.double() * step.double()).sum()
+        # both sides are sums of rows * N (grad: rows * K) fp32 values, each off
+        # by at most (K/16 + 10) 2^-22 of its sum of magnitudes (under 8 * K)
+        slack = (K / 16 + 10) * 2.0 ** -22 * 8 * K * float(dout.abs().double().sum()) * 2
+        assert abs(float(diff - want)) <= slack, (float(diff), float(want), slack)
+
+
+def test_reproducible_streams_and_graphs(capi):
+    a, b, gr, gs, out = check_matmul(capi, [100, 0, 37, 260], 264, 520)
+    again = torch.full_like(out, 7.0)
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    capi.moe_grouped_matmul(a, b, gr, gs, again, stream=side)
+    side.synchronize()
+    assert torch.equal(out, again)
+    dy, x, gr, gs, dw = check_wgrad(capi, [100, 0, 37, 260], 136, 264)
+    captured, dw2 = torch.full_like(out, 7.0), torch.empty_like(dw)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        capi.moe_grouped_matmul(a, b, gr, gs, captured)
+        capi.moe_grouped_wgrad(dy, x, gr, gs, dw2)
+    for counts in ([100, 0, 37, 260], [50, 40, 7, 13]):
+        gr.copy_(torch.tensor(counts, dtype=torch.int32))
+        captured.fill_(7.0)
+        graph.replay()
+        capi.moe_grouped_matmul(a, b, gr, gs, again.fill_(7.0))
+        capi.moe_grouped_wgrad(dy, x, gr, gs, dw)
+        torch.cuda.synchronize()
+        assert torch.equal(captured, again) and torch.equal(dw, dw2)
+
+
+def test_row_offsets_past_32_bits(capi):
+    """Output and row offsets beyond 2^31 elements and 2^32 bytes."""
+    K, N, rows = 8, 2056, 1_100_000
+    gen = torch.Generator(device="cuda").manual_seed(5)
+    counts = [40, 0, 33]
+    gr = torch.tensor(counts, dtype=torch.int32, device="cuda")
+    gs = torch.tensor([5, 7, rows - 33], dtype=torch.int32, device="cuda")
+    a, b = torch.zeros(rows, K, dtype=BF16, device="cuda"), randn(gen, 3, N, K)
+    out = torch.zeros(rows, N, dtype=BF16, device="cuda")
+    for s, c in ((5, 40), (rows - 33, 33)):
+        a[s:s + c] = randn(gen, c, K)
+    capi.moe_grouped_matmul(a, b, gr, gs, out)
+    for g, (s, c) in ((0, (5, 40)), (2, (rows - 33, 33))):
+        x, w = a[s:s + c].double(), b[g].double()
+        close(out[s:s + c], x @ w.T, x.abs() @ w.abs().T, K, g)
+    assert not out[45:rows - 33].any()
+    del a
+    x = torch.zeros(rows, N, dtype=BF16, device="cuda")
+    dy = torch.zeros(rows, K, dtype=BF16, device="cuda")
+    for s, c in ((5, 40), (rows - 33, 33)):
+        x[s:s + c], dy[s:s + c] = randn(gen, c, N), randn(gen, c, K)
+    dw = torch.empty(3, K, N, device="cuda")
+    capi.moe_grouped_wgrad(dy, x, gr, gs, dw)
+    for g, (s, c) in ((0, (5, 40)), (2, (rows - 33, 33))):
+        p, q = dy[s:s + c].double(), x[s:s + c].double()
+        close(dw[g], p.T @ q, p.abs().T @ q.abs(), c, g)
+
+
+def test_binding_refuses(capi):
+    z = lambda *s, t=BF16: torch.zeros(*s, dtype=t, device="cuda")  # noqa: E731
+    i = z(2, t=torch.int32)
+    a, b, out = z(10, 64), z(2, 32, 64), z(10, 32)
+    for args in [(a, b.half(), i, i, out), (a, b, i, i, out.half()), (a, b, i, i, z(10, 64)),
+                 (a, b, i, i, z(9, 32)), (a, z(2, 32, 72), i, i, out), (a, b, z(3, t=torch.int32), i, out),
+                 (a, b, i.long(), i, out), (a.T, b, i, i, out), (a, b, i, i.cpu(), out),
+                 (a, b.transpose(1, 2), i, i, out)]:
+        with pytest.raises(ValueError):
+            capi.moe_grouped_matmul(*args)
+    with pytest.raises(ValueError):
+        capi.moe_grouped_matmul(a, b, i, i, out, status=torch.zeros(0, device="cuda"))
+    with pytest.raises(capi.MoeError):
+        capi.moe_grouped_matmul(z(10, 60), z(2, 32, 60), i, i, out)
+    with pytest.raises(capi.MoeError):  # rows that start off a 16-byte boundary
+        capi.moe_grouped_matmul(z(641)[1:].view(10, 64), b, i, i, out)
