@@ -133,7 +133,7 @@ class GradClip:
         self.list = capi.make_grad_list(grads, out)
         if self.list.device is None:
             raise ValueError("no gradients")
-        dev = self.list.device
+        dev = torch.device("cuda", self.list.device)
         self.partials = torch.empty(capi.GRAD_PARTIALS, dtype=torch.float64, device=dev)
         self.norm = torch.empty(1, dtype=torch.float32, device=dev)
 

@@ -328,29 +328,40 @@ def _type(t: torch.Tensor, name: str) -> int:
     return TYPES[t.dtype]
 
 
-def _need(t: torch.Tensor | None, dtype: torch.dtype, shape: tuple, device: torch.device,
-          name: str):
-    """_ptr of a tensor (or None) that must have this type, shape and device."""
+def _need(t: torch.Tensor | None, dtype: torch.dtype, shape: tuple, device: int, name: str):
+    """The address of a tensor (or None) that must be contiguous, of this type
+    and shape, on the CUDA device of this index."""
     if t is None:
         return None
-    p = _ptr(t, dtype, name)
+    if t.dtype is dtype and t.shape == shape and t.get_device() == device and t.is_contiguous():
+        return t.data_ptr()
+    _ptr(t, dtype, name)
     if t.shape != shape:
         raise ValueError(f"{name} must be {list(shape)}, got {list(t.shape)}")
-    if t.device != device:
-        raise ValueError(f"{name} must be on {device}, got {t.device}")
-    return p
+    raise ValueError(f"{name} must be on cuda:{device}, got {t.device}")
 
 
-def _run(name: str, device: torch.device, stream, *args) -> None:
-    if stream is not None and stream.device != device:
-        raise ValueError(f"{name}: the stream is on {stream.device}, the tensors on {device}")
+def _device(t: torch.Tensor, name: str) -> int:
+    if not t.is_cuda:
+        raise ValueError(f"{name} must be a CUDA tensor")
+    return t.get_device()
+
+
+def _run(name: str, device: int, stream, *args) -> None:
+    if stream is None:
+        handle = torch._C._cuda_getCurrentRawStream(device)
+    elif stream.device.index != device:
+        raise ValueError(f"{name}: the stream is on {stream.device}, the tensors on cuda:{device}")
+    else:
+        handle = stream.cuda_stream
     fn = getattr(LIB, name)
-    if device.index == torch.cuda.current_device():
-        code = fn(*args, _stream(stream))
+    if device == torch._C._cuda_getDevice():
+        code = fn(*args, handle)
     else:
         with torch.cuda.device(device):
-            code = fn(*args, _stream(stream))
-    _check(name, code)
+            code = fn(*args, handle)
+    if code != MOE_OK:
+        raise MoeError(name, code)
 
 
 def _sums_type(t: torch.Tensor, of: torch.Tensor, name: str) -> int:
@@ -361,8 +372,8 @@ def _sums_type(t: torch.Tensor, of: torch.Tensor, name: str) -> int:
 
 def _groups(group_rows, group_start, n_groups: int, device, status):
     if status is not None:
-        if status.device != device:
-            raise ValueError(f"status must be on {device}, got {status.device}")
+        if status.get_device() != device:
+            raise ValueError(f"status must be on cuda:{device}, got {status.device}")
         if status.numel() * status.element_size() < 4:
             raise ValueError("status must hold the 4 bytes of a status word")
     return (_need(group_rows, torch.int32, (n_groups,), device, "group_rows"),
@@ -380,8 +391,8 @@ def moe_grouped_matmul(a, b, group_rows, group_start, out, trans_b: bool = True,
         raise ValueError("a must be [rows, K] and b three-dimensional")
     rows, K = a.shape
     G, N = b.shape[0], b.shape[1 if trans_b else 2]
-    dev = a.device
     t = _type(a, "a")
+    dev = _device(a, "a")
     ap = _need(a, a.dtype, (rows, K), dev, "a")
     bp = _need(b, a.dtype, (G, N, K) if trans_b else (G, K, N), dev, "b")
     op = _need(out, out.dtype, (rows, N), dev, "out")
@@ -399,8 +410,8 @@ def moe_grouped_wgrad(dy, x, group_rows, group_start, dw, accumulate: bool = Fal
         raise ValueError("dy and x must be [rows, N] and [rows, K], dw three-dimensional")
     rows, N = dy.shape
     K, G = x.shape[1], dw.shape[0]
-    dev = dy.device
     t = _type(dy, "dy")
+    dev = _device(dy, "dy")
     yp = _need(dy, dy.dtype, (rows, N), dev, "dy")
     xp = _need(x, dy.dtype, (rows, K), dev, "x")
     wp = _need(dw, dw.dtype, (G, N, K), dev, "dw")
@@ -416,7 +427,7 @@ def _norm_common(x, act, z, gate, weights):
     if x.dim() != 2:
         raise ValueError("the rows must be two-dimensional")
     T, H = x.shape
-    dev = x.device
+    dev = _device(x, "x")
     zp = _need(z, act.dtype, (T, H), dev, "z")
     kind, gp = 0, None
     if gate is not None:
@@ -480,8 +491,8 @@ def moe_block_norm_backward(r, eps: float, ws, dr=None, du=None, pre_weight=None
     gate_t, gate_s = (None, None) if gate is None else (gate.dtype, tuple(gate.shape))
     rp = _need(r, r.dtype, (T, H), dev, "r")
     wsp = _ptr(ws, torch.uint8, "ws")
-    if ws.device != dev:
-        raise ValueError(f"ws must be on {dev}, got {ws.device}")
+    if ws.get_device() != dev:
+        raise ValueError(f"ws must be on cuda:{dev}, got {ws.device}")
     _run("moe_block_norm_backward", dev, stream, T, H, rt, at, wt, kind, float(alpha), float(eps),
          rp, zp, gp, pre, post, sc, _need(dr, r.dtype, (T, H), dev, "dr"),
          _need(du, act.dtype, (T, H), dev, "du"), _need(dx, r.dtype, (T, H), dev, "dx"),
@@ -503,7 +514,7 @@ class GradList:
         n = len(self.grads)
         if self.out is not None and len(self.out) != n:
             raise ValueError(f"{n} gradients and {len(self.out)} outputs")
-        self.device = self.grads[0].device if n else None
+        self.device = _device(self.grads[0], "grads[0]") if n else None
         gp = [_need(g, g.dtype, g.shape, self.device, f"grads[{i}]")
               for i, g in enumerate(self.grads)]
         op = None
@@ -553,26 +564,24 @@ def make_grad_list(grads, out=None) -> GradList:
 
 
 def _partials(gl: GradList, partials):
-    p = _need(partials, torch.float64, (GRAD_PARTIALS,), partials.device, "partials")
-    if gl.device is not None and partials.device != gl.device:
-        raise ValueError(f"partials must be on {gl.device}, got {partials.device}")
-    return p
+    dev = gl.device if gl.device is not None else _device(partials, "partials")
+    return dev, _need(partials, torch.float64, (GRAD_PARTIALS,), dev, "partials")
 
 
 def moe_grad_sumsq(gl: GradList, partials, stream=None):
     """Partial sums of squares of all gradients of the list: partials float64
     [GRAD_PARTIALS]; their sum is the squared global norm. With sharded
     experts, add the ranks' partials (an all-reduce) before moe_grad_clip."""
-    _run("moe_grad_sumsq", partials.device, stream, ctypes.byref(gl.struct),
-         _partials(gl, partials))
+    dev, p = _partials(gl, partials)
+    _run("moe_grad_sumsq", dev, stream, ctypes.byref(gl.struct), p)
 
 
 def moe_grad_clip(gl: GradList, partials, max_norm: float, norm, stream=None):
     """norm (float32 [1]) = sqrt(sum of partials); every gradient times
     min(1, max_norm / (norm + 1e-6)) into the list's outputs (or in place)."""
-    _run("moe_grad_clip", partials.device, stream, ctypes.byref(gl.struct),
-         _partials(gl, partials), float(max_norm),
-         _need(norm, torch.float32, (1,), partials.device, "norm"))
+    dev, p = _partials(gl, partials)
+    _run("moe_grad_clip", dev, stream, ctypes.byref(gl.struct), p, float(max_norm),
+         _need(norm, torch.float32, (1,), dev, "norm"))
 
 
 def moe_ep_row_bytes(sh: moe_shape) -> int:

@@ -13,7 +13,6 @@
 // stored, and u is computed from the unrounded row.
 //
 // Bound by HBM: a few operations per byte.
-#include <atomic>
 #include <type_traits>
 
 #include "kernels.cuh"
@@ -22,9 +21,11 @@ namespace moe {
 
 namespace {
 
-constexpr int kNormThreads = 512;   // most threads of a CTA
-constexpr int kTeamsMax = 8;        // rows in flight per CTA
+constexpr int kNormThreads = 1024;  // most threads of a CTA
+constexpr int kBackThreads = 512;   // and of the backward's, which holds more in registers
 constexpr int kMaxParts = 1024;     // partial column sums
+constexpr size_t kRing = 208 * 1024;
+constexpr int kMaxStages = 6;       // rows asked for ahead, per team
 
 enum Gate : int { kGateNone = 0, kGateRow = 1, kGateFull = 2 };
 
@@ -42,6 +43,7 @@ struct NormArgs {
   int32_t gate_kind;
   int32_t w_f32;
   int32_t team_warps;
+  int32_t stages;     // vector form: rows in the ring
   float alpha, eps;
   // backward
   const void* dr;     // Res
@@ -52,7 +54,6 @@ struct NormArgs {
   float* part;        // [parts, 2, H]
 };
 
-// up to 8 elements from p as fp32; kVec: all 8, 16-byte aligned
 template <typename T>
 MOE_DEV float to_f(T v) {
   if constexpr (std::is_same_v<T, float>) return v;
@@ -66,157 +67,324 @@ MOE_DEV T from_f(float v) {
   else return __float2bfloat16_rn(v);
 }
 
+// 8 packed elements to and from fp32
+template <typename T>
+MOE_DEV void unpack8(const uint32_t (&w)[sizeof(T) * 2], float (&v)[8]) {
+#pragma unroll
+  for (int i = 0; i < (int)sizeof(T) * 2; ++i) {
+    if constexpr (std::is_same_v<T, float>) {
+      v[i] = __uint_as_float(w[i]);
+    } else if constexpr (std::is_same_v<T, __half>) {
+      const float2 f = __half22float2(__halves2half2(__ushort_as_half((unsigned short)(w[i] & 0xFFFFu)),
+                                                     __ushort_as_half((unsigned short)(w[i] >> 16))));
+      v[2 * i] = f.x;
+      v[2 * i + 1] = f.y;
+    } else {
+      v[2 * i] = bf16_lo(w[i]);
+      v[2 * i + 1] = bf16_hi(w[i]);
+    }
+  }
+}
+template <typename T>
+MOE_DEV void pack8(const float (&v)[8], uint32_t (&w)[sizeof(T) * 2]) {
+#pragma unroll
+  for (int i = 0; i < (int)sizeof(T) * 2; ++i) {
+    if constexpr (std::is_same_v<T, float>) {
+      w[i] = __float_as_uint(v[i]);
+    } else if constexpr (std::is_same_v<T, __half>) {
+      const __half2 h = __floats2half2_rn(v[2 * i], v[2 * i + 1]);
+      w[i] = (uint32_t)__half_as_ushort(__low2half(h)) | ((uint32_t)__half_as_ushort(__high2half(h)) << 16);
+    } else {
+      w[i] = pack_bf16x2(v[2 * i], v[2 * i + 1]);
+    }
+  }
+}
+
+// A thread's 8 columns of one chunk. kVec: consecutive (n is 0 or 8; 16-byte
+// accesses); otherwise `stride` columns apart, so that a warp's accesses are
+// consecutive, and the first n of them exist.
 template <typename T, bool kVec>
-MOE_DEV void load8(const void* base, int64_t at, int n, float (&v)[8]) {
+MOE_DEV void load8(const void* base, int64_t at, int n, int stride, float (&v)[8]) {
   const T* p = static_cast<const T*>(base) + at;
   if constexpr (kVec) {
-    constexpr int kWords = sizeof(T) * 2;
+    uint32_t w[sizeof(T) * 2] = {};
     if (n > 0) {
-      uint32_t w[kWords];
 #pragma unroll
-      for (int i = 0; i < kWords / 4; ++i) {
+      for (int i = 0; i < (int)sizeof(T) / 2; ++i) {
         const uint4 q = reinterpret_cast<const uint4*>(p)[i];
         w[4 * i] = q.x; w[4 * i + 1] = q.y; w[4 * i + 2] = q.z; w[4 * i + 3] = q.w;
       }
-      const T* e = reinterpret_cast<const T*>(w);
-#pragma unroll
-      for (int i = 0; i < 8; ++i) v[i] = to_f<T>(e[i]);
-      return;
     }
-#pragma unroll
-    for (int i = 0; i < 8; ++i) v[i] = 0.0f;
+    unpack8<T>(w, v);
   } else {
 #pragma unroll
-    for (int i = 0; i < 8; ++i) v[i] = i < n ? to_f<T>(p[i]) : 0.0f;
+    for (int i = 0; i < 8; ++i) v[i] = i < n ? to_f<T>(p[i * stride]) : 0.0f;
   }
 }
 
 template <typename T, bool kVec>
-MOE_DEV void store8(void* base, int64_t at, int n, const float (&v)[8]) {
+MOE_DEV void store8(void* base, int64_t at, int n, int stride, const float (&v)[8]) {
   T* p = static_cast<T*>(base) + at;
   if constexpr (kVec) {
     if (n > 0) {
-      alignas(16) T e[8];
-#pragma unroll
-      for (int i = 0; i < 8; ++i) e[i] = from_f<T>(v[i]);
+      uint32_t w[sizeof(T) * 2];
+      pack8<T>(v, w);
 #pragma unroll
       for (int i = 0; i < (int)sizeof(T) / 2; ++i)
-        reinterpret_cast<uint4*>(p)[i] = reinterpret_cast<const uint4*>(e)[i];
+        reinterpret_cast<uint4*>(p)[i] =
+            make_uint4(w[4 * i], w[4 * i + 1], w[4 * i + 2], w[4 * i + 3]);
     }
   } else {
 #pragma unroll
     for (int i = 0; i < 8; ++i)
-      if (i < n) p[i] = from_f<T>(v[i]);
+      if (i < n) p[i * stride] = from_f<T>(v[i]);
   }
 }
 
 template <typename Act, bool kVec>
-MOE_DEV void load_w8(const void* w, bool f32, int at, int n, float (&v)[8]) {
-  if (f32) load8<float, kVec>(w, at, n, v);
-  else load8<Act, kVec>(w, at, n, v);
+MOE_DEV void load_w8(const void* w, bool f32, int at, int n, int stride, float (&v)[8]) {
+  if (f32) load8<float, kVec>(w, at, n, stride, v);
+  else load8<Act, kVec>(w, at, n, stride, v);
 }
+
+// One row tensor in the ring: every thread asks for its own columns of the
+// rows ahead with asynchronous 16-byte copies into slots that only it reads,
+// so waiting for its own copies is enough and no barrier guards the ring.
+// A slot is read as often as wanted until the row is done, which keeps the
+// row out of registers across the row sums.
+template <typename T>
+struct Slot {
+  uint32_t base;  // this thread's first 16-byte slot of the tensor in stage 0
+  static constexpr int pieces = sizeof(T) / 2;
+  static constexpr int bytes(int threads, int nc) { return threads * nc * 8 * (int)sizeof(T); }
+  MOE_DEV void ask(const void* g, int64_t at, int c, uint32_t stage) const {
+    const T* p = static_cast<const T*>(g) + at;
+#pragma unroll
+    for (int j = 0; j < pieces; ++j)
+      asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(
+                       base + stage + (uint32_t)((c * pieces + j) * blockDim.x * 16)),
+                   "l"(p + j * (16 / sizeof(T)))
+                   : "memory");
+  }
+  MOE_DEV void get(int c, uint32_t stage, float (&v)[8]) const {
+    uint32_t w[sizeof(T) * 2];
+#pragma unroll
+    for (int j = 0; j < pieces; ++j)
+      asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];"
+                   : "=r"(w[4 * j]), "=r"(w[4 * j + 1]), "=r"(w[4 * j + 2]), "=r"(w[4 * j + 3])
+                   : "r"(base + stage + (uint32_t)((c * pieces + j) * blockDim.x * 16))
+                   : "memory");
+    unpack8<T>(w, v);
+  }
+};
+
+MOE_DEV void ask_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+
+// this thread's copies have landed, but for the youngest `n` groups
+MOE_DEV void ask_wait(int n) {
+  switch (n) {
+    case 0: asm volatile("cp.async.wait_group 0;" ::: "memory"); break;
+    case 1: asm volatile("cp.async.wait_group 1;" ::: "memory"); break;
+    case 2: asm volatile("cp.async.wait_group 2;" ::: "memory"); break;
+    case 3: asm volatile("cp.async.wait_group 3;" ::: "memory"); break;
+    case 4: asm volatile("cp.async.wait_group 4;" ::: "memory"); break;
+    default: asm volatile("cp.async.wait_group 5;" ::: "memory"); break;
+  }
+}
+
+// Where a thread stands: its team (the warps that share a row) and columns.
+template <int kNC, bool kVec>
+struct Place {
+  int W, team, wid, lane, teams, stride, H;
+  int col[kNC], n[kNC];
+  MOE_DEV explicit Place(const NormArgs& p) {
+    W = p.team_warps;
+    H = p.H;
+    lane = threadIdx.x & 31;
+    team = (threadIdx.x >> 5) / W;
+    wid = (threadIdx.x >> 5) - team * W;
+    teams = (blockDim.x >> 5) / W;
+    stride = kVec ? 1 : W * 32;
+    const int me = wid * 32 + lane;
+#pragma unroll
+    for (int c = 0; c < kNC; ++c) {
+      if (kVec) {
+        col[c] = (c * W * 32 + me) * 8;
+        n[c] = col[c] < H ? 8 : 0;
+      } else {
+        col[c] = c * 8 * stride + me;
+        n[c] = min(max((H - col[c] + stride - 1) / stride, 0), 8);
+      }
+    }
+  }
+  MOE_DEV int64_t first() const { return (int64_t)blockIdx.x * teams + team; }
+  MOE_DEV int64_t step() const { return (int64_t)gridDim.x * teams; }
+};
+
+typedef float TeamBuf[2][3][kNormThreads / 32];
 
 // Sums over a team of warps. Two buffers in turn: a thread writes one again
 // only after a barrier that every reader of its last use has passed.
-template <int kN>
-MOE_DEV void team_sum(float (&v)[kN], int warps, int team, int wid, int lane,
-                      float (*buf)[kTeamsMax][3][16], int& turn) {
+template <int kN, typename P>
+MOE_DEV void team_sum(float (&v)[kN], const P& at, TeamBuf& buf, int& turn) {
 #pragma unroll
   for (int i = 0; i < kN; ++i)
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) v[i] += __shfl_xor_sync(0xffffffffu, v[i], o);
-  if (warps == 1) return;
-  if (lane == 0) {
+  if (at.W == 1) return;
+  if (at.lane == 0) {
 #pragma unroll
-    for (int i = 0; i < kN; ++i) buf[turn][team][i][wid] = v[i];
+    for (int i = 0; i < kN; ++i) buf[turn][i][at.team * at.W + at.wid] = v[i];
   }
-  asm volatile("bar.sync %0, %1;" ::"r"(1 + team), "r"(warps * 32) : "memory");
+  asm volatile("bar.sync %0, %1;" ::"r"(at.teams == 1 ? 0 : 1 + at.team), "r"(at.W * 32) : "memory");
+  // the warps' sums, one to a lane, added in a tree: the same in every warp
 #pragma unroll
-  for (int i = 0; i < kN; ++i) {
-    float s = 0.0f;
-    for (int j = 0; j < warps; ++j) s += buf[turn][team][i][j];
-    v[i] = s;
-  }
+  for (int i = 0; i < kN; ++i) v[i] = at.lane < at.W ? buf[turn][i][at.team * at.W + at.lane] : 0.0f;
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1)
+#pragma unroll
+    for (int i = 0; i < kN; ++i) v[i] += __shfl_xor_sync(0xffffffffu, v[i], o);
   turn ^= 1;
 }
 
-template <typename Res, typename Act, int kNC, bool kVec>
-__global__ void __launch_bounds__(kNormThreads) block_norm_kernel(const NormArgs p) {
-  __shared__ float buf[2][kTeamsMax][3][16];
-  const int W = p.team_warps, lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  const int team = warp / W, wid = warp - team * W;
-  const int teams = (blockDim.x >> 5) / W;
-  const int H = p.H;
-  const float inv_h = 1.0f / (float)H;
-  int turn = 0;
-  int col[kNC], n[kNC];
-  float pre[kNC][8], post[kNC][8];  // post: alpha * scale * post
+// alpha * post * scale of a thread's columns (absent weights are 1, columns
+// beyond the row 0)
+template <typename Act, int kNC, bool kVec>
+MOE_DEV void branch_weights(const NormArgs& p, const Place<kNC, kVec>& at, float (&wq)[kNC][8]) {
 #pragma unroll
   for (int c = 0; c < kNC; ++c) {
-    col[c] = ((c * W + wid) * 32 + lane) * 8;
-    n[c] = min(max(H - col[c], 0), 8);
-    if (p.pre) load_w8<Act, kVec>(p.pre, p.w_f32, col[c], n[c], pre[c]);
-#pragma unroll
-    for (int i = 0; i < 8; ++i) post[c][i] = p.alpha;
     float w[8];
-    if (p.post) {
-      load_w8<Act, kVec>(p.post, p.w_f32, col[c], n[c], w);
 #pragma unroll
-      for (int i = 0; i < 8; ++i) post[c][i] *= w[i];
+    for (int i = 0; i < 8; ++i) wq[c][i] = p.alpha;
+    if (p.post) {
+      load_w8<Act, kVec>(p.post, p.w_f32, at.col[c], at.n[c], at.stride, w);
+#pragma unroll
+      for (int i = 0; i < 8; ++i) wq[c][i] *= w[i];
     }
     if (p.scale) {
-      load_w8<Act, kVec>(p.scale, p.w_f32, col[c], n[c], w);
+      load_w8<Act, kVec>(p.scale, p.w_f32, at.col[c], at.n[c], at.stride, w);
 #pragma unroll
-      for (int i = 0; i < 8; ++i) post[c][i] *= w[i];
+      for (int i = 0; i < 8; ++i) wq[c][i] *= w[i];
     }
   }
-  for (int64_t row = (int64_t)blockIdx.x * teams + team; row < p.T;
-       row += (int64_t)gridDim.x * teams) {
-    const int64_t at = row * H;
-    float r[kNC][8];
+}
+
+template <typename Act, int kNC, bool kVec>
+MOE_DEV void pre_weights(const NormArgs& p, const Place<kNC, kVec>& at, float (&w)[kNC][8]) {
 #pragma unroll
-    for (int c = 0; c < kNC; ++c) load8<Res, kVec>(p.x, at + col[c], n[c], r[c]);
+  for (int c = 0; c < kNC; ++c) {
+    if (p.pre) load_w8<Act, kVec>(p.pre, p.w_f32, at.col[c], at.n[c], at.stride, w[c]);
+  }
+}
+
+template <typename Res, typename Act, int kNC, bool kVec>
+__global__ void __launch_bounds__(kNormThreads, 1) block_norm_kernel(const NormArgs p) {
+  __shared__ TeamBuf buf;
+  extern __shared__ __align__(16) uint8_t ring[];
+  const Place<kNC, kVec> at(p);
+  const float inv_h = 1.0f / (float)p.H;
+  const bool full = p.gate_kind == kGateFull;
+  int turn = 0;
+  Slot<Res> sx{smem_u32(ring) + threadIdx.x * 16};
+  Slot<Act> sz{sx.base + Slot<Res>::bytes(blockDim.x, kNC)};
+  Slot<Act> sg{sz.base + Slot<Act>::bytes(blockDim.x, kNC)};
+  const uint32_t stage_bytes = (uint32_t)(Slot<Res>::bytes(blockDim.x, kNC) +
+                                          (p.z ? Slot<Act>::bytes(blockDim.x, kNC) : 0) +
+                                          (full ? Slot<Act>::bytes(blockDim.x, kNC) : 0));
+  auto ask = [&](int64_t row, int s) {
+    if (row < p.T) {
+#pragma unroll
+      for (int c = 0; c < kNC; ++c) {
+        if (at.n[c] == 0) continue;
+        const int64_t e = row * p.H + at.col[c];
+        sx.ask(p.x, e, c, s * stage_bytes);
+        if (p.z) sz.ask(p.z, e, c, s * stage_bytes);
+        if (full) sg.ask(p.gate, e, c, s * stage_bytes);
+      }
+    }
+    ask_commit();
+  };
+  if (kVec)
+    for (int s = 0; s < p.stages - 1; ++s) ask(at.first() + s * at.step(), s);
+  float pre[kNC][8], wq[kNC][8];
+  pre_weights<Act>(p, at, pre);
+  if (p.z) branch_weights<Act>(p, at, wq);
+  int slot = 0;
+  for (int64_t row = at.first(); row < p.T; row += at.step()) {
+    const int64_t e = row * p.H;
+    const uint32_t stage = slot * stage_bytes;
+    float gate = 1.0f;
+    if (p.gate_kind == kGateRow) gate = static_cast<const float*>(p.gate)[row];
+    if (kVec) {
+      const int ahead = p.stages - 1;
+      ask(row + ahead * at.step(), slot + ahead < p.stages ? slot + ahead : slot - 1);
+      ask_wait(ahead);
+      slot = slot + 1 == p.stages ? 0 : slot + 1;
+    }
+    // columns beyond the row hold zeros throughout
+    float r[kNC][8];
+    float s[1] = {0.0f};
     if (p.z) {
       float z[kNC][8];
 #pragma unroll
-      for (int c = 0; c < kNC; ++c) load8<Act, kVec>(p.z, at + col[c], n[c], z[c]);
-      float f = 1.0f;
-      if (p.gate_kind == kGateRow) f = static_cast<const float*>(p.gate)[row];
+      for (int c = 0; c < kNC; ++c) {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) z[c][i] = 0.0f;
+        if (at.n[c] > 0) {
+          if (kVec) sz.get(c, stage, z[c]);
+          else load8<Act, kVec>(p.z, e + at.col[c], at.n[c], at.stride, z[c]);
+        }
+      }
       if (p.post) {
-        float s[1] = {0.0f};
 #pragma unroll
         for (int c = 0; c < kNC; ++c)
 #pragma unroll
           for (int i = 0; i < 8; ++i) s[0] = fmaf(z[c][i], z[c][i], s[0]);
-        team_sum(s, W, team, wid, lane, buf, turn);
-        f *= rsqrtf(fmaf(s[0], inv_h, p.eps));
+        team_sum(s, at, buf, turn);
+        gate *= rsqrtf(fmaf(s[0], inv_h, p.eps));
+        s[0] = 0.0f;
       }
 #pragma unroll
       for (int c = 0; c < kNC; ++c) {
-        if (p.gate_kind == kGateFull) {
+        if (full && at.n[c] > 0) {
           float g[8];
-          load8<Act, kVec>(p.gate, at + col[c], n[c], g);
+          if (kVec) sg.get(c, stage, g);
+          else load8<Act, kVec>(p.gate, e + at.col[c], at.n[c], at.stride, g);
 #pragma unroll
           for (int i = 0; i < 8; ++i) z[c][i] *= g[i];
         }
 #pragma unroll
-        for (int i = 0; i < 8; ++i) r[c][i] = fmaf(post[c][i] * f, z[c][i], r[c][i]);
-        store8<Res, kVec>(p.r, at + col[c], n[c], r[c]);
+        for (int i = 0; i < 8; ++i) r[c][i] = 0.0f;
+        if (at.n[c] == 0) continue;
+        if (kVec) sx.get(c, stage, r[c]);
+        else load8<Res, kVec>(p.x, e + at.col[c], at.n[c], at.stride, r[c]);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) r[c][i] = fmaf(gate * z[c][i], wq[c][i], r[c][i]);
+        store8<Res, kVec>(p.r, e + at.col[c], at.n[c], at.stride, r[c]);
+      }
+    } else {
+#pragma unroll
+      for (int c = 0; c < kNC; ++c) {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) r[c][i] = 0.0f;
+        if (at.n[c] == 0) continue;
+        if (kVec) sx.get(c, stage, r[c]);
+        else load8<Res, kVec>(p.x, e + at.col[c], at.n[c], at.stride, r[c]);
       }
     }
     if (p.pre) {
-      float s[1] = {0.0f};
 #pragma unroll
       for (int c = 0; c < kNC; ++c)
 #pragma unroll
         for (int i = 0; i < 8; ++i) s[0] = fmaf(r[c][i], r[c][i], s[0]);
-      team_sum(s, W, team, wid, lane, buf, turn);
+      team_sum(s, at, buf, turn);
       const float f = rsqrtf(fmaf(s[0], inv_h, p.eps));
 #pragma unroll
       for (int c = 0; c < kNC; ++c) {
+        if (at.n[c] == 0) continue;
 #pragma unroll
         for (int i = 0; i < 8; ++i) r[c][i] *= f * pre[c][i];
-        store8<Act, kVec>(p.u, at + col[c], n[c], r[c]);
+        store8<Act, kVec>(p.u, e + at.col[c], at.n[c], at.stride, r[c]);
       }
     }
   }
@@ -226,163 +394,203 @@ __global__ void __launch_bounds__(kNormThreads) block_norm_kernel(const NormArgs
 //   e  = dr + R (du pre - h mean(du pre h))          dx = e
 //   q  = alpha scale gate e
 //   dz = Z (q post - y mean(q post y))               (without post: dz = q)
-//   dpre = sum_t du h;  c = sum_t alpha gate e y;  dpost = scale c;
-//   dscale = post c;    dgate = alpha scale post y e (summed over the row)
-// Two rounds of row sums: (r^2, du pre r, z^2), then alpha scale post y e,
-// which gives both the row's gate gradient and the mean in dz. Each thread
-// keeps its columns' sums over the rows of its CTA in registers; the CTAs'
-// sums are added in a fixed order by a second kernel.
+//   dpre = sum_t du h;  c = sum_t gate e y;          dpost = alpha scale c;
+//   dscale = alpha post c;   dgate = alpha scale post y e (summed over the row)
+// Two rounds of row sums: (r^2, du pre r, z^2), then w z e with w = alpha
+// scale post, which gives both the row's gate gradient and the mean in dz.
+// Each thread keeps its columns' sums over the rows of its CTA in registers;
+// the CTAs' sums are added in a fixed order by a second kernel.
 template <typename Res, typename Act, int kNC, bool kVec>
-__global__ void __launch_bounds__(kNormThreads) block_norm_backward_kernel(const NormArgs p) {
-  __shared__ float buf[2][kTeamsMax][3][16];
-  const int W = p.team_warps, lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  const int team = warp / W, wid = warp - team * W;
-  const int teams = (blockDim.x >> 5) / W;
+__global__ void __launch_bounds__(kBackThreads, 1) block_norm_backward_kernel(const NormArgs p) {
+  __shared__ TeamBuf buf;
+  extern __shared__ __align__(16) uint8_t ring[];
+  const Place<kNC, kVec> at(p);
   const int H = p.H;
   const float inv_h = 1.0f / (float)H;
+  const bool full = p.gate_kind == kGateFull;
   int turn = 0;
-  int col[kNC], n[kNC];
   float s_pre[kNC][8], s_c[kNC][8];
 #pragma unroll
-  for (int c = 0; c < kNC; ++c) {
-    col[c] = ((c * W + wid) * 32 + lane) * 8;
-    n[c] = min(max(H - col[c], 0), 8);
+  for (int c = 0; c < kNC; ++c)
 #pragma unroll
     for (int i = 0; i < 8; ++i) s_pre[c][i] = s_c[c][i] = 0.0f;
-  }
-  for (int64_t row = (int64_t)blockIdx.x * teams + team; row < p.T;
-       row += (int64_t)gridDim.x * teams) {
-    const int64_t at = row * H;
-    float r[kNC][8], du[kNC][8], z[kNC][8], e[kNC][8];
+
+  const uint32_t act_bytes = Slot<Act>::bytes(blockDim.x, kNC);
+  const uint32_t res_bytes = Slot<Res>::bytes(blockDim.x, kNC);
+  uint32_t next = smem_u32(ring) + threadIdx.x * 16;
+  const uint32_t ring0 = next;
+  const Slot<Res> sr{next};
+  if (p.pre) next += res_bytes;
+  const Slot<Res> sd{next};
+  if (p.dr) next += res_bytes;
+  const Slot<Act> su{next};
+  if (p.pre) next += act_bytes;
+  const Slot<Act> sz{next};
+  if (p.z) next += act_bytes;
+  const Slot<Act> sg{next};
+  if (full) next += act_bytes;
+  const uint32_t stage_bytes = next - ring0;
+  auto ask = [&](int64_t row, int s) {
+    if (row < p.T) {
+#pragma unroll
+      for (int c = 0; c < kNC; ++c) {
+        if (at.n[c] == 0) continue;
+        const int64_t e = row * H + at.col[c];
+        if (p.pre) {
+          sr.ask(p.x, e, c, s * stage_bytes);
+          su.ask(p.du, e, c, s * stage_bytes);
+        }
+        if (p.z) sz.ask(p.z, e, c, s * stage_bytes);
+        if (p.dr) sd.ask(p.dr, e, c, s * stage_bytes);
+        if (full) sg.ask(p.gate, e, c, s * stage_bytes);
+      }
+    }
+    ask_commit();
+  };
+  if (kVec)
+    for (int s = 0; s < p.stages - 1; ++s) ask(at.first() + s * at.step(), s);
+  float pre[kNC][8], wq[kNC][8];
+  pre_weights<Act>(p, at, pre);
+  if (p.z) branch_weights<Act>(p, at, wq);
+  int slot = 0;
+  for (int64_t row = at.first(); row < p.T; row += at.step()) {
+    const int64_t e0 = row * H;
+    const uint32_t stage = slot * stage_bytes;
+    float row_gate = 1.0f;
+    if (p.gate_kind == kGateRow) row_gate = static_cast<const float*>(p.gate)[row];
+    if (kVec) {
+      const int ahead = p.stages - 1;
+      ask(row + ahead * at.step(), slot + ahead < p.stages ? slot + ahead : slot - 1);
+      ask_wait(ahead);
+      slot = slot + 1 == p.stages ? 0 : slot + 1;
+    }
+    auto get = [&](auto s, const void* g, int c, float (&v)[8]) {
+      using S = decltype(s);
+      if (kVec) s.get(c, stage, v);
+      else if constexpr (std::is_same_v<S, Slot<Res>>)
+        load8<Res, kVec>(g, e0 + at.col[c], at.n[c], at.stride, v);
+      else
+        load8<Act, kVec>(g, e0 + at.col[c], at.n[c], at.stride, v);
+    };
     float s[3] = {0.0f, 0.0f, 0.0f};
 #pragma unroll
     for (int c = 0; c < kNC; ++c) {
+      if (at.n[c] == 0) continue;
+      if (p.pre) {
+        float r[8], du[8];
+        get(sr, p.x, c, r);
+        get(su, p.du, c, du);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+          s[0] = fmaf(r[i], r[i], s[0]);
+          s[1] = fmaf(du[i] * pre[c][i], r[i], s[1]);
+        }
+      }
+      if (p.post) {
+        float z[8];
+        get(sz, p.z, c, z);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) s[2] = fmaf(z[i], z[i], s[2]);
+      }
+    }
+    if (p.pre || p.post) team_sum(s, at, buf, turn);
+    const float R = rsqrtf(fmaf(s[0], inv_h, p.eps));
+    const float r_part = -R * R * R * (s[1] * inv_h);  // of r in dx
+    const float Z = p.post ? rsqrtf(fmaf(s[2], inv_h, p.eps)) : 1.0f;
+    float e[kNC][8];  // dx, then w e (times a full gate)
+    float t[1] = {0.0f};
+#pragma unroll
+    for (int c = 0; c < kNC; ++c) {
+      if (at.n[c] == 0) continue;
       if (p.dr) {
-        load8<Res, kVec>(p.dr, at + col[c], n[c], e[c]);
+        get(sd, p.dr, c, e[c]);
       } else {
 #pragma unroll
         for (int i = 0; i < 8; ++i) e[c][i] = 0.0f;
       }
       if (p.pre) {
-        load8<Res, kVec>(p.x, at + col[c], n[c], r[c]);
-        load8<Act, kVec>(p.du, at + col[c], n[c], du[c]);
-        float w[8];
-        load_w8<Act, kVec>(p.pre, p.w_f32, col[c], n[c], w);
+        float r[8], du[8];
+        get(sr, p.x, c, r);
+        get(su, p.du, c, du);
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
-          s[0] = fmaf(r[c][i], r[c][i], s[0]);
-          s[1] = fmaf(du[c][i] * w[i], r[c][i], s[1]);
+          s_pre[c][i] = fmaf(du[i], r[i] * R, s_pre[c][i]);
+          e[c][i] = fmaf(du[i] * pre[c][i], R, fmaf(r[i], r_part, e[c][i]));
         }
+        store8<Res, kVec>(p.dx, e0 + at.col[c], at.n[c], at.stride, e[c]);
       }
-      if (p.z) {
-        load8<Act, kVec>(p.z, at + col[c], n[c], z[c]);
-        if (p.post) {
-#pragma unroll
-          for (int i = 0; i < 8; ++i) s[2] = fmaf(z[c][i], z[c][i], s[2]);
-        }
-      }
-    }
-    team_sum(s, W, team, wid, lane, buf, turn);
-    if (p.pre) {
-      const float R = rsqrtf(fmaf(s[0], inv_h, p.eps));
-      const float mean = s[1] * R * inv_h;
-#pragma unroll
-      for (int c = 0; c < kNC; ++c) {
-        float w[8];
-        load_w8<Act, kVec>(p.pre, p.w_f32, col[c], n[c], w);
+      if (!p.z) continue;
+      float z[8];
+      get(sz, p.z, c, z);
+      if (full) {
+        float g[8], dg[8];
+        get(sg, p.gate, c, g);
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
-          const float h = r[c][i] * R;
-          s_pre[c][i] = fmaf(du[c][i], h, s_pre[c][i]);
-          e[c][i] = fmaf(R, fmaf(du[c][i], w[i], -h * mean), e[c][i]);
+          const float y = z[i] * Z;
+          s_c[c][i] = fmaf(e[c][i] * g[i], y, s_c[c][i]);
+          e[c][i] *= wq[c][i];
+          dg[i] = e[c][i] * y;
+          e[c][i] *= g[i];
+          t[0] = fmaf(e[c][i], z[i], t[0]);
         }
-        if (p.dx) store8<Res, kVec>(p.dx, at + col[c], n[c], e[c]);
+        store8<Act, kVec>(p.dgate, e0 + at.col[c], at.n[c], at.stride, dg);
+      } else {
+        const float zg = Z * row_gate;
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+          s_c[c][i] = fmaf(e[c][i], z[i] * zg, s_c[c][i]);
+          e[c][i] *= wq[c][i];
+          t[0] = fmaf(e[c][i], z[i], t[0]);
+        }
       }
     }
     if (!p.z) continue;
-    const float Z = p.post ? rsqrtf(fmaf(s[2], inv_h, p.eps)) : 1.0f;
-    float row_gate = 1.0f;
-    if (p.gate_kind == kGateRow) row_gate = static_cast<const float*>(p.gate)[row];
-    float t[1] = {0.0f};
-    // e becomes q post; with a full gate its gradient goes out here
-#pragma unroll
-    for (int c = 0; c < kNC; ++c) {
-      float post[8], sc[8];
-#pragma unroll
-      for (int i = 0; i < 8; ++i) post[i] = sc[i] = 1.0f;
-      if (p.post) load_w8<Act, kVec>(p.post, p.w_f32, col[c], n[c], post);
-      if (p.scale) load_w8<Act, kVec>(p.scale, p.w_f32, col[c], n[c], sc);
-      float g[8], dg[8];
-#pragma unroll
-      for (int i = 0; i < 8; ++i) g[i] = row_gate;
-      if (p.gate_kind == kGateFull) load8<Act, kVec>(p.gate, at + col[c], n[c], g);
-#pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        const float y = z[c][i] * Z;
-        const float ae = p.alpha * e[c][i];
-        s_c[c][i] = fmaf(ae * g[i], y, s_c[c][i]);
-        const float b = ae * sc[i] * post[i];
-        dg[i] = b * y;
-        t[0] += p.gate_kind == kGateFull ? dg[i] * g[i] : dg[i];
-        e[c][i] = b * g[i];
-        z[c][i] = y;
-      }
-      if (p.gate_kind == kGateFull) store8<Act, kVec>(p.dgate, at + col[c], n[c], dg);
-    }
-    float mean = 0.0f;
+    float z_part = 0.0f;  // of z in dz
     if (p.post || p.gate_kind == kGateRow) {
-      team_sum(t, W, team, wid, lane, buf, turn);
-      if (p.gate_kind == kGateRow && wid == 0 && lane == 0)
-        static_cast<float*>(p.dgate)[row] = t[0];
-      mean = p.post ? t[0] * row_gate * inv_h : 0.0f;
+      team_sum(t, at, buf, turn);
+      if (p.gate_kind == kGateRow && at.wid == 0 && at.lane == 0)
+        static_cast<float*>(p.dgate)[row] = t[0] * Z;
+      if (p.post) z_part = -Z * Z * Z * row_gate * (t[0] * inv_h);
     }
+    const float zg = Z * row_gate;
 #pragma unroll
     for (int c = 0; c < kNC; ++c) {
+      if (at.n[c] == 0) continue;
+      float z[8];
+      get(sz, p.z, c, z);
 #pragma unroll
-      for (int i = 0; i < 8; ++i) e[c][i] = Z * fmaf(-z[c][i], mean, e[c][i]);
-      store8<Act, kVec>(p.dz, at + col[c], n[c], e[c]);
+      for (int i = 0; i < 8; ++i) e[c][i] = fmaf(e[c][i], zg, z[i] * z_part);
+      store8<Act, kVec>(p.dz, e0 + at.col[c], at.n[c], at.stride, e[c]);
     }
   }
-  // the CTA's column sums: its teams' in turn, through shared memory
-  if (teams == 1) {
-#pragma unroll
-    for (int c = 0; c < kNC; ++c) {
-      if (n[c] > 0) {
-        float* dst = p.part + (int64_t)blockIdx.x * 2 * H + col[c];
-#pragma unroll
-        for (int i = 0; i < 8; ++i)
-          if (i < n[c]) {
-            dst[i] = s_pre[c][i];
-            dst[H + i] = s_c[c][i];
-          }
-      }
-    }
-    return;
-  }
-  __shared__ float sum[2][kNormThreads * 8];
-  for (int t = 0; t < teams; ++t) {
-    if (team == t) {
+  // the CTA's column sums: its teams' in turn, through the ring's memory
+  // (every thread has read its own slots; the others' are behind the barrier)
+  if (kVec) ask_wait(0);
+  __syncthreads();
+  float* const sum = reinterpret_cast<float*>(ring);
+  for (int t = 0; t < at.teams; ++t) {
+    if (at.team == t) {
 #pragma unroll
       for (int c = 0; c < kNC; ++c)
 #pragma unroll
         for (int i = 0; i < 8; ++i)
-          if (i < n[c]) {
-            const int h = col[c] + i;
-            sum[0][h] = s_pre[c][i] + (t > 0 ? sum[0][h] : 0.0f);
-            sum[1][h] = s_c[c][i] + (t > 0 ? sum[1][h] : 0.0f);
+          if (i < at.n[c]) {
+            const int h = at.col[c] + i * at.stride;
+            sum[h] = s_pre[c][i] + (t > 0 ? sum[h] : 0.0f);
+            sum[H + h] = s_c[c][i] + (t > 0 ? sum[H + h] : 0.0f);
           }
     }
     __syncthreads();
   }
-  for (int h = threadIdx.x; h < H; h += blockDim.x) {
-    p.part[(int64_t)blockIdx.x * 2 * H + h] = sum[0][h];
-    p.part[(int64_t)blockIdx.x * 2 * H + H + h] = sum[1][h];
-  }
+  for (int h = threadIdx.x; h < 2 * H; h += blockDim.x)
+    p.part[(int64_t)blockIdx.x * 2 * H + h] = sum[h];
 }
 
 struct ColumnArgs {
   const float* part;
   int32_t parts, H, w_f32;
+  float alpha;
   const void* post;
   const void* scale;
   float* dpre;
@@ -390,15 +598,16 @@ struct ColumnArgs {
   float* dscale;
 };
 
-// Sums of the CTAs' column sums, in a fixed order: 32 columns x 8 strands.
+// Sums of the CTAs' column sums, in a fixed order: 32 columns x 32 strands.
 template <typename Act>
-__global__ void __launch_bounds__(256) block_norm_columns_kernel(const ColumnArgs p) {
-  __shared__ float sh[2][8][33];
+__global__ void __launch_bounds__(1024) block_norm_columns_kernel(const ColumnArgs p) {
+  __shared__ float sh[2][32][33];
   const int x = threadIdx.x & 31, y = threadIdx.x >> 5;
-  const int h = blockIdx.x * 32 + x;
+  int h = blockIdx.x * 32 + x;
   float a = 0.0f, b = 0.0f;
   if (h < p.H) {
-    for (int i = y; i < p.parts; i += 8) {
+#pragma unroll 4
+    for (int i = y; i < p.parts; i += 32) {
       a += p.part[(int64_t)i * 2 * p.H + h];
       b += p.part[(int64_t)i * 2 * p.H + p.H + h];
     }
@@ -406,34 +615,54 @@ __global__ void __launch_bounds__(256) block_norm_columns_kernel(const ColumnArg
   sh[0][y][x] = a;
   sh[1][y][x] = b;
   __syncthreads();
-  if (y != 0 || h >= p.H) return;
-  for (int i = 1; i < 8; ++i) {
-    a += sh[0][i][x];
-    b += sh[1][i][x];
+  // each warp adds one column's strands
+  a = sh[0][x][y];
+  b = sh[1][x][y];
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) {
+    a += __shfl_xor_sync(0xffffffffu, a, o);
+    b += __shfl_xor_sync(0xffffffffu, b, o);
   }
+  h = blockIdx.x * 32 + y;
+  if (x != 0 || h >= p.H) return;
   auto weight = [&](const void* w) {
     if (w == nullptr) return 1.0f;
     return p.w_f32 ? static_cast<const float*>(w)[h] : to_f<Act>(static_cast<const Act*>(w)[h]);
   };
   if (p.dpre) p.dpre[h] = a;
-  if (p.dpost) p.dpost[h] = b * weight(p.scale);
-  if (p.dscale) p.dscale[h] = b * weight(p.post);
+  if (p.dpost) p.dpost[h] = p.alpha * b * weight(p.scale);
+  if (p.dscale) p.dscale[h] = p.alpha * b * weight(p.post);
 }
 
+// How rows are spread over threads, and the rows asked for ahead.
 struct Plan {
-  int nc, team_warps, teams, threads;
+  int nc, team_warps, teams, threads, stages;
+  bool vec;
+  size_t smem;
 };
 
-// Columns per thread (8 nc) and warps per row: a row within 4096 columns is
-// spread over up to 16 warps with 8 columns a thread; wider rows take 16 or
-// 32 columns a thread. Narrow rows share a CTA of 8 warps.
-Plan plan_of(int H) {
+// 8 columns a thread up to 8192 columns, 16 above: the weights and column sums
+// of so many fit in registers beside the row's. One CTA per SM of up to 1024
+// threads, with fewer teams where there are not rows enough for every SM's.
+// per_column: bytes of the row tensors per column.
+Plan plan_of(int64_t T, int H, int per_column, bool vec, int sms, bool backward) {
   Plan q;
   const int chunks = (H + 7) / 8;
-  q.nc = chunks <= kNormThreads ? 1 : chunks <= 2 * kNormThreads ? 2 : 4;
+  const int threads = backward ? kBackThreads : kNormThreads;
+  q.nc = chunks <= threads ? 1 : chunks <= 2 * threads ? 2 : 4;
   q.team_warps = (chunks + 32 * q.nc - 1) / (32 * q.nc);
-  q.teams = q.team_warps <= 4 ? kTeamsMax / q.team_warps : 1;
+  const int fit = threads / 32 / q.team_warps;
+  // teams of more than a warp meet at a barrier of their own, of which there are 15
+  const int most = q.team_warps > 1 && fit > 15 ? 15 : fit;
+  const int64_t want = (T + sms - 1) / sms;
+  q.teams = (int)(want < most ? want : most);
   q.threads = 32 * q.team_warps * q.teams;
+  const size_t stage = (size_t)q.threads * q.nc * 8 * per_column;
+  q.vec = vec && stage <= kRing;
+  q.stages = q.vec ? (int)(kRing / stage < kMaxStages ? kRing / stage : kMaxStages) : 0;
+  q.smem = q.stages * stage;
+  // the backward's column sums of the teams meet in the same memory
+  if (backward && q.smem < (size_t)8 * H) q.smem = (size_t)8 * H;
   return q;
 }
 
@@ -452,33 +681,26 @@ cudaError_t by_types(int res, int act, F&& f) {
   return cudaErrorInvalidValue;
 }
 
-template <typename F>
-cudaError_t by_plan(const Plan& q, bool vec, F&& f) {
+template <bool kBackward, typename F>
+cudaError_t by_plan(const Plan& q, F&& f) {
   using std::integral_constant;
   auto go = [&](auto v) {
     if (q.nc == 1) return f(integral_constant<int, 1>{}, v);
-    if (q.nc == 2) return f(integral_constant<int, 2>{}, v);
-    return f(integral_constant<int, 4>{}, v);
+    if constexpr (kBackward) {
+      if (q.nc == 4) return f(integral_constant<int, 4>{}, v);
+    }
+    return f(integral_constant<int, 2>{}, v);
   };
-  return vec ? go(std::true_type{}) : go(std::false_type{});
+  return q.vec ? go(std::true_type{}) : go(std::false_type{});
 }
 
-// CTAs that are resident together on the whole device, by CTA size
+// the ring may take most of an SM's shared memory
 template <typename K>
-struct Resident {
-  std::atomic<int> by_warps[kNormThreads / 32 + 1] = {};
-  int get(K kernel, int threads, int sms) {
-    std::atomic<int>& known = by_warps[threads / 32];
-    int per = known.load(std::memory_order_relaxed);
-    if (per == 0) {
-      if (cudaOccupancyMaxActiveBlocksPerMultiprocessor(&per, kernel, threads, 0) != cudaSuccess ||
-          per < 1)
-        per = 1;
-      known.store(per, std::memory_order_relaxed);
-    }
-    return per * sms;
-  }
-};
+cudaError_t allow_smem(DeviceOnce& once, K kernel) {
+  return once.run([&] {
+    return cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kRing);
+  });
+}
 
 bool norm_vec(const NormArgs& a) {
   const void* const all[] = {a.x, a.z, a.pre, a.post, a.scale, a.r, a.u, a.dr, a.du, a.dx, a.dz,
@@ -542,17 +764,22 @@ int moe_block_norm(int64_t T, int32_t H, int32_t res_type, int32_t act_type, int
   a.w_f32 = w_type == MOE_FP32;
   a.alpha = alpha;
   a.eps = eps;
-  const Plan q = plan_of(H);
+  const int sms = moe_device_sm_count();
+  const int res_size = res_type == MOE_FP32 ? 4 : 2, act_size = act_type == MOE_FP32 ? 4 : 2;
+  const int per_column = res_size + (z ? act_size : 0) + (gate_kind == kGateFull ? act_size : 0);
+  const Plan q = plan_of(T, H, per_column, norm_vec(a), sms, false);
   a.team_warps = q.team_warps;
+  a.stages = q.stages;
   const cudaError_t e = by_types(res_type, act_type, [&](auto res, auto act) {
     using Res = decltype(res);
     using Act = decltype(act);
-    return by_plan(q, norm_vec(a), [&](auto nc, auto vec) {
+    return by_plan<false>(q, [&](auto nc, auto vec) {
       auto* kernel = block_norm_kernel<Res, Act, decltype(nc)::value, decltype(vec)::value>;
-      static Resident<decltype(kernel)> resident;
-      const int all = resident.get(kernel, q.threads, moe_device_sm_count());
+      static DeviceOnce once;
+      const cudaError_t r0 = allow_smem(once, kernel);
+      if (r0 != cudaSuccess) return r0;
       const int64_t need = (T + q.teams - 1) / q.teams;
-      kernel<<<(unsigned)(need < all ? need : all), q.threads, 0,
+      kernel<<<(unsigned)(need < sms ? need : sms), q.threads, q.smem,
                static_cast<cudaStream_t>(stream)>>>(a);
       return cudaGetLastError();
     });
@@ -617,25 +844,31 @@ int moe_block_norm_backward(int64_t T, int32_t H, int32_t res_type, int32_t act_
   a.alpha = alpha;
   a.eps = eps;
   a.part = static_cast<float*>(ws);
-  const Plan q = plan_of(H);
+  const int sms = moe_device_sm_count();
+  const int res_size = res_type == MOE_FP32 ? 4 : 2, act_size = act_type == MOE_FP32 ? 4 : 2;
+  const int per_column = (pre ? res_size + act_size : 0) + (dr ? res_size : 0) +
+                         (z ? act_size : 0) + (gate_kind == kGateFull ? act_size : 0);
+  const Plan q = plan_of(T, H, per_column, norm_vec(a), sms, true);
   a.team_warps = q.team_warps;
+  a.stages = q.stages;
   const cudaError_t e = by_types(res_type, act_type, [&](auto res, auto act) {
     using Res = decltype(res);
     using Act = decltype(act);
-    return by_plan(q, norm_vec(a), [&](auto nc, auto vec) {
+    return by_plan<true>(q, [&](auto nc, auto vec) {
       auto* kernel = block_norm_backward_kernel<Res, Act, decltype(nc)::value,
                                                 decltype(vec)::value>;
-      static Resident<decltype(kernel)> resident;
-      const int all = resident.get(kernel, q.threads, moe_device_sm_count());
+      static DeviceOnce once;
+      const cudaError_t r0 = allow_smem(once, kernel);
+      if (r0 != cudaSuccess) return r0;
       int64_t grid = (T + q.teams - 1) / q.teams;
-      if (grid > all) grid = all;
+      if (grid > sms) grid = sms;
       if (grid > kMaxParts) grid = kMaxParts;
-      kernel<<<(unsigned)grid, q.threads, 0, s>>>(a);
+      kernel<<<(unsigned)grid, q.threads, q.smem, s>>>(a);
       const cudaError_t r1 = cudaGetLastError();
       if (r1 != cudaSuccess || (!pre && !post && !scale)) return r1;
-      const ColumnArgs c{a.part, (int32_t)grid, H, a.w_f32, post, scale,
+      const ColumnArgs c{a.part, (int32_t)grid, H, a.w_f32, alpha, post, scale,
                          pre ? dpre : nullptr, post ? dpost : nullptr, scale ? dscale : nullptr};
-      block_norm_columns_kernel<Act><<<(H + 31) / 32, 256, 0, s>>>(c);
+      block_norm_columns_kernel<Act><<<(H + 31) / 32, 1024, 0, s>>>(c);
       return cudaGetLastError();
     });
   });
