@@ -3,8 +3,8 @@
 //   norm = sqrt(sum_i sum_j g_ij^2)     c = min(1, max_norm / (norm + 1e-6))
 //   out_ij = g_ij * c                   (out may be g itself)
 //
-// The tensors are cut into chunks of 8192 elements; each CTA takes a
-// contiguous run of chunks. The first kernel leaves one partial sum of
+// The tensors are cut into chunks of at most 32 KiB; the CTAs
+// go through them side by side, and a thread has 4 x 16 bytes in flight. The first kernel leaves one partial sum of
 // squares per CTA, the second adds them (every CTA the same sum, in the same
 // order) and scales. No atomics: the norm is the same in every run.
 //
@@ -23,13 +23,15 @@ namespace moe {
 
 namespace {
 
-constexpr int kChunk = 8192;
 constexpr int kClipThreads = 256;
+constexpr int kVectors = 8;       // 16-byte vectors of a chunk per thread
+constexpr int kAtOnce = 4;        // of them in flight
+constexpr int kCtasPerSm = 6;
 constexpr int kParts = MOE_GRAD_PARTIALS;
-constexpr int kMaxTensors = 256;  // per launch: the table travels as kernel arguments
+constexpr int kMaxTensors = 1024;  // per launch: the table travels as kernel arguments
 
 // `chunk0[i]` is the tensor's first chunk. Its first chunk also holds the
-// elements before its first 16-byte boundary.
+// elements before its first 128-byte boundary.
 template <int kCap>
 struct GradTable {
   const void* g[kCap];
@@ -39,24 +41,25 @@ struct GradTable {
   uint8_t type[kCap];
   int32_t n;
   int32_t in_place;  // every tensor's output is the tensor itself
+  int32_t vectors;   // 16-byte vectors per thread and chunk, 1 to kVectors
 };
 
 struct Span {
   int64_t begin, end;
 };
 
-MOE_DEV int elements_to_boundary(const void* p, int es) {
-  return (int)((16u - (uint32_t)(reinterpret_cast<uintptr_t>(p) & 15u)) & 15u) / es;
+MOE_DEV int elements_to_boundary(const void* p, int es, uint32_t boundary = 16u) {
+  return (int)((0u - (uint32_t)reinterpret_cast<uintptr_t>(p)) & (boundary - 1u)) / es;
 }
 
 template <int kCap>
 MOE_DEV Span span_of(const GradTable<kCap>& t, int i, int chunk) {
   const int es = t.type[i] == MOE_FP32 ? 4 : 2;
-  const int64_t head = elements_to_boundary(t.g[i], es);
-  const int64_t k = chunk - t.chunk0[i];
+  const int64_t head = elements_to_boundary(t.g[i], es, 128u);
+  const int64_t k = chunk - t.chunk0[i], len = t.vectors * (kClipThreads * 16 / es);
   Span s;
-  s.begin = k == 0 ? 0 : head + k * kChunk;
-  s.end = min(head + (k + 1) * kChunk, t.size[i]);
+  s.begin = k == 0 ? 0 : head + k * len;
+  s.end = min(head + (k + 1) * len, t.size[i]);
   return s;
 }
 
@@ -83,63 +86,109 @@ MOE_DEV T grad_t(float v) {
   else return __float2bfloat16_rn(v);
 }
 
+// the elements of a 32-bit word as fp32, and back
 template <typename T>
-struct alignas(16) Vec {
-  T v[16 / sizeof(T)];
-};
+MOE_DEV void word_to_f(uint32_t w, float (&f)[4 / sizeof(T)]) {
+  if constexpr (std::is_same_v<T, float>) {
+    f[0] = __uint_as_float(w);
+  } else if constexpr (std::is_same_v<T, __half>) {
+    f[0] = __half2float(__ushort_as_half((unsigned short)(w & 0xFFFFu)));
+    f[1] = __half2float(__ushort_as_half((unsigned short)(w >> 16)));
+  } else {
+    f[0] = bf16_lo(w);
+    f[1] = bf16_hi(w);
+  }
+}
+template <typename T>
+MOE_DEV uint32_t word_scaled(uint32_t w, float c) {
+  float f[4 / sizeof(T)];
+  word_to_f<T>(w, f);
+  if constexpr (std::is_same_v<T, float>) {
+    return __float_as_uint(f[0] * c);
+  } else if constexpr (std::is_same_v<T, __half>) {
+    return (uint32_t)__half_as_ushort(__float2half_rn(f[0] * c)) |
+           ((uint32_t)__half_as_ushort(__float2half_rn(f[1] * c)) << 16);
+  } else {
+    return pack_bf16x2(f[0] * c, f[1] * c);
+  }
+}
+
+template <typename T>
+MOE_DEV uint4 vector_scaled(const uint4& x, float c) {
+  return make_uint4(word_scaled<T>(x.x, c), word_scaled<T>(x.y, c), word_scaled<T>(x.z, c),
+                    word_scaled<T>(x.w, c));
+}
+
+// the squares of one 16-byte vector, out of line: zeros and extremes only
+template <typename T>
+__device__ __noinline__ double squares_in_fp64(uint4 x) {
+  constexpr int kE = 4 / sizeof(T);
+  const uint32_t w[4] = {x.x, x.y, x.z, x.w};
+  double d = 0.0;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    float f[kE];
+    word_to_f<T>(w[i], f);
+#pragma unroll
+    for (int j = 0; j < kE; ++j) d = fma((double)f[j], (double)f[j], d);
+  }
+  return d;
+}
 
 // The squares of one 16-byte vector. fp32 keeps them to 2^-22 unless their
 // sum is outside [2^-80, 2^100], where a square may have been lost or have
 // overflowed.
 template <typename T>
-MOE_DEV double squares(const Vec<T>& x) {
-  constexpr int kV = 16 / sizeof(T);
-  float s = 0.0f, any = 0.0f;
+MOE_DEV double squares(const uint4& x) {
+  constexpr int kE = 4 / sizeof(T);
+  const uint32_t w[4] = {x.x, x.y, x.z, x.w};
+  float s = 0.0f;
 #pragma unroll
-  for (int i = 0; i < kV; ++i) {
-    const float f = grad_f<T>(x.v[i]);
-    s = fmaf(f, f, s);
-    any = fmaxf(any, fabsf(f));
-  }
-  if ((s > 0x1p-80f && s < 0x1p100f) || (s == 0.0f && any == 0.0f)) return (double)s;
-  double d = 0.0;
+  for (int i = 0; i < 4; ++i) {
+    float f[kE];
+    word_to_f<T>(w[i], f);
 #pragma unroll
-  for (int i = 0; i < kV; ++i) {
-    const double f = (double)grad_f<T>(x.v[i]);
-    d = fma(f, f, d);
+    for (int j = 0; j < kE; ++j) s = fmaf(f[j], f[j], s);
   }
-  return d;
+  return s > 0x1p-80f && s < 0x1p100f ? (double)s : squares_in_fp64<T>(x);
 }
 
 template <typename T>
 MOE_DEV double span_squares(const T* g, const Span& s) {
   constexpr int kV = 16 / sizeof(T);
-  constexpr int kStep = kClipThreads * kV;
   double sum = 0.0;
-  int64_t at = min(s.begin + elements_to_boundary(g + s.begin, sizeof(T)), s.end);
+  const int64_t at = min(s.begin + elements_to_boundary(g + s.begin, sizeof(T)), s.end);
   if (s.begin + threadIdx.x < at) {
     const double f = (double)grad_f<T>(g[s.begin + threadIdx.x]);
     sum = fma(f, f, sum);
   }
-  for (; at + kStep <= s.end; at += kStep)
-    sum += squares<T>(*reinterpret_cast<const Vec<T>*>(g + at + threadIdx.x * kV));
-  for (int64_t i = at + threadIdx.x; i < s.end; i += kClipThreads) {
-    const double f = (double)grad_f<T>(g[i]);
+  const int n = (int)(s.end - at) / kV;
+  const uint4* const v = reinterpret_cast<const uint4*>(g + at);
+  int q = threadIdx.x;
+  for (; q + (kAtOnce - 1) * kClipThreads < n; q += kAtOnce * kClipThreads) {
+    uint4 x[kAtOnce];
+#pragma unroll
+    for (int i = 0; i < kAtOnce; ++i) x[i] = v[q + i * kClipThreads];
+#pragma unroll
+    for (int i = 0; i < kAtOnce; ++i) sum += squares<T>(x[i]);
+  }
+  for (; q < n; q += kClipThreads) sum += squares<T>(v[q]);
+  const int64_t rest = at + (int64_t)n * kV + threadIdx.x;
+  if (rest < s.end) {
+    const double f = (double)grad_f<T>(g[rest]);
     sum = fma(f, f, sum);
   }
   return sum;
 }
 
 template <int kCap>
-__global__ void __launch_bounds__(kClipThreads)
+__global__ void __launch_bounds__(kClipThreads, kCtasPerSm)
     grad_sumsq_kernel(const __grid_constant__ GradTable<kCap> t, double* partials, int add) {
   __shared__ double red[kClipThreads / 32];
   const int total = t.chunk0[t.n];
-  const int c0 = (int)((int64_t)total * blockIdx.x / gridDim.x);
-  const int c1 = (int)((int64_t)total * (blockIdx.x + 1) / gridDim.x);
   double sum = 0.0;
-  int i = c0 < c1 ? tensor_of(t, c0) : 0;
-  for (int c = c0; c < c1; ++c) {
+  int i = (int)blockIdx.x < total ? tensor_of(t, blockIdx.x) : 0;
+  for (int c = blockIdx.x; c < total; c += gridDim.x) {
     while (c >= t.chunk0[i + 1]) ++i;
     const Span s = span_of(t, i, c);
     if (t.type[i] == MOE_FP32) sum += span_squares(static_cast<const float*>(t.g[i]), s);
@@ -162,25 +211,32 @@ __global__ void __launch_bounds__(kClipThreads)
 template <typename T>
 MOE_DEV void span_scale(const T* g, T* out, const Span& s, float c) {
   constexpr int kV = 16 / sizeof(T);
-  constexpr int kStep = kClipThreads * kV;
-  int64_t at = s.begin;
-  if (((reinterpret_cast<uintptr_t>(g) ^ reinterpret_cast<uintptr_t>(out)) & 15u) == 0) {
-    at = min(s.begin + elements_to_boundary(g + s.begin, sizeof(T)), s.end);
-    if (s.begin + threadIdx.x < at)
-      out[s.begin + threadIdx.x] = grad_t<T>(grad_f<T>(g[s.begin + threadIdx.x]) * c);
-    for (; at + kStep <= s.end; at += kStep) {
-      Vec<T> x = *reinterpret_cast<const Vec<T>*>(g + at + threadIdx.x * kV);
-#pragma unroll
-      for (int i = 0; i < kV; ++i) x.v[i] = grad_t<T>(grad_f<T>(x.v[i]) * c);
-      *reinterpret_cast<Vec<T>*>(out + at + threadIdx.x * kV) = x;
-    }
+  if (((reinterpret_cast<uintptr_t>(g) ^ reinterpret_cast<uintptr_t>(out)) & 15u) != 0) {
+    for (int64_t i = s.begin + threadIdx.x; i < s.end; i += kClipThreads)
+      out[i] = grad_t<T>(grad_f<T>(g[i]) * c);
+    return;
   }
-  for (int64_t i = at + threadIdx.x; i < s.end; i += kClipThreads)
-    out[i] = grad_t<T>(grad_f<T>(g[i]) * c);
+  const int64_t at = min(s.begin + elements_to_boundary(g + s.begin, sizeof(T)), s.end);
+  if (s.begin + threadIdx.x < at)
+    out[s.begin + threadIdx.x] = grad_t<T>(grad_f<T>(g[s.begin + threadIdx.x]) * c);
+  const int n = (int)(s.end - at) / kV;
+  const uint4* const v = reinterpret_cast<const uint4*>(g + at);
+  uint4* const o = reinterpret_cast<uint4*>(out + at);
+  int q = threadIdx.x;
+  for (; q + (kAtOnce - 1) * kClipThreads < n; q += kAtOnce * kClipThreads) {
+    uint4 x[kAtOnce];
+#pragma unroll
+    for (int i = 0; i < kAtOnce; ++i) x[i] = __ldcs(v + q + i * kClipThreads);
+#pragma unroll
+    for (int i = 0; i < kAtOnce; ++i) __stcs(o + q + i * kClipThreads, vector_scaled<T>(x[i], c));
+  }
+  for (; q < n; q += kClipThreads) __stcs(o + q, vector_scaled<T>(__ldcs(v + q), c));
+  const int64_t rest = at + (int64_t)n * kV + threadIdx.x;
+  if (rest < s.end) out[rest] = grad_t<T>(grad_f<T>(g[rest]) * c);
 }
 
 template <int kCap>
-__global__ void __launch_bounds__(kClipThreads)
+__global__ void __launch_bounds__(kClipThreads, kCtasPerSm)
     grad_clip_kernel(const __grid_constant__ GradTable<kCap> t, const double* partials,
                      float max_norm, float* norm) {
   __shared__ double red[kClipThreads / 32];
@@ -202,12 +258,10 @@ __global__ void __launch_bounds__(kClipThreads)
   const float c = factor;
   if (c == 1.0f && t.in_place) return;
   const int total = t.chunk0[t.n];
-  const int c0 = (int)((int64_t)total * blockIdx.x / gridDim.x);
-  const int c1 = (int)((int64_t)total * (blockIdx.x + 1) / gridDim.x);
-  if (c0 >= c1) return;
   // backwards: the last chunks that the norm read are still in L2
-  int i = tensor_of(t, c1 - 1);
-  for (int k = c1 - 1; k >= c0; --k) {
+  int k = total - 1 - (int)blockIdx.x;
+  int i = k >= 0 ? tensor_of(t, k) : 0;
+  for (; k >= 0; k -= gridDim.x) {
     while (k < t.chunk0[i]) --i;
     const Span s = span_of(t, i, k);
     if (t.type[i] == MOE_FP32)
@@ -221,17 +275,26 @@ __global__ void __launch_bounds__(kClipThreads)
 
 int element_size(int type) { return type == MOE_FP32 ? 4 : 2; }
 
-int chunks_of(const void* g, int64_t size, int es) {
+int chunks_of(const void* g, int64_t size, int es, int vectors) {
   if (size == 0) return 0;
-  const int64_t head = (int64_t)((16 - (reinterpret_cast<uintptr_t>(g) & 15)) & 15) / es;
-  const int64_t rest = size > head ? size - head : 1;
-  return (int)((rest + kChunk - 1) / kChunk);
+  const int64_t head = (int64_t)((0 - reinterpret_cast<uintptr_t>(g)) & 127) / es;
+  const int64_t rest = size > head ? size - head : 1, len = vectors * (kClipThreads * 16 / es);
+  return (int)((rest + len - 1) / len);
+}
+
+// Vectors per thread and chunk: fewer where the tensors are small, so that
+// the chunks still go round the CTAs that fit on the device.
+int vectors_of(const moe_grad_list& l, int ctas) {
+  int64_t bytes = 0;
+  for (int i = 0; i < l.n; ++i) bytes += l.sizes[i] * element_size(l.types[i]);
+  const int64_t each = bytes / ((int64_t)ctas * kClipThreads * 16);
+  return each >= kVectors ? kVectors : each < 1 ? 1 : (int)each;
 }
 
 // Runs f(table) over the list's tensors, kCap at a time; tensors without
 // elements are left out.
 template <int kCap, typename F>
-cudaError_t over_tables(const moe_grad_list& l, F&& f) {
+cudaError_t over_tables(const moe_grad_list& l, int ctas, F&& f) {
   int at = 0;
   bool first = true;
   do {
@@ -239,6 +302,7 @@ cudaError_t over_tables(const moe_grad_list& l, F&& f) {
     t.n = 0;
     t.chunk0[0] = 0;
     t.in_place = 1;
+    t.vectors = vectors_of(l, ctas);
     for (; at < l.n && t.n < kCap; ++at) {
       if (l.sizes[at] == 0) continue;
       const int i = t.n++;
@@ -247,7 +311,7 @@ cudaError_t over_tables(const moe_grad_list& l, F&& f) {
       if (t.out[i] != t.g[i]) t.in_place = 0;
       t.size[i] = l.sizes[at];
       t.type[i] = (uint8_t)l.types[at];
-      t.chunk0[i + 1] = t.chunk0[i] + chunks_of(t.g[i], t.size[i], element_size(l.types[at]));
+      t.chunk0[i + 1] = t.chunk0[i] + chunks_of(t.g[i], t.size[i], element_size(l.types[at]), t.vectors);
     }
     const cudaError_t e = f(t, first);
     if (e != cudaSuccess) return e;
@@ -256,7 +320,13 @@ cudaError_t over_tables(const moe_grad_list& l, F&& f) {
   return cudaSuccess;
 }
 
-int clip_grid(int sms) { return std::min(kParts, 4 * sms); }
+template <typename F>
+cudaError_t over_list(const moe_grad_list& l, int ctas, F&& f) {
+  return l.n <= 16 ? over_tables<16>(l, ctas, f)
+         : l.n <= 128 ? over_tables<128>(l, ctas, f) : over_tables<kMaxTensors>(l, ctas, f);
+}
+
+int clip_grid(int sms) { return std::min(kParts, kCtasPerSm * sms); }
 
 int check_list(const moe_grad_list* l) {
   if (!l) return MOE_ERR_NULL;
@@ -266,7 +336,8 @@ int check_list(const moe_grad_list* l) {
   for (int i = 0; i < l->n; ++i) {
     if (l->sizes[i] < 0 || l->sizes[i] > (1ll << 42)) return MOE_ERR_SHAPE;
     if (l->types[i] < MOE_BF16 || l->types[i] > MOE_FP32) return MOE_ERR_SHAPE;
-    total += l->sizes[i] / kChunk + 2;
+    // chunks: of kVectors vectors a thread, but for lists that are small
+    total += l->sizes[i] * element_size(l->types[i]) / (kVectors * kClipThreads * 16) + 4;
     if (total >= (1ll << 31)) return MOE_ERR_SHAPE;
     if (l->sizes[i] == 0) continue;
     if (!l->grads[i] || (l->out && !l->out[i])) return MOE_ERR_NULL;
@@ -298,8 +369,7 @@ int moe_grad_sumsq(const moe_grad_list* list, double* partials, void* stream) {
     grad_sumsq_kernel<<<grid, kClipThreads, 0, s>>>(t, partials, first ? 0 : 1);
     return cudaGetLastError();
   };
-  return cuda_status(list->n <= 32 ? over_tables<32>(*list, go)
-                                   : over_tables<kMaxTensors>(*list, go));
+  return cuda_status(over_list(*list, most, go));
 }
 
 int moe_grad_clip(const moe_grad_list* list, const double* partials, float max_norm, float* norm,
@@ -318,8 +388,7 @@ int moe_grad_clip(const moe_grad_list* list, const double* partials, float max_n
     grad_clip_kernel<<<grid, kClipThreads, 0, s>>>(t, partials, max_norm, norm);
     return cudaGetLastError();
   };
-  return cuda_status(list->n <= 32 ? over_tables<32>(*list, go)
-                                   : over_tables<kMaxTensors>(*list, go));
+  return cuda_status(over_list(*list, most, go));
 }
 
 }  // extern "C"
