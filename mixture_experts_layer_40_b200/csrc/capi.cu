@@ -135,20 +135,32 @@ cudaError_t make_tmap_bf16(CUtensorMap* map, const void* base, int64_t inner, in
   return r == CUDA_SUCCESS ? cudaSuccess : cudaErrorInvalidValue;
 }
 
-cudaError_t make_tmap_16b_3d(CUtensorMap* map, const void* base, int64_t inner, int64_t rows,
-                             int64_t depth, int box_inner, int box_rows) {
+static cudaError_t make_tmap_3d(CUtensorMap* map, CUtensorMapDataType type, int size,
+                                const void* base, int64_t inner, int64_t rows, int64_t depth,
+                                int box_inner, int box_rows) {
   EncodeTiledFn fn = encode_fn();
   if (fn == nullptr) return cudaErrorNotSupported;
   const cuuint64_t dims[3] = {(cuuint64_t)inner, (cuuint64_t)rows, (cuuint64_t)depth};
-  const cuuint64_t strides[2] = {(cuuint64_t)inner * 2, (cuuint64_t)inner * 2 * (cuuint64_t)rows};
+  const cuuint64_t strides[2] = {(cuuint64_t)inner * size, (cuuint64_t)inner * size * (cuuint64_t)rows};
   const cuuint32_t box[3] = {(cuuint32_t)box_inner, (cuuint32_t)box_rows, 1};
   const cuuint32_t estr[3] = {1, 1, 1};
-  // the element type only sets the value of a fill, which is zero in both
-  const CUresult r = fn(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void*>(base), dims,
-                        strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
-                        CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
-                        CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+  const CUresult r = fn(map, type, 3, const_cast<void*>(base), dims, strides, box, estr,
+                        CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+                        CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
   return r == CUDA_SUCCESS ? cudaSuccess : cudaErrorInvalidValue;
+}
+
+cudaError_t make_tmap_16b_3d(CUtensorMap* map, const void* base, int64_t inner, int64_t rows,
+                             int64_t depth, int box_inner, int box_rows) {
+  // copies move bits, and a fill is zero in both 16-bit types
+  return make_tmap_3d(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, base, inner, rows, depth, box_inner,
+                      box_rows);
+}
+
+cudaError_t make_tmap_f32_3d(CUtensorMap* map, const void* base, int64_t inner, int64_t rows,
+                             int64_t depth, int box_inner, int box_rows) {
+  return make_tmap_3d(map, CU_TENSOR_MAP_DATA_TYPE_FLOAT32, 4, base, inner, rows, depth, box_inner,
+                      box_rows);
 }
 
 }  // namespace moe

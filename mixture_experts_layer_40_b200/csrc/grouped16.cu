@@ -13,20 +13,31 @@
 // (K-major) or slowest (MN-major), so all three products read the tensors as
 // they lie: no transposed copy of the weights or of the rows is made.
 //
-// One persistent CTA per SM, 256 threads:
-//   warp 0     TMA producer: 64-deep k-blocks of A (128 rows) and B (kBN
-//              columns) into a ring of shared-memory stages
-//   warp 1     MMA issuer, M=128, N=kBN, K=16 into one of two TMEM buffers
+// Forward and input gradient put the weights on the M side of the MMA (128
+// output columns a CTA) and the group's rows on the N side, whose size goes
+// in steps of 16: a ragged group costs its own rows rounded up to 16, not to
+// a tile of 128, and a decoded token's weights stream through shared memory
+// beside a few KB of rows. The accumulator is then out^T, which the epilogue
+// turns round in shared memory.
+//
+// Kernels of two CTAs (cta_group::2) share a tile of M = 256: each SM holds
+// half of either operand, so it reads 32 KB of L2 per 64-deep k-block instead
+// of 48 KB, which is what bounds a single SM's 128 x 256 tile.
+//
+// One persistent CTA per SM:
+//   warp 0     TMA producer: 64-deep k-blocks into a ring of stages
+//   warp 1     MMA issuer (of the pair's first CTA), K=16 steps into one of
+//              two TMEM buffers
 //   warp 2     TMEM allocator; scans the groups into a tile prefix
-//   warps 4-7  epilogue: TMEM -> registers -> global memory, while the next
-//              tile's MMAs fill the other buffer
+//   warp 3     weight gradient: clears rows behind a group (below)
+//   warps 4-   epilogue: TMEM -> registers -> shared memory -> global memory,
+//              while the next tile's MMAs fill the other buffer
 // Rows of a tile beyond its group are another group's rows or padding: each
-// row of the accumulator depends on its own row of A alone, so whatever they
-// hold stays in accumulator rows that are never stored. In the weight
-// gradient the rows are the reduction: the last k-block's rows beyond the
-// group are cleared in shared memory, in both operands (a NaN or infinity
-// there would survive a product with zero), and 16-row steps past them are
-// not issued.
+// column of out^T depends on its own row alone, so whatever they hold stays
+// in accumulator columns that are never stored. In the weight gradient the
+// rows are the reduction: the last k-block's rows beyond the group are
+// cleared in shared memory, in both operands (a NaN or infinity there would
+// survive a product with zero), and 16-row steps past them are not issued.
 #include <type_traits>
 
 #include "kernels.cuh"
@@ -35,43 +46,35 @@ namespace moe {
 
 namespace {
 
-constexpr int kBM = 128;
+constexpr int kBM = 128;  // rows of the M operand per CTA
 constexpr int kBK = 64;
-constexpr int kThreads16 = 256;
 constexpr int kABytes = kBM * kBK * 2;
 constexpr int kMaxGroups16 = 1025;
-constexpr int kSmemBudget = 200 * 1024;
+constexpr int kMaxStages16 = 10;
 
-enum Way : int { kForward = 0, kInputGrad = 1, kWeightGrad = 2 };
-
-template <int kBN>
-struct Tile {
-  static constexpr int b_bytes = kBN * kBK * 2;
-  static constexpr int stage_bytes = kABytes + b_bytes;
-  static constexpr int stages = kSmemBudget / stage_bytes < 8 ? kSmemBudget / stage_bytes : 8;
-  static constexpr size_t dyn_smem = (size_t)stages * stage_bytes + 1024;
-};
+enum Way : int { kForward = 0, kInputGrad = 1 };
 
 struct Args16 {
   const int32_t* group_rows;
   const int32_t* group_start;
   int32_t n_groups;
-  int32_t kblocks;   // forward, input gradient: ceil(K / 64)
-  int32_t n_tiles;   // kBN-wide column tiles per group
-  int32_t m_tiles;   // weight gradient: 128-high row tiles of dw per group
+  int32_t kblocks;   // matmul: ceil(K / 64)
+  int32_t n_tiles;   // weight gradient: column tiles of dw per group
+  int32_t m_tiles;   // weight gradient: row tiles of dw per group
   int64_t rows;      // rows of the row buffers
   int32_t M;         // weight gradient: rows of dw per group
   int32_t N;         // columns of the output
   void* out;
   int32_t out_type;  // MOE_BF16, MOE_FP16, MOE_FP32
   int32_t accumulate;
-  uint32_t idesc;
+  uint32_t idesc;    // without the N size where that varies
   uint32_t* status;
 };
 
 struct alignas(8) Shared16 {
-  uint64_t full[8];
-  uint64_t empty[8];
+  uint64_t full[kMaxStages16];
+  uint64_t empty[kMaxStages16];
+  uint64_t ready[kMaxStages16];  // weight gradient: both CTAs' stages, cleared
   uint64_t tfull[2];
   uint64_t tempty[2];
   uint64_t drained;
@@ -82,13 +85,101 @@ struct alignas(8) Shared16 {
   int start[kMaxGroups16];
 };
 
-MOE_DEV void tma_load_3d(uint32_t dst, const CUtensorMap* map, int32_t x, int32_t y, int32_t z,
-                         uint32_t bar) {
-  asm volatile(
-      "cp.async.bulk.tensor.3d.shared::cluster.global.mbarrier::complete_tx::bytes"
-      " [%0], [%1, {%2, %3, %4}], [%5];" ::"r"(dst),
-      "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y), "r"(z), "r"(bar)
-      : "memory");
+// ------------------------------------------------------ pairs of CTAs
+MOE_DEV uint32_t cluster_rank() {
+  uint32_t r;
+  asm("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
+  return r;
+}
+MOE_DEV void cluster_sync() {
+  asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::
+                   : "memory");
+}
+// the same shared-memory address in the pair's first CTA
+MOE_DEV uint32_t in_leader(uint32_t addr) {
+  uint32_t r;
+  asm("mapa.shared::cluster.u32 %0, %1, 0;" : "=r"(r) : "r"(addr));
+  return r;
+}
+MOE_DEV void mbar_arrive_cluster(uint32_t bar) {
+  asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(bar) : "memory");
+}
+MOE_DEV void fence_acquire_cluster() { asm volatile("fence.acq_rel.cluster;" ::: "memory"); }
+
+template <int kCtas>
+MOE_DEV void load_2d(uint32_t dst, const CUtensorMap* map, int32_t x, int32_t y, uint32_t bar) {
+  if constexpr (kCtas == 1) {
+    tma_load_2d(dst, map, x, y, bar);
+  } else {
+    asm volatile(
+        "cp.async.bulk.tensor.2d.cta_group::2.shared::cluster.global.mbarrier::complete_tx::bytes"
+        " [%0], [%1, {%2, %3}], [%4];" ::"r"(dst),
+        "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y), "r"(bar)
+        : "memory");
+  }
+}
+template <int kCtas>
+MOE_DEV void load_3d(uint32_t dst, const CUtensorMap* map, int32_t x, int32_t y, int32_t z,
+                     uint32_t bar) {
+  if constexpr (kCtas == 1) {
+    asm volatile(
+        "cp.async.bulk.tensor.3d.shared::cluster.global.mbarrier::complete_tx::bytes"
+        " [%0], [%1, {%2, %3, %4}], [%5];" ::"r"(dst),
+        "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y), "r"(z), "r"(bar)
+        : "memory");
+  } else {
+    asm volatile(
+        "cp.async.bulk.tensor.3d.cta_group::2.shared::cluster.global.mbarrier::complete_tx::bytes"
+        " [%0], [%1, {%2, %3, %4}], [%5];" ::"r"(dst),
+        "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y), "r"(z), "r"(bar)
+        : "memory");
+  }
+}
+template <int kCtas>
+MOE_DEV void alloc16(uint32_t dst, uint32_t cols) {
+  if constexpr (kCtas == 1) {
+    tmem_alloc(dst, cols);
+  } else {
+    asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(dst),
+                 "r"(cols)
+                 : "memory");
+    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;" ::: "memory");
+  }
+}
+template <int kCtas>
+MOE_DEV void dealloc16(uint32_t taddr, uint32_t cols) {
+  if constexpr (kCtas == 1) {
+    tmem_dealloc(taddr, cols);
+  } else {
+    asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;" ::"r"(taddr), "r"(cols)
+                 : "memory");
+  }
+}
+template <int kCtas>
+MOE_DEV void mma16(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t accumulate) {
+  if constexpr (kCtas == 1) {
+    mma_bf16(d, a, b, idesc, accumulate);
+  } else {
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "setp.ne.b32 p, %4, 0;\n\t"
+        "tcgen05.mma.cta_group::2.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
+        "l"(a), "l"(b), "r"(idesc), "r"(accumulate)
+        : "memory");
+  }
+}
+// arrives on `bar` in every CTA of the tile when the MMAs issued so far are done
+template <int kCtas>
+MOE_DEV void commit16(uint32_t bar) {
+  if constexpr (kCtas == 1) {
+    mma_commit(bar);
+  } else {
+    asm volatile(
+        "tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64"
+        " [%0], %1;" ::"r"(bar),
+        "h"((uint16_t)3)
+        : "memory");
+  }
 }
 
 // Descriptor of an MN-major tile with 128-byte swizzling, as 64-wide TMA boxes
@@ -104,11 +195,16 @@ MOE_DEV uint64_t smem_desc_mn_sw128(uint32_t smem_addr) {
   d |= (uint64_t)2 << 61;
   return d;
 }
+// 16 reduction steps further, in the descriptor's 16-byte address units
+constexpr uint64_t kStepK = 32 >> 4;
+constexpr uint64_t kStepMN = 16 * 128 >> 4;
 
 struct TileAt {
   int g, m, n;
 };
 
+// tile -> (group, row tile of the group, column tile), columns fastest: the
+// column tiles of one row tile run side by side and share its rows in L2
 MOE_DEV TileAt tile_at(int tile, const int* prefix, int n_groups, int n_tiles) {
   int lo = 0, hi = n_groups;
   while (hi - lo > 1) {
@@ -125,9 +221,10 @@ MOE_DEV TileAt tile_at(int tile, const int* prefix, int n_groups, int n_tiles) {
 
 // Group table into shared memory, by one warp: each group's rows and start
 // (zero rows for a group that fails its check, which is flagged), and the
-// running number of row tiles. Starts must ascend without overlap, so that no
-// row of the output has two writers.
-MOE_DEV void scan_groups(const Args16& p, Shared16& sh, int lane, bool weight_grad) {
+// running number of row tiles (tile_rows rows each; 0: m_tiles for every
+// group). Starts must ascend without overlap, so that no row of the output
+// has two writers.
+MOE_DEV void scan_groups(const Args16& p, Shared16& sh, int lane, int tile_rows) {
   int carry = 0;
   int64_t end = 0;
   if (lane == 0) sh.prefix[0] = 0;
@@ -155,7 +252,8 @@ MOE_DEV void scan_groups(const Args16& p, Shared16& sh, int lane, bool weight_gr
     }
     const int64_t last = __shfl_sync(0xffffffffu, upto, 31);
     if (last > end) end = last;
-    const int mt = weight_grad ? (g < p.n_groups ? p.m_tiles : 0) : (r + kBM - 1) / kBM;
+    const int mt = tile_rows == 0 ? (g < p.n_groups ? p.m_tiles : 0)
+                                  : (r + tile_rows - 1) / tile_rows;
     int incl = mt;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
@@ -176,66 +274,51 @@ MOE_DEV uint32_t pack_f16x2(float lo, float hi) {
   return *reinterpret_cast<const uint32_t*>(&v);
 }
 
-MOE_DEV void unpack16(uint32_t w, bool f16, float& lo, float& hi) {
-  if (f16) {
-    const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&w));
-    lo = f.x;
-    hi = f.y;
-  } else {
-    lo = bf16_lo(w);
-    hi = bf16_hi(w);
-  }
+// ============================================ forward and input gradient
+//
+// kNT: the most rows of a tile (N of the MMA). A group's rows are cut into
+// equal tiles, so that none is nearly empty.
+template <int kCtas, int kNT>
+struct MatCfg {
+  static constexpr int b_bytes = kNT / kCtas * kBK * 2;
+  static constexpr int stage_bytes = kABytes + b_bytes;
+  // a warp's 32 rows x 32 columns of the output, fp32 or 16 bits, with the
+  // rows padded by 16 bytes against bank conflicts
+  static constexpr int turn_bytes = 32 * (32 * 4 + 16);
+  static constexpr int room = 212 * 1024 - 4 * turn_bytes;
+  static constexpr int stages =
+      room / stage_bytes < kMaxStages16 ? room / stage_bytes : kMaxStages16;
+  static constexpr size_t dyn_smem = (size_t)stages * stage_bytes + 4 * turn_bytes + 1024;
+};
+
+struct RowTile {
+  int first, live, cols;  // first row, rows of the group, N of the MMA
+};
+
+// the group's rows in ceil(rows / kNT) tiles of equal size (multiples of 16)
+template <int kNT>
+MOE_DEV RowTile row_tile(int start, int rows, int m) {
+  const int tiles = (rows + kNT - 1) / kNT;
+  const int size = ((rows + tiles - 1) / tiles + 15) & ~15;
+  RowTile t;
+  t.first = start + m * size;
+  t.live = min(size, rows - m * size);
+  t.cols = (max(t.live, 1) + 15) & ~15;
+  return t;
 }
 
-// 8 consecutive output columns of one row; added to what is there first when
-// accumulating
-MOE_DEV void store8(const Args16& p, int64_t at, const float* v) {
-  if (p.out_type == MOE_FP32) {
-    float4* dst = reinterpret_cast<float4*>(static_cast<float*>(p.out) + at);
-    float4 a = make_float4(v[0], v[1], v[2], v[3]), b = make_float4(v[4], v[5], v[6], v[7]);
-    if (p.accumulate) {
-      const float4 c = dst[0], d = dst[1];
-      a.x += c.x; a.y += c.y; a.z += c.z; a.w += c.w;
-      b.x += d.x; b.y += d.y; b.z += d.z; b.w += d.w;
-    }
-    dst[0] = a;
-    dst[1] = b;
-    return;
-  }
-  const bool f16 = p.out_type == MOE_FP16;
-  uint4* dst = reinterpret_cast<uint4*>(static_cast<uint16_t*>(p.out) + at);
-  float o[8];
-#pragma unroll
-  for (int i = 0; i < 8; ++i) o[i] = v[i];
-  if (p.accumulate) {
-    const uint4 c = *dst;
-    const uint32_t w[4] = {c.x, c.y, c.z, c.w};
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      float lo, hi;
-      unpack16(w[i], f16, lo, hi);
-      o[2 * i] += lo;
-      o[2 * i + 1] += hi;
-    }
-  }
-  *dst = f16 ? make_uint4(pack_f16x2(o[0], o[1]), pack_f16x2(o[2], o[3]), pack_f16x2(o[4], o[5]),
-                          pack_f16x2(o[6], o[7]))
-             : make_uint4(pack_bf16x2(o[0], o[1]), pack_bf16x2(o[2], o[3]),
-                          pack_bf16x2(o[4], o[5]), pack_bf16x2(o[6], o[7]));
-}
-
-template <int kWay, int kBN>
-__global__ void __launch_bounds__(kThreads16, 1)
-    grouped16_kernel(const __grid_constant__ CUtensorMap tm_a,
-                     const __grid_constant__ CUtensorMap tm_a32,
-                     const __grid_constant__ CUtensorMap tm_b, const Args16 p) {
-  using C = Tile<kBN>;
-  constexpr bool kWgrad = kWay == kWeightGrad;
+template <int kWay, int kCtas, int kNT>
+__global__ void __cluster_dims__(kCtas, 1, 1) __launch_bounds__(256, 1)
+    grouped_matmul_kernel(const __grid_constant__ CUtensorMap tm_w,
+                          const __grid_constant__ CUtensorMap tm_x,
+                          const __grid_constant__ CUtensorMap tm_x32, const Args16 p) {
+  using C = MatCfg<kCtas, kNT>;
   __shared__ Shared16 sh;
   extern __shared__ uint8_t dyn_smem[];
   const uint32_t ring = (smem_u32(dyn_smem) + 1023u) & ~1023u;
   const int warp = threadIdx.x >> 5;
   const int lane = threadIdx.x & 31;
+  const int rank = kCtas == 1 ? 0 : (int)cluster_rank();
 
   if (threadIdx.x == 0) {
     for (int s = 0; s < C::stages; ++s) {
@@ -244,39 +327,379 @@ __global__ void __launch_bounds__(kThreads16, 1)
     }
     for (int b = 0; b < 2; ++b) {
       mbar_init(smem_u32(&sh.tfull[b]), 1);
-      mbar_init(smem_u32(&sh.tempty[b]), 4);
+      mbar_init(smem_u32(&sh.tempty[b]), 4 * kCtas);
     }
     mbar_init(smem_u32(&sh.drained), 1);
     sh.abort = 0;
     fence_mbar_init();
-    prefetch_tensormap(&tm_a);
-    prefetch_tensormap(&tm_a32);
-    prefetch_tensormap(&tm_b);
+    prefetch_tensormap(&tm_w);
+    prefetch_tensormap(&tm_x);
+    prefetch_tensormap(&tm_x32);
   }
   if (warp == 2) {
-    tmem_alloc(smem_u32(&sh.tmem_base), 2 * kBN);
-    scan_groups(p, sh, lane, kWgrad);
+    alloc16<kCtas>(smem_u32(&sh.tmem_base), 2 * kNT);
+    scan_groups(p, sh, lane, kNT);
   }
   tc_fence_before();
-  __syncthreads();
+  if constexpr (kCtas == 2) cluster_sync();
+  else __syncthreads();
   tc_fence_after();
 
   const uint32_t tmem_base = sh.tmem_base;
-  const int64_t total = (int64_t)sh.prefix[p.n_groups] * p.n_tiles;
+  const int row_tiles = sh.prefix[p.n_groups];
+  const int team = blockIdx.x / kCtas, teams = gridDim.x / kCtas;
+  // Output columns per tile. With few tiles the last round would leave most
+  // CTAs idle: tiles of a smaller height, whose loads overlap their
+  // neighbour's rows in L2, fill it.
+  int height = kBM * kCtas;
+  if (kCtas == 1) {
+    int64_t best = -1;
+    for (int h = kBM; h >= kBM / 2; h -= 8) {
+      const int64_t rounds = ((int64_t)row_tiles * ((p.N + h - 1) / h) + teams - 1) / teams;
+      if (rounds > 8) break;  // an idle share under an eighth
+      if (best < 0 || rounds * h < best) {
+        best = rounds * h;
+        height = h;
+      }
+    }
+  }
+  const int n_tiles = (p.N + height - 1) / height;
+  const int64_t total = (int64_t)row_tiles * n_tiles;
   volatile int* abort = &sh.abort;
+  const int kb_n = p.kblocks;
 
   if (warp == 0) {
     if (lane == 0) {
       // ------------------------------------------------------------ producer
       int it = 0;
       bool ok = true;
-      for (int64_t tile = blockIdx.x; ok && tile < total; tile += gridDim.x) {
+      for (int64_t tile = team; ok && tile < total; tile += teams) {
+        const TileAt t = tile_at((int)tile, sh.prefix, p.n_groups, n_tiles);
+        const RowTile rt = row_tile<kNT>(sh.start[t.g], sh.rows[t.g], t.m);
+        const int half = rt.cols / kCtas;
+        const int pieces = (half + 31) / 32;
+        const bool whole = kNT / kCtas >= 128 && pieces == 4;
+        const int row = rt.first + rank * half;
+        const int n0 = t.n * height + rank * kBM;
+        const uint32_t bytes = kCtas * (kABytes + pieces * 32 * kBK * 2);
+        for (int kb = 0; kb < kb_n; ++kb, ++it) {
+          const int s = it % C::stages;
+          if (!mbar_wait(smem_u32(&sh.empty[s]), ((uint32_t)(it / C::stages) & 1u) ^ 1u, abort,
+                         p.status)) {
+            ok = false;
+            break;
+          }
+          // a pair's loads all count on its first CTA's barrier
+          uint32_t full = smem_u32(&sh.full[s]);
+          if (rank == 0) mbar_arrive_expect_tx(full, bytes);
+          if (kCtas == 2) full = in_leader(full);
+          const uint32_t sa = ring + s * C::stage_bytes, sb = sa + kABytes;
+          if (kWay == kForward) {
+            load_3d<kCtas>(sa, &tm_w, kb * kBK, n0, t.g, full);
+          } else {
+#pragma unroll
+            for (int i = 0; i < kBM / 64; ++i)
+              load_3d<kCtas>(sa + i * kBK * 128, &tm_w, n0 + i * 64, kb * kBK, t.g, full);
+          }
+          if (whole) {
+            load_2d<kCtas>(sb, &tm_x, kb * kBK, row, full);
+          } else {
+            for (int i = 0; i < pieces; ++i)
+              load_2d<kCtas>(sb + i * 32 * kBK * 2, &tm_x32, kb * kBK, row + 32 * i, full);
+          }
+        }
+      }
+      if (!ok && rank == 0) {
+        // drain: every armed stage must land before the CTA may exit
+        for (int s = 0; s < C::stages && s < it; ++s) {
+          const int last = s + ((it - 1 - s) / C::stages) * C::stages;
+          mbar_wait(smem_u32(&sh.full[s]), (uint32_t)(last / C::stages) & 1u, nullptr, p.status);
+        }
+      }
+    }
+  } else if (warp == 1) {
+    if (lane == 0 && rank == 0) {
+      // ------------------------------------------------------------ MMA issuer
+      int it = 0, used = 0;
+      bool ok = true;
+      for (int64_t tile = team; ok && tile < total; tile += teams, ++used) {
+        const TileAt t = tile_at((int)tile, sh.prefix, p.n_groups, n_tiles);
+        const RowTile rt = row_tile<kNT>(sh.start[t.g], sh.rows[t.g], t.m);
+        const uint32_t idesc = p.idesc | ((uint32_t)(rt.cols >> 3) << 17);
+        const int buf = used & 1;
+        ok = mbar_wait(smem_u32(&sh.tempty[buf]), ((uint32_t)(used >> 1) & 1u) ^ 1u, abort, p.status);
+        if (!ok) break;
+        if (kCtas == 2) fence_acquire_cluster();
+        tc_fence_after();
+        const uint32_t d = tmem_base + (uint32_t)(buf * kNT);
+        for (int kb = 0; kb < kb_n; ++kb, ++it) {
+          const int s = it % C::stages;
+          ok = mbar_wait(smem_u32(&sh.full[s]), (uint32_t)(it / C::stages) & 1u, abort, p.status);
+          if (!ok) break;
+          tc_fence_after();
+          const uint32_t sa = ring + s * C::stage_bytes;
+          const uint64_t da = kWay == kForward ? smem_desc_sw128(sa) : smem_desc_mn_sw128(sa);
+          const uint64_t db = smem_desc_sw128(sa + kABytes);
+          constexpr uint64_t step_a = kWay == kForward ? kStepK : kStepMN;
+#pragma unroll
+          for (int i = 0; i < kBK / 16; ++i)
+            mma16<kCtas>(d, da + step_a * i, db + kStepK * i, idesc, (kb | i) > 0 ? 1u : 0u);
+          commit16<kCtas>(smem_u32(&sh.empty[s]));
+        }
+        if (ok) commit16<kCtas>(smem_u32(&sh.tfull[buf]));
+      }
+      if (!ok && it > 0) {
+        // every issued MMA has completed before TMEM is released
+        commit16<kCtas>(smem_u32(&sh.drained));
+        mbar_wait(smem_u32(&sh.drained), 0u, nullptr, p.status);
+      }
+    }
+  } else if (warp >= 4) {
+    // -------------------------------------------------------------- epilogue
+    const int quarter = warp & 3;  // TMEM lanes 32 * quarter .. = output columns
+    const uint32_t lane_addr = tmem_base + ((uint32_t)(quarter * 32) << 16);
+    const uint32_t turn = ring + (uint32_t)(C::stages * C::stage_bytes + quarter * C::turn_bytes);
+    const bool wide = p.out_type == MOE_FP32;
+    const bool f16 = p.out_type == MOE_FP16;
+    const int es = wide ? 4 : 2;
+    const int pitch = 32 * es + 16;
+    const int per_row = 32 * es / 16;  // 16-byte pieces of a row's 32 columns
+    const int piece = lane % per_row, row0 = lane / per_row, row_step = 32 / per_row;
+    int used = 0;
+    for (int64_t tile = team; tile < total; tile += teams, ++used) {
+      const TileAt t = tile_at((int)tile, sh.prefix, p.n_groups, n_tiles);
+      const RowTile rt = row_tile<kNT>(sh.start[t.g], sh.rows[t.g], t.m);
+      const int buf = used & 1;
+      if (!__all_sync(0xffffffffu, mbar_wait(smem_u32(&sh.tfull[buf]), (uint32_t)(used >> 1) & 1u,
+                                             abort, p.status)))
+        break;
+      tc_fence_after();
+      // this tile's output columns end where the next tile's begin
+      const int n0 = t.n * height + rank * kBM + quarter * 32;
+      const int n_end = min(t.n * height + height, p.N);
+      const int n = n0 + piece * (16 / es);
+      uint8_t* const out = static_cast<uint8_t*>(p.out) + ((int64_t)rt.first * p.N + n) * es;
+      for (int c = 0; c < rt.live; c += 32) {
+        float v[32];
+        tmem_ld32(lane_addr + (uint32_t)(buf * kNT + c), v);
+        tmem_wait_ld();
+        if (n0 >= n_end) continue;
+        if (wide) {
+#pragma unroll
+          for (int j = 0; j < 32; ++j)
+            asm volatile("st.shared.f32 [%0], %1;" ::"r"(turn + j * pitch + lane * 4), "f"(v[j])
+                         : "memory");
+        } else {
+#pragma unroll
+          for (int j = 0; j < 32; j += 2) {
+            const uint32_t w = f16 ? pack_f16x2(v[j], v[j + 1]) : pack_bf16x2(v[j], v[j + 1]);
+            asm volatile("st.shared.u16 [%0], %1;" ::"r"(turn + j * pitch + lane * 2),
+                         "h"((uint16_t)w)
+                         : "memory");
+            asm volatile("st.shared.u16 [%0], %1;" ::"r"(turn + (j + 1) * pitch + lane * 2),
+                         "h"((uint16_t)(w >> 16))
+                         : "memory");
+          }
+        }
+        __syncwarp();
+        if (n < n_end) {
+          for (int j = row0; j < 32 && c + j < rt.live; j += row_step) {
+            uint32_t q[4];
+            asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];"
+                         : "=r"(q[0]), "=r"(q[1]), "=r"(q[2]), "=r"(q[3])
+                         : "r"(turn + j * pitch + piece * 16)
+                         : "memory");
+            *reinterpret_cast<uint4*>(out + (int64_t)(c + j) * p.N * es) =
+                make_uint4(q[0], q[1], q[2], q[3]);
+          }
+        }
+        __syncwarp();
+      }
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) {
+        if (kCtas == 2) mbar_arrive_cluster(in_leader(smem_u32(&sh.tempty[buf])));
+        else mbar_arrive(smem_u32(&sh.tempty[buf]));
+      }
+    }
+  }
+
+  tc_fence_before();
+  if constexpr (kCtas == 2) cluster_sync();
+  else __syncthreads();
+  tc_fence_after();
+  if (warp == 2) dealloc16<kCtas>(tmem_base, 2 * kNT);
+}
+
+// ====================================================== weight gradient
+//
+// dw_g = dy_g^T x_g: both operands MN-major, the reduction over the group's
+// rows. The tensor core's fp32 sums lose about half a unit in the last place
+// per step, always towards zero, which grows with the rows of a group (5.6e-7
+// of the result at 512 rows, 7e-5 at 65536); so the sums are taken over at
+// most 512 rows and added up in registers, rounded to nearest.
+constexpr int kSegment = 8;  // k-blocks per TMEM sum
+constexpr int kWThreads = 384;
+constexpr int kWRegsLaunch = 168, kWRegsCtl = 40, kWRegsEpi = 232;
+static_assert(128 * kWRegsCtl + 256 * kWRegsEpi <= kWThreads * kWRegsLaunch, "register split");
+
+template <int kCtas, int kBN>
+struct WgCfg {
+  static constexpr int b_bytes = kBN / kCtas * kBK * 2;
+  static constexpr int stage_bytes = kABytes + b_bytes;
+  static constexpr int buf_bytes = 32 * 128;  // a warp's 32 rows x 128 bytes
+  static constexpr int room = 208 * 1024 - 8 * 2 * buf_bytes;
+  static constexpr int stages = room / stage_bytes < 6 ? room / stage_bytes : 6;
+  static constexpr size_t dyn_smem = (size_t)stages * stage_bytes + 8 * 2 * buf_bytes + 1024;
+};
+
+MOE_DEV void store_3d(const CUtensorMap* map, uint32_t src, int32_t x, int32_t y, int32_t z,
+                      bool add) {
+  if (add)
+    asm volatile(
+        "cp.reduce.async.bulk.tensor.3d.global.shared::cta.add.tile.bulk_group"
+        " [%0, {%2, %3, %4}], [%1];" ::"l"(reinterpret_cast<uint64_t>(map)),
+        "r"(src), "r"(x), "r"(y), "r"(z)
+        : "memory");
+  else
+    asm volatile(
+        "cp.async.bulk.tensor.3d.global.shared::cta.tile.bulk_group [%0, {%2, %3, %4}], [%1];" ::"l"(
+            reinterpret_cast<uint64_t>(map)),
+        "r"(src), "r"(x), "r"(y), "r"(z)
+        : "memory");
+}
+
+// 32 consecutive columns of a warp's 32 rows (one row a lane) of dw, out
+// through shared memory and a TMA store that clips at dw's edges; 16-bit
+// outputs gather two calls' 32 columns in one 128-byte row.
+struct DwOut {
+  const CUtensorMap* map;
+  uint32_t buf;
+  int turn;
+  MOE_DEV void put(const Args16& p, const float (&v)[32], int x, int y, int g, int lane) {
+    const bool wide = p.out_type == MOE_FP32;
+    const uint32_t swz = (uint32_t)(lane & 7);
+    const int part = wide ? 0 : (x >> 5) & 1;  // which half of the 128-byte row
+    if (part == 0) {
+      if (lane == 0) bulk_wait_read_1();  // the store that last read this buffer is done
+      __syncwarp();
+    }
+    const uint32_t row = buf + (uint32_t)(turn * 32 * 128 + lane * 128);
+    if (wide) {
+#pragma unroll
+      for (int c = 0; c < 8; ++c)
+        asm volatile("st.shared.v4.f32 [%0], {%1, %2, %3, %4};" ::"r"(row + (((uint32_t)c ^ swz) << 4)),
+                     "f"(v[4 * c]), "f"(v[4 * c + 1]), "f"(v[4 * c + 2]), "f"(v[4 * c + 3])
+                     : "memory");
+    } else {
+      const bool f16 = p.out_type == MOE_FP16;
+#pragma unroll
+      for (int c = 0; c < 4; ++c) {
+        uint32_t w[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+          w[i] = f16 ? pack_f16x2(v[8 * c + 2 * i], v[8 * c + 2 * i + 1])
+                     : pack_bf16x2(v[8 * c + 2 * i], v[8 * c + 2 * i + 1]);
+        asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(
+                         row + (((uint32_t)(4 * part + c) ^ swz) << 4)),
+                     "r"(w[0]), "r"(w[1]), "r"(w[2]), "r"(w[3])
+                     : "memory");
+      }
+    }
+    if (wide || part == 1) {
+      fence_proxy_async_smem();
+      __syncwarp();
+      if (lane == 0) {
+        store_3d(map, buf + (uint32_t)(turn * 32 * 128), wide ? x : x - 32, y, g, p.accumulate != 0);
+        bulk_commit();
+      }
+      turn ^= 1;
+    }
+  }
+};
+
+// 32 consecutive columns of one row added to the 16-bit values there, rounded
+// once (a TMA add would round the addend first)
+MOE_DEV void add16(const Args16& p, const float (&v)[32], int x, int64_t at, bool live) {
+  const bool f16 = p.out_type == MOE_FP16;
+#pragma unroll
+  for (int c = 0; c < 4; ++c) {
+    if (!live || x + 8 * c >= p.N) continue;
+    uint4* dst = reinterpret_cast<uint4*>(static_cast<uint16_t*>(p.out) + at + 8 * c);
+    const uint4 q = *dst;
+    uint32_t w[4] = {q.x, q.y, q.z, q.w};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      float lo = bf16_lo(w[i]), hi = bf16_hi(w[i]);
+      if (f16) {
+        const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&w[i]));
+        lo = f.x;
+        hi = f.y;
+      }
+      lo += v[8 * c + 2 * i];
+      hi += v[8 * c + 2 * i + 1];
+      w[i] = f16 ? pack_f16x2(lo, hi) : pack_bf16x2(lo, hi);
+    }
+    *dst = make_uint4(w[0], w[1], w[2], w[3]);
+  }
+}
+
+template <int kCtas, int kBN>
+__global__ void __cluster_dims__(kCtas, 1, 1) __launch_bounds__(kWThreads, 1)
+    grouped_wgrad_kernel(const __grid_constant__ CUtensorMap tm_a,
+                         const __grid_constant__ CUtensorMap tm_b,
+                         const __grid_constant__ CUtensorMap tm_out, const Args16 p) {
+  using C = WgCfg<kCtas, kBN>;
+  constexpr int kHalf = kBN / kCtas;     // columns of x this CTA loads
+  constexpr int kEpiCols = kBN / 2;      // accumulator columns of an epilogue warp
+  __shared__ Shared16 sh;
+  extern __shared__ uint8_t dyn_smem[];
+  const uint32_t ring = (smem_u32(dyn_smem) + 1023u) & ~1023u;
+  const int warp = threadIdx.x >> 5;
+  const int lane = threadIdx.x & 31;
+  const int rank = kCtas == 1 ? 0 : (int)cluster_rank();
+
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < C::stages; ++s) {
+      mbar_init(smem_u32(&sh.full[s]), 1);
+      mbar_init(smem_u32(&sh.empty[s]), 1);
+      mbar_init(smem_u32(&sh.ready[s]), kCtas);
+    }
+    for (int b = 0; b < 2; ++b) {
+      mbar_init(smem_u32(&sh.tfull[b]), 1);
+      mbar_init(smem_u32(&sh.tempty[b]), 8 * kCtas);
+    }
+    mbar_init(smem_u32(&sh.drained), 1);
+    sh.abort = 0;
+    fence_mbar_init();
+    prefetch_tensormap(&tm_a);
+    prefetch_tensormap(&tm_b);
+    prefetch_tensormap(&tm_out);
+  }
+  if (warp == 2) {
+    alloc16<kCtas>(smem_u32(&sh.tmem_base), 2 * kBN);
+    scan_groups(p, sh, lane, 0);
+  }
+  tc_fence_before();
+  if constexpr (kCtas == 2) cluster_sync();
+  else __syncthreads();
+  tc_fence_after();
+
+  const uint32_t tmem_base = sh.tmem_base;
+  const int team = blockIdx.x / kCtas, teams = gridDim.x / kCtas;
+  const int64_t total = (int64_t)sh.prefix[p.n_groups] * p.n_tiles;
+  volatile int* abort = &sh.abort;
+
+  if (warp < 4) asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kWRegsCtl));
+  if (warp == 0) {
+    if (lane == 0) {
+      // ------------------------------------------------------------ producer
+      int it = 0;
+      bool ok = true;
+      for (int64_t tile = team; ok && tile < total; tile += teams) {
         const TileAt t = tile_at((int)tile, sh.prefix, p.n_groups, p.n_tiles);
-        const int rows = sh.rows[t.g], start = sh.start[t.g];
-        const int kb_n = kWgrad ? (rows + kBK - 1) / kBK : p.kblocks;
-        const int live = rows - t.m * kBM;
-        const int pieces = live > 96 ? 4 : (live + 31) / 32;
-        const uint32_t bytes = (kWgrad ? kABytes : pieces * (kABytes / 4)) + C::b_bytes;
+        const int kb_n = (sh.rows[t.g] + kBK - 1) / kBK;
+        const int a0 = (t.m * kCtas + rank) * kBM, b0 = t.n * kBN + rank * kHalf;
         for (int kb = 0; kb < kb_n; ++kb, ++it) {
           const int s = it % C::stages;
           if (!mbar_wait(smem_u32(&sh.empty[s]), ((uint32_t)(it / C::stages) & 1u) ^ 1u, abort,
@@ -285,32 +708,13 @@ __global__ void __launch_bounds__(kThreads16, 1)
             break;
           }
           const uint32_t full = smem_u32(&sh.full[s]);
-          mbar_arrive_expect_tx(full, bytes);
+          mbar_arrive_expect_tx(full, C::stage_bytes);
           const uint32_t sa = ring + s * C::stage_bytes, sb = sa + kABytes;
-          if (kWgrad) {
-            const int r = start + kb * kBK;
+          const int r = sh.start[t.g] + kb * kBK;
 #pragma unroll
-            for (int i = 0; i < kBM / 64; ++i)
-              tma_load_2d(sa + i * kBK * 128, &tm_a, t.m * kBM + i * 64, r, full);
+          for (int i = 0; i < kBM / 64; ++i) tma_load_2d(sa + i * kBK * 128, &tm_a, a0 + i * 64, r, full);
 #pragma unroll
-            for (int i = 0; i < kBN / 64; ++i)
-              tma_load_2d(sb + i * kBK * 128, &tm_b, t.n * kBN + i * 64, r, full);
-          } else {
-            const int r = start + t.m * kBM;
-            if (pieces == 4) {
-              tma_load_2d(sa, &tm_a, kb * kBK, r, full);
-            } else {
-              for (int i = 0; i < pieces; ++i)
-                tma_load_2d(sa + i * (kABytes / 4), &tm_a32, kb * kBK, r + 32 * i, full);
-            }
-            if (kWay == kForward) {
-              tma_load_3d(sb, &tm_b, kb * kBK, t.n * kBN, t.g, full);
-            } else {
-#pragma unroll
-              for (int i = 0; i < kBN / 64; ++i)
-                tma_load_3d(sb + i * kBK * 128, &tm_b, t.n * kBN + i * 64, kb * kBK, t.g, full);
-            }
-          }
+          for (int i = 0; i < kHalf / 64; ++i) tma_load_2d(sb + i * kBK * 128, &tm_b, b0 + i * 64, r, full);
         }
       }
       if (!ok) {
@@ -321,138 +725,214 @@ __global__ void __launch_bounds__(kThreads16, 1)
         }
       }
     }
-  } else if (warp == 1) {
-    // -------------------------------------------------------------- MMA issuer
-    int it = 0, used = 0;
+  } else if (warp == 3) {
+    // ---------------------------------------------- rows behind a group cleared
+    int it = 0;
     bool ok = true;
-    for (int64_t tile = blockIdx.x; ok && tile < total; tile += gridDim.x) {
+    for (int64_t tile = team; ok && tile < total; tile += teams) {
       const TileAt t = tile_at((int)tile, sh.prefix, p.n_groups, p.n_tiles);
       const int rows = sh.rows[t.g];
-      const int kb_n = kWgrad ? (rows + kBK - 1) / kBK : p.kblocks;
-      if (kb_n == 0) continue;
-      const int buf = used & 1;
-      ok = __all_sync(0xffffffffu, mbar_wait(smem_u32(&sh.tempty[buf]),
-                                             ((uint32_t)(used >> 1) & 1u) ^ 1u, abort, p.status));
-      if (!ok) break;
-      tc_fence_after();
-      const uint32_t d = tmem_base + (uint32_t)(buf * kBN);
+      const int kb_n = (rows + kBK - 1) / kBK;
       for (int kb = 0; kb < kb_n; ++kb, ++it) {
         const int s = it % C::stages;
         ok = __all_sync(0xffffffffu, mbar_wait(smem_u32(&sh.full[s]),
                                                (uint32_t)(it / C::stages) & 1u, abort, p.status));
         if (!ok) break;
-        tc_fence_after();
-        const uint32_t sa = ring + s * C::stage_bytes, sb = sa + kABytes;
-        int steps = kBK / 16;
-        if (kWgrad && rows - kb * kBK < kBK) {
-          // rows beyond the group, up to the next 16-row step: cleared in
-          // every 64-column box (a swizzled row stays within its 128 bytes)
-          const int live = rows - kb * kBK;
-          steps = (live + 15) / 16;
-          const int dead = steps * 16 - live;
-          for (int i = lane; i < dead * 8 * (kBM + kBN) / 64; i += 32) {
+        const int live = rows - kb * kBK;
+        if (live < kBK) {
+          // up to the next 16-row step, in every 64-column box (a swizzled
+          // row stays within its 128 bytes)
+          const uint32_t sa = ring + s * C::stage_bytes;
+          const int dead = ((live + 15) & ~15) - live;
+          for (int i = lane; i < dead * 8 * (kBM + kHalf) / 64; i += 32) {
             const int box = i / (dead * 8), q = i - box * dead * 8;
             asm volatile("st.shared.v4.b32 [%0], {%1, %1, %1, %1};" ::"r"(
                              sa + (uint32_t)(box * kBK * 128 + live * 128 + q * 16)),
                          "r"(0)
                          : "memory");
           }
-          fence_proxy_async_smem();
-          __syncwarp();
         }
-        if (lane == 0) {
-          const uint64_t da = kWgrad ? smem_desc_mn_sw128(sa) : smem_desc_sw128(sa);
-          const uint64_t db = kWay == kForward ? smem_desc_sw128(sb) : smem_desc_mn_sw128(sb);
-          constexpr uint64_t step_a = kWgrad ? 2048 >> 4 : 32 >> 4;
-          constexpr uint64_t step_b = kWay == kForward ? 32 >> 4 : 2048 >> 4;
-          for (int i = 0; i < steps; ++i)
-            mma_bf16(d, da + step_a * i, db + step_b * i, p.idesc, (kb | i) > 0 ? 1u : 0u);
-          mma_commit(smem_u32(&sh.empty[s]));
-          if (kb == kb_n - 1) mma_commit(smem_u32(&sh.tfull[buf]));
-        }
+        fence_proxy_async_smem();
         __syncwarp();
+        if (lane == 0) {
+          if (kCtas == 2) mbar_arrive_cluster(in_leader(smem_u32(&sh.ready[s])));
+          else mbar_arrive(smem_u32(&sh.ready[s]));
+        }
       }
-      ++used;
     }
-    if (!ok && it > 0 && lane == 0) {
-      // every issued MMA has completed before TMEM is released
-      mma_commit(smem_u32(&sh.drained));
-      mbar_wait(smem_u32(&sh.drained), 0u, nullptr, p.status);
+  } else if (warp == 1) {
+    if (lane == 0 && rank == 0) {
+      // ------------------------------------------------------------ MMA issuer
+      int it = 0, used = 0;
+      bool ok = true;
+      for (int64_t tile = team; ok && tile < total; tile += teams) {
+        const TileAt t = tile_at((int)tile, sh.prefix, p.n_groups, p.n_tiles);
+        const int rows = sh.rows[t.g];
+        const int kb_n = (rows + kBK - 1) / kBK;
+        for (int kb = 0; kb < kb_n; ++kb, ++it) {
+          const int buf = used & 1;
+          if (kb % kSegment == 0) {
+            ok = mbar_wait(smem_u32(&sh.tempty[buf]), ((uint32_t)(used >> 1) & 1u) ^ 1u, abort,
+                           p.status);
+            if (!ok) break;
+            if (kCtas == 2) fence_acquire_cluster();
+            tc_fence_after();
+          }
+          const uint32_t d = tmem_base + (uint32_t)(buf * kBN);
+          const int s = it % C::stages;
+          ok = mbar_wait(smem_u32(&sh.ready[s]), (uint32_t)(it / C::stages) & 1u, abort, p.status);
+          if (!ok) break;
+          if (kCtas == 2) fence_acquire_cluster();
+          tc_fence_after();
+          const uint32_t sa = ring + s * C::stage_bytes;
+          const uint64_t da = smem_desc_mn_sw128(sa), db = smem_desc_mn_sw128(sa + kABytes);
+          const int steps = (min(rows - kb * kBK, kBK) + 15) / 16;
+          for (int i = 0; i < steps; ++i)
+            mma16<kCtas>(d, da + kStepMN * i, db + kStepMN * i, p.idesc,
+                         (kb % kSegment) > 0 || i > 0 ? 1u : 0u);
+          commit16<kCtas>(smem_u32(&sh.empty[s]));
+          if (kb % kSegment == kSegment - 1 || kb == kb_n - 1) {
+            commit16<kCtas>(smem_u32(&sh.tfull[buf]));
+            ++used;
+          }
+        }
+      }
+      if (!ok && it > 0) {
+        // every issued MMA has completed before TMEM is released
+        commit16<kCtas>(smem_u32(&sh.drained));
+        mbar_wait(smem_u32(&sh.drained), 0u, nullptr, p.status);
+      }
     }
   } else if (warp >= 4) {
     // -------------------------------------------------------------- epilogue
-    const int quarter = warp & 3;  // TMEM lanes 32 * quarter ..
-    const int row = quarter * 32 + lane;
-    const uint32_t lane_addr = tmem_base + ((uint32_t)(quarter * 32) << 16);
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kWRegsEpi));
+    const int ew = warp - 4;
+    const int quarter = warp & 3;  // TMEM lanes 32 * quarter .. = rows of dw
+    const int c0 = (ew >> 2) * kEpiCols;
+    const uint32_t lane_addr = tmem_base + ((uint32_t)(quarter * 32) << 16) + (uint32_t)c0;
+    DwOut out{&tm_out, ring + (uint32_t)(C::stages * C::stage_bytes + ew * 2 * C::buf_bytes), 0};
+    const bool direct = p.accumulate && p.out_type != MOE_FP32;
     int used = 0;
-    for (int64_t tile = blockIdx.x; tile < total; tile += gridDim.x) {
+    bool ok = true;
+    for (int64_t tile = team; ok && tile < total; tile += teams) {
       const TileAt t = tile_at((int)tile, sh.prefix, p.n_groups, p.n_tiles);
-      const int rows = sh.rows[t.g];
-      const bool empty = kWgrad && rows == 0;
-      if (empty && p.accumulate) continue;
-      const int buf = used & 1;
-      if (!empty) {
-        if (!__all_sync(0xffffffffu, mbar_wait(smem_u32(&sh.tfull[buf]),
-                                               (uint32_t)(used >> 1) & 1u, abort, p.status)))
-          break;
-        tc_fence_after();
-      }
-      const int in_group = t.m * kBM + row;
-      const bool live = in_group < (kWgrad ? p.M : rows);
-      const int64_t out_row = kWgrad ? (int64_t)t.g * p.M + in_group
-                                     : (int64_t)sh.start[t.g] + in_group;
-      const int cols = min(kBN, p.N - t.n * kBN);
-      const int64_t at = out_row * p.N + (int64_t)t.n * kBN;
-      for (int c = 0; c < cols; c += 32) {
-        float v[32];
-        if (empty) {
-#pragma unroll
-          for (int i = 0; i < 32; ++i) v[i] = 0.0f;
-        } else {
-          tmem_ld32(lane_addr + (uint32_t)(buf * kBN + c), v);
-          tmem_wait_ld();
-        }
-        if (live) {
-#pragma unroll
-          for (int j = 0; j < 4; ++j)
-            if (c + 8 * j < cols) store8(p, at + c + 8 * j, v + 8 * j);
-        }
-        __syncwarp();
-      }
-      if (!empty) {
+      const int kb_n = (sh.rows[t.g] + kBK - 1) / kBK;
+      if (kb_n == 0 && p.accumulate) continue;
+      const int segments = (kb_n + kSegment - 1) / kSegment;
+      const int y = (t.m * kCtas + rank) * kBM + quarter * 32, x0 = t.n * kBN + c0;
+      auto emit = [&](const float (&v)[32], int c) {
+        const int x = x0 + c;
+        // a 16-bit row is stored when its second half is in: beyond the last
+        // column both halves are skipped, or neither
+        if (y >= p.M || (p.out_type == MOE_FP32 ? x : x & ~63) >= p.N) return;
+        if (direct)
+          add16(p, v, x, ((int64_t)t.g * p.M + y + lane) * p.N + x, y + lane < p.M);
+        else
+          out.put(p, v, x, y, t.g, lane);
+      };
+      auto wait_segment = [&] {
+        ok = __all_sync(0xffffffffu, mbar_wait(smem_u32(&sh.tfull[used & 1]),
+                                               (uint32_t)(used >> 1) & 1u, abort, p.status));
+        if (ok) tc_fence_after();
+        return ok;
+      };
+      auto release_segment = [&] {
         tc_fence_before();
         __syncwarp();
-        if (lane == 0) mbar_arrive(smem_u32(&sh.tempty[buf]));
+        if (lane == 0) {
+          const uint32_t bar = smem_u32(&sh.tempty[used & 1]);
+          if (kCtas == 2) mbar_arrive_cluster(in_leader(bar));
+          else mbar_arrive(bar);
+        }
         ++used;
+      };
+      if (segments <= 1) {
+        if (segments == 1 && !wait_segment()) break;
+#pragma unroll 1
+        for (int c = 0; c < kEpiCols; c += 32) {
+          float v[32];
+          if (segments == 1) {
+            tmem_ld32(lane_addr + (uint32_t)((used & 1) * kBN + c), v);
+            tmem_wait_ld();
+          } else {
+#pragma unroll
+            for (int i = 0; i < 32; ++i) v[i] = 0.0f;
+          }
+          emit(v, c);
+        }
+        if (segments == 1) release_segment();
+      } else {
+        float sum[kEpiCols / 32][32];
+        for (int seg = 0; seg < segments; ++seg) {
+          if (!wait_segment()) break;
+#pragma unroll
+          for (int c = 0; c < kEpiCols / 32; ++c) {
+            float v[32];
+            tmem_ld32(lane_addr + (uint32_t)((used & 1) * kBN + 32 * c), v);
+            tmem_wait_ld();
+#pragma unroll
+            for (int i = 0; i < 32; ++i) sum[c][i] = seg == 0 ? v[i] : sum[c][i] + v[i];
+          }
+          release_segment();
+        }
+        if (!ok) break;
+#pragma unroll
+        for (int c = 0; c < kEpiCols / 32; ++c) emit(sum[c], 32 * c);
       }
     }
+    if (lane == 0) bulk_wait_all();
   }
 
   tc_fence_before();
-  __syncthreads();
+  if constexpr (kCtas == 2) cluster_sync();
+  else __syncthreads();
   tc_fence_after();
-  if (warp == 2) tmem_dealloc(tmem_base, 2 * kBN);
+  if (warp == 2) dealloc16<kCtas>(tmem_base, 2 * kBN);
 }
 
-template <int kWay, int kBN>
-cudaError_t launch16(const Args16& a, const CUtensorMap& ma, const CUtensorMap& ma32,
-                     const CUtensorMap& mb, int64_t tile_bound, cudaStream_t stream, int sms) {
+// ================================================================ launches
+template <int kWay, int kCtas, int kNT>
+cudaError_t launch_mat(Args16 a, const CUtensorMap& mw, const CUtensorMap& mx,
+                       const CUtensorMap& mx32, int64_t row_tiles, cudaStream_t stream, int sms) {
+  using C = MatCfg<kCtas, kNT>;
   static DeviceOnce once;
   cudaError_t e = once.run([] {
-    return cudaFuncSetAttribute(grouped16_kernel<kWay, kBN>,
-                                cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                (int)Tile<kBN>::dyn_smem);
+    return cudaFuncSetAttribute(grouped_matmul_kernel<kWay, kCtas, kNT>,
+                                cudaFuncAttributeMaxDynamicSharedMemorySize, (int)C::dyn_smem);
   });
   if (e != cudaSuccess) return e;
-  if (tile_bound <= 0) return cudaSuccess;
-  const int grid = (int)(tile_bound < sms ? tile_bound : sms);
-  grouped16_kernel<kWay, kBN><<<grid, kThreads16, Tile<kBN>::dyn_smem, stream>>>(ma, ma32, mb, a);
+  a.idesc = make_idesc(kBM * kCtas, 0, a.idesc, a.idesc) | (kWay == kInputGrad ? 1u << 15 : 0u);
+  // tiles of half height at the least
+  const int64_t tiles = row_tiles * ((a.N + kBM / 2 - 1) / (kBM / 2));
+  if (tiles >= (1ll << 31)) return cudaErrorInvalidValue;
+  const int64_t grid = tiles * kCtas < sms ? tiles * kCtas : sms / kCtas * kCtas;
+  grouped_matmul_kernel<kWay, kCtas, kNT><<<(unsigned)grid, 256, C::dyn_smem, stream>>>(mw, mx, mx32, a);
   return cudaGetLastError();
 }
 
-uint32_t idesc16(int bn, bool f16, bool a_mn, bool b_mn) {
-  const uint32_t fmt = f16 ? 0u : 1u;
-  return make_idesc(kBM, bn, fmt, fmt) | (a_mn ? 1u << 15 : 0u) | (b_mn ? 1u << 16 : 0u);
+template <int kCtas, int kBN>
+cudaError_t launch_wg(Args16 a, const CUtensorMap& ma, const CUtensorMap& mb,
+                      const CUtensorMap& mo, cudaStream_t stream, int sms) {
+  using C = WgCfg<kCtas, kBN>;
+  static DeviceOnce once;
+  cudaError_t e = once.run([] {
+    // the register split is only safe if the kernel was built for it
+    cudaFuncAttributes fa;
+    cudaError_t r = cudaFuncGetAttributes(&fa, grouped_wgrad_kernel<kCtas, kBN>);
+    if (r != cudaSuccess) return r;
+    if (fa.numRegs != kWRegsLaunch) return cudaErrorInvalidConfiguration;
+    return cudaFuncSetAttribute(grouped_wgrad_kernel<kCtas, kBN>,
+                                cudaFuncAttributeMaxDynamicSharedMemorySize, (int)C::dyn_smem);
+  });
+  if (e != cudaSuccess) return e;
+  a.m_tiles = (a.M + kBM * kCtas - 1) / (kBM * kCtas);
+  a.n_tiles = (a.N + kBN - 1) / kBN;
+  a.idesc = make_idesc(kBM * kCtas, kBN, a.idesc, a.idesc) | 1u << 15 | 1u << 16;
+  const int64_t tiles = (int64_t)a.n_groups * a.m_tiles * a.n_tiles;
+  if (tiles >= (1ll << 31)) return cudaErrorInvalidValue;
+  const int64_t grid = tiles * kCtas < sms ? tiles * kCtas : sms / kCtas * kCtas;
+  grouped_wgrad_kernel<kCtas, kBN><<<(unsigned)grid, kWThreads, C::dyn_smem, stream>>>(ma, mb, mo, a);
+  return cudaGetLastError();
 }
 
 }  // namespace
@@ -470,32 +950,27 @@ cudaError_t launch_grouped_matmul(const Groups16& gr, bool f16, int out_type, in
   p.N = N;
   p.out = out;
   p.out_type = out_type;
+  p.idesc = f16 ? 0u : 1u;
   p.status = gr.status;
-  CUtensorMap ma, ma32, mb;
-  cudaError_t e = make_tmap_bf16(&ma, a, K, gr.rows, 1, kBK, kBM);
-  if (e == cudaSuccess) e = make_tmap_bf16(&ma32, a, K, gr.rows, 1, kBK, 32);
+  CUtensorMap mw, mx, mx32;
+  cudaError_t e = make_tmap_bf16(&mx, a, K, gr.rows, 1, kBK, kBM);
+  if (e == cudaSuccess) e = make_tmap_bf16(&mx32, a, K, gr.rows, 1, kBK, 32);
+  if (e == cudaSuccess)
+    e = trans_b ? make_tmap_16b_3d(&mw, b, K, N, gr.n_groups, kBK, kBM)
+                : make_tmap_16b_3d(&mw, b, N, K, gr.n_groups, 64, kBK);
   if (e != cudaSuccess) return e;
-  // the row tiles there can be: every full one, and a partial one per group
-  const int64_t m_bound = gr.rows / kBM + (gr.rows < gr.n_groups ? gr.rows : gr.n_groups);
-  auto go = [&](auto bn_tag, auto launch_fwd, auto launch_dx) {
-    constexpr int bn = decltype(bn_tag)::value;
-    p.n_tiles = (N + bn - 1) / bn;
-    p.idesc = idesc16(bn, f16, false, !trans_b);
-    e = trans_b ? make_tmap_16b_3d(&mb, b, K, N, gr.n_groups, kBK, bn)
-                : make_tmap_16b_3d(&mb, b, N, K, gr.n_groups, 64, kBK);
-    if (e != cudaSuccess) return e;
-    const int64_t bound = m_bound * p.n_tiles;
-    if (bound >= (1ll << 31)) return cudaErrorInvalidValue;
-    return trans_b ? launch_fwd(bound) : launch_dx(bound);
+  const int64_t busy = gr.rows < gr.n_groups ? gr.rows : gr.n_groups;
+  const int64_t each = gr.rows / busy;  // rows of a group, if they were alike
+  auto go = [&](auto ctas, auto nt) {
+    constexpr int kCtas = decltype(ctas)::value, kNT = decltype(nt)::value;
+    const int64_t row_tiles = gr.rows / kNT + busy;
+    return trans_b ? launch_mat<kForward, kCtas, kNT>(p, mw, mx, mx32, row_tiles, stream, sms)
+                   : launch_mat<kInputGrad, kCtas, kNT>(p, mw, mx, mx32, row_tiles, stream, sms);
   };
-#define MOE_GO(BN)                                                                        \
-  go(std::integral_constant<int, BN>{},                                                   \
-     [&](int64_t t) { return launch16<kForward, BN>(p, ma, ma32, mb, t, stream, sms); },  \
-     [&](int64_t t) { return launch16<kInputGrad, BN>(p, ma, ma32, mb, t, stream, sms); })
-  if (m_bound * ((N + 255) / 256) >= 4 * sms) return MOE_GO(256);
-  if (m_bound * ((N + 127) / 128) >= 4 * sms) return MOE_GO(128);
-  return MOE_GO(64);
-#undef MOE_GO
+  using std::integral_constant;
+  if (each > 160 && N > kBM) return go(integral_constant<int, 2>{}, integral_constant<int, 256>{});
+  if (each > 24) return go(integral_constant<int, 1>{}, integral_constant<int, 128>{});
+  return go(integral_constant<int, 1>{}, integral_constant<int, 32>{});
 }
 
 cudaError_t launch_grouped_wgrad(const Groups16& gr, bool f16, int out_type, int N, int K,
@@ -508,27 +983,22 @@ cudaError_t launch_grouped_wgrad(const Groups16& gr, bool f16, int out_type, int
   p.rows = gr.rows;
   p.M = N;
   p.N = K;
-  p.m_tiles = (N + kBM - 1) / kBM;
   p.out = dw;
   p.out_type = out_type;
   p.accumulate = accumulate ? 1 : 0;
+  p.idesc = f16 ? 0u : 1u;
   p.status = gr.status;
-  CUtensorMap ma, mb;
+  CUtensorMap ma, mb, mo;
   // without rows nothing is loaded, and the row buffers may be NULL
   cudaError_t e = make_tmap_bf16(&ma, gr.rows > 0 ? dy : dw, N, gr.rows, 1, 64, kBK);
   if (e == cudaSuccess) e = make_tmap_bf16(&mb, gr.rows > 0 ? x : dw, K, gr.rows, 1, 64, kBK);
+  if (e == cudaSuccess)
+    e = out_type == MOE_FP32 ? make_tmap_f32_3d(&mo, dw, K, N, gr.n_groups, 32, 32)
+                             : make_tmap_16b_3d(&mo, dw, K, N, gr.n_groups, 64, 32);
   if (e != cudaSuccess) return e;
-  const int64_t m_all = (int64_t)gr.n_groups * p.m_tiles;
-  auto go = [&](auto bn_tag) {
-    constexpr int bn = decltype(bn_tag)::value;
-    p.n_tiles = (K + bn - 1) / bn;
-    p.idesc = idesc16(bn, f16, true, true);
-    const int64_t bound = m_all * p.n_tiles;
-    if (bound >= (1ll << 31)) return cudaErrorInvalidValue;
-    return launch16<kWeightGrad, bn>(p, ma, ma, mb, bound, stream, sms);
-  };
-  if (m_all * ((K + 255) / 256) >= 2 * sms) return go(std::integral_constant<int, 256>{});
-  return go(std::integral_constant<int, 128>{});
+  const int64_t pairs = (int64_t)gr.n_groups * ((N + 255) / 256) * ((K + 255) / 256);
+  if (N > kBM && pairs >= sms / 2) return launch_wg<2, 256>(p, ma, mb, mo, stream, sms);
+  return launch_wg<1, 128>(p, ma, mb, mo, stream, sms);
 }
 
 }  // namespace moe

@@ -35,6 +35,9 @@ cudaError_t make_tmap_bf16(CUtensorMap* map, const void* base, int64_t inner, in
 // 128-byte swizzle and a box of box_inner x box_rows x 1 (host side).
 cudaError_t make_tmap_16b_3d(CUtensorMap* map, const void* base, int64_t inner, int64_t rows,
                              int64_t depth, int box_inner, int box_rows);
+// The same for fp32 (box_inner * 4 = 128 bytes).
+cudaError_t make_tmap_f32_3d(CUtensorMap* map, const void* base, int64_t inner, int64_t rows,
+                             int64_t depth, int box_inner, int box_rows);
 
 // The sizes every entry point accepts (see moe_shape in moe_capi.h).
 bool shape_ok(const moe_shape& s);
