@@ -74,7 +74,9 @@ struct Args16 {
 struct alignas(8) Shared16 {
   uint64_t full[kMaxStages16];
   uint64_t empty[kMaxStages16];
-  uint64_t ready[kMaxStages16];  // weight gradient: both CTAs' stages, cleared
+  uint64_t part[kMaxStages16];   // weight gradient: this CTA's own loads of a
+                                 // stage whose last rows are to be cleared
+  uint64_t ready[kMaxStages16];  // and both CTAs have cleared them
   uint64_t tfull[2];
   uint64_t tempty[2];
   uint64_t drained;
@@ -101,10 +103,42 @@ MOE_DEV uint32_t in_leader(uint32_t addr) {
   asm("mapa.shared::cluster.u32 %0, %1, 0;" : "=r"(r) : "r"(addr));
   return r;
 }
-MOE_DEV void mbar_arrive_cluster(uint32_t bar) {
+// Arrival on a barrier of the pair's first CTA. The releasing form, which
+// also publishes the thread's stores to the other CTA, costs a memory barrier
+// (a microsecond and more in the MMA's path); where only tcgen05 reads are
+// done and nothing was stored, the relaxed one is enough.
+MOE_DEV void mbar_arrive_release(uint32_t bar) {
   asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(bar) : "memory");
 }
-MOE_DEV void fence_acquire_cluster() { asm volatile("fence.acq_rel.cluster;" ::: "memory"); }
+MOE_DEV void mbar_arrive_relaxed(uint32_t bar) {
+  asm volatile("mbarrier.arrive.relaxed.cluster.shared::cluster.b64 _, [%0];" ::"r"(bar) : "memory");
+}
+// mbar_wait for a barrier on which the pair's other CTA arrives as well
+template <int kCtas>
+MOE_DEV bool mbar_wait_pair(uint32_t bar, uint32_t parity, volatile int* abort, uint32_t* status) {
+  if constexpr (kCtas == 1) return mbar_wait(bar, parity, abort, status);
+  unsigned long long t0 = 0;
+  for (uint32_t i = 0;; ++i) {
+    uint32_t ok;
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "mbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2;\n\t"
+        "selp.u32 %0, 1, 0, p;\n\t}"
+        : "=r"(ok)
+        : "r"(bar), "r"(parity)
+        : "memory");
+    if (ok) return true;
+    if (i == 0) t0 = global_ns();
+    if ((i & 63u) == 63u) {
+      if (*abort) return false;
+      if (global_ns() - t0 > kWaitLimitNs) {
+        flag_status(status, kStatusTimeout);
+        *abort = 1;
+        return false;
+      }
+    }
+  }
+}
 
 template <int kCtas>
 MOE_DEV void load_2d(uint32_t dst, const CUtensorMap* map, int32_t x, int32_t y, uint32_t bar) {
@@ -429,7 +463,6 @@ __global__ void __cluster_dims__(kCtas, 1, 1) __launch_bounds__(256, 1)
         const int buf = used & 1;
         ok = mbar_wait(smem_u32(&sh.tempty[buf]), ((uint32_t)(used >> 1) & 1u) ^ 1u, abort, p.status);
         if (!ok) break;
-        if (kCtas == 2) fence_acquire_cluster();
         tc_fence_after();
         const uint32_t d = tmem_base + (uint32_t)(buf * kNT);
         for (int kb = 0; kb < kb_n; ++kb, ++it) {
@@ -518,7 +551,7 @@ __global__ void __cluster_dims__(kCtas, 1, 1) __launch_bounds__(256, 1)
       tc_fence_before();
       __syncwarp();
       if (lane == 0) {
-        if (kCtas == 2) mbar_arrive_cluster(in_leader(smem_u32(&sh.tempty[buf])));
+        if (kCtas == 2) mbar_arrive_relaxed(in_leader(smem_u32(&sh.tempty[buf])));
         else mbar_arrive(smem_u32(&sh.tempty[buf]));
       }
     }
@@ -644,6 +677,12 @@ MOE_DEV void add16(const Args16& p, const float (&v)[32], int x, int64_t at, boo
   }
 }
 
+// whether k-block kb of a group ends inside a 16-row step
+MOE_DEV bool to_clear(int rows, int kb) {
+  const int live = rows - kb * kBK;
+  return live < kBK && (live & 15) != 0;
+}
+
 template <int kCtas, int kBN>
 __global__ void __cluster_dims__(kCtas, 1, 1) __launch_bounds__(kWThreads, 1)
     grouped_wgrad_kernel(const __grid_constant__ CUtensorMap tm_a,
@@ -663,6 +702,7 @@ __global__ void __cluster_dims__(kCtas, 1, 1) __launch_bounds__(kWThreads, 1)
     for (int s = 0; s < C::stages; ++s) {
       mbar_init(smem_u32(&sh.full[s]), 1);
       mbar_init(smem_u32(&sh.empty[s]), 1);
+      mbar_init(smem_u32(&sh.part[s]), 1);
       mbar_init(smem_u32(&sh.ready[s]), kCtas);
     }
     for (int b = 0; b < 2; ++b) {
@@ -695,10 +735,12 @@ __global__ void __cluster_dims__(kCtas, 1, 1) __launch_bounds__(kWThreads, 1)
     if (lane == 0) {
       // ------------------------------------------------------------ producer
       int it = 0;
+      uint32_t part_phase = 0;  // a bit per stage
       bool ok = true;
       for (int64_t tile = team; ok && tile < total; tile += teams) {
         const TileAt t = tile_at((int)tile, sh.prefix, p.n_groups, p.n_tiles);
-        const int kb_n = (sh.rows[t.g] + kBK - 1) / kBK;
+        const int rows = sh.rows[t.g];
+        const int kb_n = (rows + kBK - 1) / kBK;
         const int a0 = (t.m * kCtas + rank) * kBM, b0 = t.n * kBN + rank * kHalf;
         for (int kb = 0; kb < kb_n; ++kb, ++it) {
           const int s = it % C::stages;
@@ -707,63 +749,78 @@ __global__ void __cluster_dims__(kCtas, 1, 1) __launch_bounds__(kWThreads, 1)
             ok = false;
             break;
           }
-          const uint32_t full = smem_u32(&sh.full[s]);
-          mbar_arrive_expect_tx(full, C::stage_bytes);
+          // A pair's loads count on its first CTA's barrier. Each CTA's loads
+          // of a block to be cleared count on a barrier of its own, and the
+          // first CTA's full barrier completes at once.
+          uint32_t bar = smem_u32(&sh.full[s]);
+          if (to_clear(rows, kb)) {
+            if (rank == 0) mbar_arrive(bar);
+            bar = smem_u32(&sh.part[s]);
+            mbar_arrive_expect_tx(bar, C::stage_bytes);
+            part_phase ^= 1u << s;
+          } else {
+            if (rank == 0) mbar_arrive_expect_tx(bar, kCtas * C::stage_bytes);
+            if (kCtas == 2) bar = in_leader(bar);
+          }
           const uint32_t sa = ring + s * C::stage_bytes, sb = sa + kABytes;
           const int r = sh.start[t.g] + kb * kBK;
 #pragma unroll
-          for (int i = 0; i < kBM / 64; ++i) tma_load_2d(sa + i * kBK * 128, &tm_a, a0 + i * 64, r, full);
+          for (int i = 0; i < kBM / 64; ++i)
+            load_2d<kCtas>(sa + i * kBK * 128, &tm_a, a0 + i * 64, r, bar);
 #pragma unroll
-          for (int i = 0; i < kHalf / 64; ++i) tma_load_2d(sb + i * kBK * 128, &tm_b, b0 + i * 64, r, full);
+          for (int i = 0; i < kHalf / 64; ++i)
+            load_2d<kCtas>(sb + i * kBK * 128, &tm_b, b0 + i * 64, r, bar);
         }
       }
       if (!ok) {
         // drain: every armed stage must land before the CTA may exit
         for (int s = 0; s < C::stages && s < it; ++s) {
           const int last = s + ((it - 1 - s) / C::stages) * C::stages;
-          mbar_wait(smem_u32(&sh.full[s]), (uint32_t)(last / C::stages) & 1u, nullptr, p.status);
+          if (rank == 0)
+            mbar_wait(smem_u32(&sh.full[s]), (uint32_t)(last / C::stages) & 1u, nullptr, p.status);
+          mbar_wait(smem_u32(&sh.part[s]), ((part_phase >> s) & 1u) ^ 1u, nullptr, p.status);
         }
       }
     }
   } else if (warp == 3) {
     // ---------------------------------------------- rows behind a group cleared
     int it = 0;
-    bool ok = true;
-    for (int64_t tile = team; ok && tile < total; tile += teams) {
+    uint32_t part_phase = 0;
+    for (int64_t tile = team; tile < total; tile += teams) {
       const TileAt t = tile_at((int)tile, sh.prefix, p.n_groups, p.n_tiles);
       const int rows = sh.rows[t.g];
       const int kb_n = (rows + kBK - 1) / kBK;
-      for (int kb = 0; kb < kb_n; ++kb, ++it) {
-        const int s = it % C::stages;
-        ok = __all_sync(0xffffffffu, mbar_wait(smem_u32(&sh.full[s]),
-                                               (uint32_t)(it / C::stages) & 1u, abort, p.status));
-        if (!ok) break;
-        const int live = rows - kb * kBK;
-        if (live < kBK) {
-          // up to the next 16-row step, in every 64-column box (a swizzled
-          // row stays within its 128 bytes)
-          const uint32_t sa = ring + s * C::stage_bytes;
-          const int dead = ((live + 15) & ~15) - live;
-          for (int i = lane; i < dead * 8 * (kBM + kHalf) / 64; i += 32) {
-            const int box = i / (dead * 8), q = i - box * dead * 8;
-            asm volatile("st.shared.v4.b32 [%0], {%1, %1, %1, %1};" ::"r"(
-                             sa + (uint32_t)(box * kBK * 128 + live * 128 + q * 16)),
-                         "r"(0)
-                         : "memory");
-          }
-        }
-        fence_proxy_async_smem();
-        __syncwarp();
-        if (lane == 0) {
-          if (kCtas == 2) mbar_arrive_cluster(in_leader(smem_u32(&sh.ready[s])));
-          else mbar_arrive(smem_u32(&sh.ready[s]));
-        }
+      it += kb_n;
+      if (kb_n == 0 || !to_clear(rows, kb_n - 1)) continue;
+      const int s = (it - 1) % C::stages;
+      if (!__all_sync(0xffffffffu, mbar_wait(smem_u32(&sh.part[s]), (part_phase >> s) & 1u, abort,
+                                             p.status)))
+        break;
+      part_phase ^= 1u << s;
+      // up to the next 16-row step, in every 64-column box (a swizzled row
+      // stays within its 128 bytes)
+      const uint32_t sa = ring + s * C::stage_bytes;
+      const int live = rows - (kb_n - 1) * kBK;
+      const int dead = ((live + 15) & ~15) - live;
+      for (int i = lane; i < dead * 8 * (kBM + kHalf) / 64; i += 32) {
+        const int box = i / (dead * 8), q = i - box * dead * 8;
+        asm volatile("st.shared.v4.b32 [%0], {%1, %1, %1, %1};" ::"r"(
+                         sa + (uint32_t)(box * kBK * 128 + live * 128 + q * 16)),
+                     "r"(0)
+                     : "memory");
+      }
+      fence_proxy_async_smem();
+      __syncwarp();
+      if (lane == 0) {
+        if (kCtas == 2) mbar_arrive_release(in_leader(smem_u32(&sh.ready[s])));
+        else mbar_arrive(smem_u32(&sh.ready[s]));
       }
     }
   } else if (warp == 1) {
     if (lane == 0 && rank == 0) {
       // ------------------------------------------------------------ MMA issuer
       int it = 0, used = 0;
+      uint32_t ready_phase = 0;
       bool ok = true;
       for (int64_t tile = team; ok && tile < total; tile += teams) {
         const TileAt t = tile_at((int)tile, sh.prefix, p.n_groups, p.n_tiles);
@@ -775,14 +832,17 @@ __global__ void __cluster_dims__(kCtas, 1, 1) __launch_bounds__(kWThreads, 1)
             ok = mbar_wait(smem_u32(&sh.tempty[buf]), ((uint32_t)(used >> 1) & 1u) ^ 1u, abort,
                            p.status);
             if (!ok) break;
-            if (kCtas == 2) fence_acquire_cluster();
             tc_fence_after();
           }
           const uint32_t d = tmem_base + (uint32_t)(buf * kBN);
           const int s = it % C::stages;
-          ok = mbar_wait(smem_u32(&sh.ready[s]), (uint32_t)(it / C::stages) & 1u, abort, p.status);
+          ok = mbar_wait(smem_u32(&sh.full[s]), (uint32_t)(it / C::stages) & 1u, abort, p.status);
+          if (ok && to_clear(rows, kb)) {
+            ok = mbar_wait_pair<kCtas>(smem_u32(&sh.ready[s]), (ready_phase >> s) & 1u, abort,
+                                       p.status);
+            ready_phase ^= 1u << s;
+          }
           if (!ok) break;
-          if (kCtas == 2) fence_acquire_cluster();
           tc_fence_after();
           const uint32_t sa = ring + s * C::stage_bytes;
           const uint64_t da = smem_desc_mn_sw128(sa), db = smem_desc_mn_sw128(sa + kABytes);
@@ -841,7 +901,7 @@ __global__ void __cluster_dims__(kCtas, 1, 1) __launch_bounds__(kWThreads, 1)
         __syncwarp();
         if (lane == 0) {
           const uint32_t bar = smem_u32(&sh.tempty[used & 1]);
-          if (kCtas == 2) mbar_arrive_cluster(in_leader(bar));
+          if (kCtas == 2) mbar_arrive_relaxed(in_leader(bar));
           else mbar_arrive(bar);
         }
         ++used;
