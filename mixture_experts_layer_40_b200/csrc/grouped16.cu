@@ -312,18 +312,25 @@ MOE_DEV uint32_t pack_f16x2(float lo, float hi) {
 //
 // kNT: the most rows of a tile (N of the MMA). A group's rows are cut into
 // equal tiles, so that none is nearly empty.
-template <int kCtas, int kNT>
+// kSub: tiles of kSub x 128 columns of the output a CTA, one accumulator each.
+template <int kCtas, int kNT, int kSub>
 struct MatCfg {
+  static constexpr int threads = 128 + 128 * kSub;  // an epilogue warpgroup for each accumulator
+  static constexpr int a_bytes = kSub * kABytes;
   static constexpr int b_bytes = kNT / kCtas * kBK * 2;
-  static constexpr int stage_bytes = kABytes + b_bytes;
-  // a warp's 32 rows x 32 columns of the output, fp32 or 16 bits, with the
-  // rows padded by 16 bytes against bank conflicts
-  static constexpr int turn_bytes = 32 * (32 * 4 + 16);
-  static constexpr int room = 212 * 1024 - 4 * turn_bytes;
+  static constexpr int stage_bytes = a_bytes + b_bytes;
+  // a warp's 32 (fp32: 16) rows x 32 columns of the output, each row padded
+  // by 16 bytes against bank conflicts
+  static constexpr int turn_bytes = 32 * (32 * 2 + 16);
+  static constexpr int room = 213 * 1024 - 4 * kSub * turn_bytes;
   static constexpr int stages =
       room / stage_bytes < kMaxStages16 ? room / stage_bytes : kMaxStages16;
-  static constexpr size_t dyn_smem = (size_t)stages * stage_bytes + 4 * turn_bytes + 1024;
+  static constexpr size_t dyn_smem = (size_t)stages * stage_bytes + 4 * kSub * turn_bytes + 1024;
+  // accumulators: two tiles of one (the next tile's MMAs run while one is
+  // read), or the two of one tile
+  static constexpr int tmem_cols = 2 * kNT;
 };
+static_assert(16 * (32 * 4 + 16) <= 32 * (32 * 2 + 16), "fp32 rows in the turn buffer");
 
 struct RowTile {
   int first, live, cols;  // first row, rows of the group, N of the MMA
@@ -341,12 +348,12 @@ MOE_DEV RowTile row_tile(int start, int rows, int m) {
   return t;
 }
 
-template <int kWay, int kCtas, int kNT>
-__global__ void __cluster_dims__(kCtas, 1, 1) __launch_bounds__(256, 1)
+template <int kWay, int kCtas, int kNT, int kSub>
+__global__ void __cluster_dims__(kCtas, 1, 1) __launch_bounds__(128 + 128 * kSub, 1)
     grouped_matmul_kernel(const __grid_constant__ CUtensorMap tm_w,
                           const __grid_constant__ CUtensorMap tm_x,
                           const __grid_constant__ CUtensorMap tm_x32, const Args16 p) {
-  using C = MatCfg<kCtas, kNT>;
+  using C = MatCfg<kCtas, kNT, kSub>;
   __shared__ Shared16 sh;
   extern __shared__ uint8_t dyn_smem[];
   const uint32_t ring = (smem_u32(dyn_smem) + 1023u) & ~1023u;
@@ -371,7 +378,7 @@ __global__ void __cluster_dims__(kCtas, 1, 1) __launch_bounds__(256, 1)
     prefetch_tensormap(&tm_x32);
   }
   if (warp == 2) {
-    alloc16<kCtas>(smem_u32(&sh.tmem_base), 2 * kNT);
+    alloc16<kCtas>(smem_u32(&sh.tmem_base), C::tmem_cols);
     scan_groups(p, sh, lane, kNT);
   }
   tc_fence_before();
@@ -385,8 +392,8 @@ __global__ void __cluster_dims__(kCtas, 1, 1) __launch_bounds__(256, 1)
   // Output columns per tile. With few tiles the last round would leave most
   // CTAs idle: tiles of a smaller height, whose loads overlap their
   // neighbour's rows in L2, fill it.
-  int height = kBM * kCtas;
-  if (kCtas == 1) {
+  int height = kBM * kCtas * kSub;
+  if (kCtas == 1 && kSub == 1) {
     int64_t best = -1;
     for (int h = kBM; h >= kBM / 2; h -= 8) {
       const int64_t rounds = ((int64_t)row_tiles * ((p.N + h - 1) / h) + teams - 1) / teams;
@@ -415,7 +422,7 @@ __global__ void __cluster_dims__(kCtas, 1, 1) __launch_bounds__(256, 1)
         const bool whole = kNT / kCtas >= 128 && pieces == 4;
         const int row = rt.first + rank * half;
         const int n0 = t.n * height + rank * kBM;
-        const uint32_t bytes = kCtas * (kABytes + pieces * 32 * kBK * 2);
+        const uint32_t bytes = kCtas * (C::a_bytes + pieces * 32 * kBK * 2);
         for (int kb = 0; kb < kb_n; ++kb, ++it) {
           const int s = it % C::stages;
           if (!mbar_wait(smem_u32(&sh.empty[s]), ((uint32_t)(it / C::stages) & 1u) ^ 1u, abort,
@@ -427,13 +434,18 @@ __global__ void __cluster_dims__(kCtas, 1, 1) __launch_bounds__(256, 1)
           uint32_t full = smem_u32(&sh.full[s]);
           if (rank == 0) mbar_arrive_expect_tx(full, bytes);
           if (kCtas == 2) full = in_leader(full);
-          const uint32_t sa = ring + s * C::stage_bytes, sb = sa + kABytes;
-          if (kWay == kForward) {
-            load_3d<kCtas>(sa, &tm_w, kb * kBK, n0, t.g, full);
-          } else {
+          const uint32_t sa = ring + s * C::stage_bytes, sb = sa + C::a_bytes;
 #pragma unroll
-            for (int i = 0; i < kBM / 64; ++i)
-              load_3d<kCtas>(sa + i * kBK * 128, &tm_w, n0 + i * 64, kb * kBK, t.g, full);
+          for (int u = 0; u < kSub; ++u) {
+            const int n = n0 + u * kBM * kCtas;
+            if (kWay == kForward) {
+              load_3d<kCtas>(sa + u * kABytes, &tm_w, kb * kBK, n, t.g, full);
+            } else {
+#pragma unroll
+              for (int i = 0; i < kBM / 64; ++i)
+                load_3d<kCtas>(sa + u * kABytes + i * kBK * 128, &tm_w, n + i * 64, kb * kBK, t.g,
+                               full);
+            }
           }
           if (whole) {
             load_2d<kCtas>(sb, &tm_x, kb * kBK, row, full);
@@ -460,26 +472,35 @@ __global__ void __cluster_dims__(kCtas, 1, 1) __launch_bounds__(256, 1)
         const TileAt t = tile_at((int)tile, sh.prefix, p.n_groups, n_tiles);
         const RowTile rt = row_tile<kNT>(sh.start[t.g], sh.rows[t.g], t.m);
         const uint32_t idesc = p.idesc | ((uint32_t)(rt.cols >> 3) << 17);
-        const int buf = used & 1;
-        ok = mbar_wait(smem_u32(&sh.tempty[buf]), ((uint32_t)(used >> 1) & 1u) ^ 1u, abort, p.status);
-        if (!ok) break;
-        tc_fence_after();
-        const uint32_t d = tmem_base + (uint32_t)(buf * kNT);
-        for (int kb = 0; kb < kb_n; ++kb, ++it) {
+        // accumulators in use: tile by tile in turn, or both by each tile
+        const int buf = kSub == 1 ? used & 1 : 0;
+        const uint32_t free_phase = ((uint32_t)(kSub == 1 ? used >> 1 : used) & 1u) ^ 1u;
+        for (int kb = 0; ok && kb < kb_n; ++kb, ++it) {
           const int s = it % C::stages;
           ok = mbar_wait(smem_u32(&sh.full[s]), (uint32_t)(it / C::stages) & 1u, abort, p.status);
           if (!ok) break;
           tc_fence_after();
           const uint32_t sa = ring + s * C::stage_bytes;
-          const uint64_t da = kWay == kForward ? smem_desc_sw128(sa) : smem_desc_mn_sw128(sa);
-          const uint64_t db = smem_desc_sw128(sa + kABytes);
+          const uint64_t db = smem_desc_sw128(sa + C::a_bytes);
           constexpr uint64_t step_a = kWay == kForward ? kStepK : kStepMN;
 #pragma unroll
-          for (int i = 0; i < kBK / 16; ++i)
-            mma16<kCtas>(d, da + step_a * i, db + kStepK * i, idesc, (kb | i) > 0 ? 1u : 0u);
+          for (int u = 0; u < kSub; ++u) {
+            if (kb == 0) {
+              ok = mbar_wait(smem_u32(&sh.tempty[buf + u]), free_phase, abort, p.status);
+              if (!ok) break;
+              tc_fence_after();
+            }
+            const uint32_t sw = sa + u * kABytes;
+            const uint64_t da = kWay == kForward ? smem_desc_sw128(sw) : smem_desc_mn_sw128(sw);
+            const uint32_t d = tmem_base + (uint32_t)((buf + u) * kNT);
+#pragma unroll
+            for (int i = 0; i < kBK / 16; ++i)
+              mma16<kCtas>(d, da + step_a * i, db + kStepK * i, idesc, (kb | i) > 0 ? 1u : 0u);
+            if (kb == kb_n - 1) commit16<kCtas>(smem_u32(&sh.tfull[buf + u]));
+          }
+          if (!ok) break;
           commit16<kCtas>(smem_u32(&sh.empty[s]));
         }
-        if (ok) commit16<kCtas>(smem_u32(&sh.tfull[buf]));
       }
       if (!ok && it > 0) {
         // every issued MMA has completed before TMEM is released
@@ -490,8 +511,9 @@ __global__ void __cluster_dims__(kCtas, 1, 1) __launch_bounds__(256, 1)
   } else if (warp >= 4) {
     // -------------------------------------------------------------- epilogue
     const int quarter = warp & 3;  // TMEM lanes 32 * quarter .. = output columns
+    const int sub = (warp - 4) >> 2;
     const uint32_t lane_addr = tmem_base + ((uint32_t)(quarter * 32) << 16);
-    const uint32_t turn = ring + (uint32_t)(C::stages * C::stage_bytes + quarter * C::turn_bytes);
+    const uint32_t turn = ring + (uint32_t)(C::stages * C::stage_bytes + (warp - 4) * C::turn_bytes);
     const bool wide = p.out_type == MOE_FP32;
     const bool f16 = p.out_type == MOE_FP16;
     const int es = wide ? 4 : 2;
@@ -502,26 +524,55 @@ __global__ void __cluster_dims__(kCtas, 1, 1) __launch_bounds__(256, 1)
     for (int64_t tile = team; tile < total; tile += teams, ++used) {
       const TileAt t = tile_at((int)tile, sh.prefix, p.n_groups, n_tiles);
       const RowTile rt = row_tile<kNT>(sh.start[t.g], sh.rows[t.g], t.m);
-      const int buf = used & 1;
-      if (!__all_sync(0xffffffffu, mbar_wait(smem_u32(&sh.tfull[buf]), (uint32_t)(used >> 1) & 1u,
-                                             abort, p.status)))
+      const int buf = kSub == 1 ? used & 1 : sub;
+      const uint32_t full_phase = (uint32_t)(kSub == 1 ? used >> 1 : used) & 1u;
+      if (!__all_sync(0xffffffffu, mbar_wait(smem_u32(&sh.tfull[buf]), full_phase, abort, p.status)))
         break;
       tc_fence_after();
       // this tile's output columns end where the next tile's begin
-      const int n0 = t.n * height + rank * kBM + quarter * 32;
+      const int n0 = t.n * height + (sub * kCtas + rank) * kBM + quarter * 32;
       const int n_end = min(t.n * height + height, p.N);
       const int n = n0 + piece * (16 / es);
       uint8_t* const out = static_cast<uint8_t*>(p.out) + ((int64_t)rt.first * p.N + n) * es;
+      // the `count` rows from c on in the turn buffer, to global memory
+      auto copy_out = [&](int c, int count) {
+        __syncwarp();
+        if (n < n_end) {
+          for (int j = row0; j < count && c + j < rt.live; j += row_step) {
+            uint32_t q[4];
+            asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];"
+                         : "=r"(q[0]), "=r"(q[1]), "=r"(q[2]), "=r"(q[3])
+                         : "r"(turn + j * pitch + piece * 16)
+                         : "memory");
+            *reinterpret_cast<uint4*>(out + (int64_t)(c + j) * p.N * es) =
+                make_uint4(q[0], q[1], q[2], q[3]);
+          }
+        }
+        __syncwarp();
+      };
       for (int c = 0; c < rt.live; c += 32) {
         float v[32];
         tmem_ld32(lane_addr + (uint32_t)(buf * kNT + c), v);
         tmem_wait_ld();
+        if (c + 32 >= rt.live) {  // all read: the next MMAs may overwrite
+          tc_fence_before();
+          __syncwarp();
+          if (lane == 0) {
+            if (kCtas == 2) mbar_arrive_relaxed(in_leader(smem_u32(&sh.tempty[buf])));
+            else mbar_arrive(smem_u32(&sh.tempty[buf]));
+          }
+        }
         if (n0 >= n_end) continue;
         if (wide) {
 #pragma unroll
-          for (int j = 0; j < 32; ++j)
-            asm volatile("st.shared.f32 [%0], %1;" ::"r"(turn + j * pitch + lane * 4), "f"(v[j])
-                         : "memory");
+          for (int h = 0; h < 2; ++h) {
+#pragma unroll
+            for (int j = 0; j < 16; ++j)
+              asm volatile("st.shared.f32 [%0], %1;" ::"r"(turn + j * pitch + lane * 4),
+                           "f"(v[16 * h + j])
+                           : "memory");
+            copy_out(c + 16 * h, 16);
+          }
         } else {
 #pragma unroll
           for (int j = 0; j < 32; j += 2) {
@@ -533,26 +584,8 @@ __global__ void __cluster_dims__(kCtas, 1, 1) __launch_bounds__(256, 1)
                          "h"((uint16_t)(w >> 16))
                          : "memory");
           }
+          copy_out(c, 32);
         }
-        __syncwarp();
-        if (n < n_end) {
-          for (int j = row0; j < 32 && c + j < rt.live; j += row_step) {
-            uint32_t q[4];
-            asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];"
-                         : "=r"(q[0]), "=r"(q[1]), "=r"(q[2]), "=r"(q[3])
-                         : "r"(turn + j * pitch + piece * 16)
-                         : "memory");
-            *reinterpret_cast<uint4*>(out + (int64_t)(c + j) * p.N * es) =
-                make_uint4(q[0], q[1], q[2], q[3]);
-          }
-        }
-        __syncwarp();
-      }
-      tc_fence_before();
-      __syncwarp();
-      if (lane == 0) {
-        if (kCtas == 2) mbar_arrive_relaxed(in_leader(smem_u32(&sh.tempty[buf])));
-        else mbar_arrive(smem_u32(&sh.tempty[buf]));
       }
     }
   }
@@ -561,7 +594,7 @@ __global__ void __cluster_dims__(kCtas, 1, 1) __launch_bounds__(256, 1)
   if constexpr (kCtas == 2) cluster_sync();
   else __syncthreads();
   tc_fence_after();
-  if (warp == 2) dealloc16<kCtas>(tmem_base, 2 * kNT);
+  if (warp == 2) dealloc16<kCtas>(tmem_base, C::tmem_cols);
 }
 
 // ====================================================== weight gradient
@@ -951,13 +984,13 @@ __global__ void __cluster_dims__(kCtas, 1, 1) __launch_bounds__(kWThreads, 1)
 }
 
 // ================================================================ launches
-template <int kWay, int kCtas, int kNT>
+template <int kWay, int kCtas, int kNT, int kSub>
 cudaError_t launch_mat(Args16 a, const CUtensorMap& mw, const CUtensorMap& mx,
                        const CUtensorMap& mx32, int64_t row_tiles, cudaStream_t stream, int sms) {
-  using C = MatCfg<kCtas, kNT>;
+  using C = MatCfg<kCtas, kNT, kSub>;
   static DeviceOnce once;
   cudaError_t e = once.run([] {
-    return cudaFuncSetAttribute(grouped_matmul_kernel<kWay, kCtas, kNT>,
+    return cudaFuncSetAttribute(grouped_matmul_kernel<kWay, kCtas, kNT, kSub>,
                                 cudaFuncAttributeMaxDynamicSharedMemorySize, (int)C::dyn_smem);
   });
   if (e != cudaSuccess) return e;
@@ -966,7 +999,7 @@ cudaError_t launch_mat(Args16 a, const CUtensorMap& mw, const CUtensorMap& mx,
   const int64_t tiles = row_tiles * ((a.N + kBM / 2 - 1) / (kBM / 2));
   if (tiles >= (1ll << 31)) return cudaErrorInvalidValue;
   const int64_t grid = tiles * kCtas < sms ? tiles * kCtas : sms / kCtas * kCtas;
-  grouped_matmul_kernel<kWay, kCtas, kNT><<<(unsigned)grid, 256, C::dyn_smem, stream>>>(mw, mx, mx32, a);
+  grouped_matmul_kernel<kWay, kCtas, kNT, kSub><<<(unsigned)grid, C::threads, C::dyn_smem, stream>>>(mw, mx, mx32, a);
   return cudaGetLastError();
 }
 
@@ -1021,16 +1054,20 @@ cudaError_t launch_grouped_matmul(const Groups16& gr, bool f16, int out_type, in
   if (e != cudaSuccess) return e;
   const int64_t busy = gr.rows < gr.n_groups ? gr.rows : gr.n_groups;
   const int64_t each = gr.rows / busy;  // rows of a group, if they were alike
-  auto go = [&](auto ctas, auto nt) {
+  auto go = [&](auto ctas, auto nt, auto sub) {
     constexpr int kCtas = decltype(ctas)::value, kNT = decltype(nt)::value;
+    constexpr int kSub = decltype(sub)::value;
     const int64_t row_tiles = gr.rows / kNT + busy;
-    return trans_b ? launch_mat<kForward, kCtas, kNT>(p, mw, mx, mx32, row_tiles, stream, sms)
-                   : launch_mat<kInputGrad, kCtas, kNT>(p, mw, mx, mx32, row_tiles, stream, sms);
+    return trans_b ? launch_mat<kForward, kCtas, kNT, kSub>(p, mw, mx, mx32, row_tiles, stream, sms)
+                   : launch_mat<kInputGrad, kCtas, kNT, kSub>(p, mw, mx, mx32, row_tiles, stream, sms);
   };
   using std::integral_constant;
-  if (each > 160 && N > kBM) return go(integral_constant<int, 2>{}, integral_constant<int, 256>{});
-  if (each > 24) return go(integral_constant<int, 1>{}, integral_constant<int, 128>{});
-  return go(integral_constant<int, 1>{}, integral_constant<int, 32>{});
+  constexpr integral_constant<int, 1> one{};
+  constexpr integral_constant<int, 2> two{};
+  if (each > 160 && N > 2 * kBM) return go(two, integral_constant<int, 256>{}, two);
+  if (each > 160 && N > kBM) return go(two, integral_constant<int, 256>{}, one);
+  if (each > 24) return go(one, integral_constant<int, 128>{}, one);
+  return go(one, integral_constant<int, 32>{}, one);
 }
 
 cudaError_t launch_grouped_wgrad(const Groups16& gr, bool f16, int out_type, int N, int K,
