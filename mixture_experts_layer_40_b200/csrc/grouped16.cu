@@ -614,10 +614,13 @@ struct WgCfg {
   static constexpr int b_bytes = kBN / kCtas * kBK * 2;
   static constexpr int stage_bytes = kABytes + b_bytes;
   static constexpr int buf_bytes = 32 * 128;  // a warp's 32 rows x 128 bytes
-  static constexpr int room = 208 * 1024 - 8 * 2 * buf_bytes;
+  static constexpr int room = 213 * 1024 - 8 * buf_bytes;
   static constexpr int stages = room / stage_bytes < 6 ? room / stage_bytes : 6;
-  static constexpr size_t dyn_smem = (size_t)stages * stage_bytes + 8 * 2 * buf_bytes + 1024;
+  static constexpr size_t dyn_smem = (size_t)stages * stage_bytes + 8 * buf_bytes + 1024;
 };
+
+// the shared-memory sources of this thread's committed stores may be reused
+MOE_DEV void bulk_wait_read() { asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory"); }
 
 MOE_DEV void store_3d(const CUtensorMap* map, uint32_t src, int32_t x, int32_t y, int32_t z,
                       bool add) {
@@ -641,16 +644,15 @@ MOE_DEV void store_3d(const CUtensorMap* map, uint32_t src, int32_t x, int32_t y
 struct DwOut {
   const CUtensorMap* map;
   uint32_t buf;
-  int turn;
   MOE_DEV void put(const Args16& p, const float (&v)[32], int x, int y, int g, int lane) {
     const bool wide = p.out_type == MOE_FP32;
     const uint32_t swz = (uint32_t)(lane & 7);
     const int part = wide ? 0 : (x >> 5) & 1;  // which half of the 128-byte row
     if (part == 0) {
-      if (lane == 0) bulk_wait_read_1();  // the store that last read this buffer is done
+      if (lane == 0) bulk_wait_read();  // the last store has read the buffer
       __syncwarp();
     }
-    const uint32_t row = buf + (uint32_t)(turn * 32 * 128 + lane * 128);
+    const uint32_t row = buf + (uint32_t)(lane * 128);
     if (wide) {
 #pragma unroll
       for (int c = 0; c < 8; ++c)
@@ -676,10 +678,9 @@ struct DwOut {
       fence_proxy_async_smem();
       __syncwarp();
       if (lane == 0) {
-        store_3d(map, buf + (uint32_t)(turn * 32 * 128), wide ? x : x - 32, y, g, p.accumulate != 0);
+        store_3d(map, buf, wide ? x : x - 32, y, g, p.accumulate != 0);
         bulk_commit();
       }
-      turn ^= 1;
     }
   }
 };
@@ -903,7 +904,7 @@ __global__ void __cluster_dims__(kCtas, 1, 1) __launch_bounds__(kWThreads, 1)
     const int quarter = warp & 3;  // TMEM lanes 32 * quarter .. = rows of dw
     const int c0 = (ew >> 2) * kEpiCols;
     const uint32_t lane_addr = tmem_base + ((uint32_t)(quarter * 32) << 16) + (uint32_t)c0;
-    DwOut out{&tm_out, ring + (uint32_t)(C::stages * C::stage_bytes + ew * 2 * C::buf_bytes), 0};
+    DwOut out{&tm_out, ring + (uint32_t)(C::stages * C::stage_bytes + ew * C::buf_bytes)};
     const bool direct = p.accumulate && p.out_type != MOE_FP32;
     int used = 0;
     bool ok = true;
