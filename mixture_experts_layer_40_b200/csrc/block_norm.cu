@@ -21,8 +21,8 @@ namespace moe {
 
 namespace {
 
-constexpr int kNormThreads = 1024;  // most threads of a CTA
-constexpr int kBackThreads = 512;   // and of the backward's, which holds more in registers
+constexpr int kNormThreads = 896;  // most threads of a CTA (with 8 columns a thread)
+constexpr int kBackThreads = 512;  // and of the kernels that hold more in registers
 constexpr int kMaxParts = 1024;     // partial column sums
 constexpr size_t kRing = 208 * 1024;
 constexpr int kMaxStages = 6;       // rows asked for ahead, per team
@@ -67,35 +67,60 @@ MOE_DEV T from_f(float v) {
   else return __float2bfloat16_rn(v);
 }
 
-// 8 packed elements to and from fp32
+// Two fp32 values in a register pair: two-lane multiplies and FMAs (each lane
+// rounded once) halve the instructions of these row loops, which a few warps
+// per scheduler could not issue fast enough one by one.
+typedef uint64_t F2;
+MOE_DEV F2 pack2(float lo, float hi) {
+  F2 r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(lo), "f"(hi));
+  return r;
+}
+MOE_DEV F2 mul2(F2 a, F2 b) {
+  F2 r;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+MOE_DEV F2 fma2(F2 a, F2 b, F2 c) {
+  F2 r;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+  return r;
+}
+MOE_DEV float lanes_sum(F2 a) {
+  float lo, hi;
+  unpack_f32x2(a, lo, hi);
+  return lo + hi;
+}
+
+// 8 packed elements to and from fp32 pairs
 template <typename T>
-MOE_DEV void unpack8(const uint32_t (&w)[sizeof(T) * 2], float (&v)[8]) {
+MOE_DEV void unpack8(const uint32_t (&w)[sizeof(T) * 2], F2 (&v)[4]) {
 #pragma unroll
-  for (int i = 0; i < (int)sizeof(T) * 2; ++i) {
+  for (int i = 0; i < 4; ++i) {
     if constexpr (std::is_same_v<T, float>) {
-      v[i] = __uint_as_float(w[i]);
+      v[i] = pack2(__uint_as_float(w[2 * i]), __uint_as_float(w[2 * i + 1]));
     } else if constexpr (std::is_same_v<T, __half>) {
-      const float2 f = __half22float2(__halves2half2(__ushort_as_half((unsigned short)(w[i] & 0xFFFFu)),
-                                                     __ushort_as_half((unsigned short)(w[i] >> 16))));
-      v[2 * i] = f.x;
-      v[2 * i + 1] = f.y;
+      v[i] = pack2(__half2float(__ushort_as_half((unsigned short)(w[i] & 0xFFFFu))),
+                   __half2float(__ushort_as_half((unsigned short)(w[i] >> 16))));
     } else {
-      v[2 * i] = bf16_lo(w[i]);
-      v[2 * i + 1] = bf16_hi(w[i]);
+      v[i] = pack2(bf16_lo(w[i]), bf16_hi(w[i]));
     }
   }
 }
 template <typename T>
-MOE_DEV void pack8(const float (&v)[8], uint32_t (&w)[sizeof(T) * 2]) {
+MOE_DEV void pack8(const F2 (&v)[4], uint32_t (&w)[sizeof(T) * 2]) {
 #pragma unroll
-  for (int i = 0; i < (int)sizeof(T) * 2; ++i) {
+  for (int i = 0; i < 4; ++i) {
+    float lo, hi;
+    unpack_f32x2(v[i], lo, hi);
     if constexpr (std::is_same_v<T, float>) {
-      w[i] = __float_as_uint(v[i]);
+      w[2 * i] = __float_as_uint(lo);
+      w[2 * i + 1] = __float_as_uint(hi);
     } else if constexpr (std::is_same_v<T, __half>) {
-      const __half2 h = __floats2half2_rn(v[2 * i], v[2 * i + 1]);
-      w[i] = (uint32_t)__half_as_ushort(__low2half(h)) | ((uint32_t)__half_as_ushort(__high2half(h)) << 16);
+      w[i] = (uint32_t)__half_as_ushort(__float2half_rn(lo)) |
+             ((uint32_t)__half_as_ushort(__float2half_rn(hi)) << 16);
     } else {
-      w[i] = pack_bf16x2(v[2 * i], v[2 * i + 1]);
+      w[i] = pack_bf16x2(lo, hi);
     }
   }
 }
@@ -104,7 +129,7 @@ MOE_DEV void pack8(const float (&v)[8], uint32_t (&w)[sizeof(T) * 2]) {
 // accesses); otherwise `stride` columns apart, so that a warp's accesses are
 // consecutive, and the first n of them exist.
 template <typename T, bool kVec>
-MOE_DEV void load8(const void* base, int64_t at, int n, int stride, float (&v)[8]) {
+MOE_DEV void load8(const void* base, int64_t at, int n, int stride, F2 (&v)[4]) {
   const T* p = static_cast<const T*>(base) + at;
   if constexpr (kVec) {
     uint32_t w[sizeof(T) * 2] = {};
@@ -118,12 +143,14 @@ MOE_DEV void load8(const void* base, int64_t at, int n, int stride, float (&v)[8
     unpack8<T>(w, v);
   } else {
 #pragma unroll
-    for (int i = 0; i < 8; ++i) v[i] = i < n ? to_f<T>(p[i * stride]) : 0.0f;
+    for (int i = 0; i < 4; ++i)
+      v[i] = pack2(2 * i < n ? to_f<T>(p[2 * i * stride]) : 0.0f,
+                   2 * i + 1 < n ? to_f<T>(p[(2 * i + 1) * stride]) : 0.0f);
   }
 }
 
 template <typename T, bool kVec>
-MOE_DEV void store8(void* base, int64_t at, int n, int stride, const float (&v)[8]) {
+MOE_DEV void store8(void* base, int64_t at, int n, int stride, const F2 (&v)[4]) {
   T* p = static_cast<T*>(base) + at;
   if constexpr (kVec) {
     if (n > 0) {
@@ -136,13 +163,17 @@ MOE_DEV void store8(void* base, int64_t at, int n, int stride, const float (&v)[
     }
   } else {
 #pragma unroll
-    for (int i = 0; i < 8; ++i)
-      if (i < n) p[i * stride] = from_f<T>(v[i]);
+    for (int i = 0; i < 4; ++i) {
+      float lo, hi;
+      unpack_f32x2(v[i], lo, hi);
+      if (2 * i < n) p[2 * i * stride] = from_f<T>(lo);
+      if (2 * i + 1 < n) p[(2 * i + 1) * stride] = from_f<T>(hi);
+    }
   }
 }
 
 template <typename Act, bool kVec>
-MOE_DEV void load_w8(const void* w, bool f32, int at, int n, int stride, float (&v)[8]) {
+MOE_DEV void load_w8(const void* w, bool f32, int at, int n, int stride, F2 (&v)[4]) {
   if (f32) load8<float, kVec>(w, at, n, stride, v);
   else load8<Act, kVec>(w, at, n, stride, v);
 }
@@ -166,7 +197,17 @@ struct Slot {
                    "l"(p + j * (16 / sizeof(T)))
                    : "memory");
   }
-  MOE_DEV void get(int c, uint32_t stage, float (&v)[8]) const {
+  MOE_DEV void put(int c, const F2 (&v)[4]) const {
+    uint32_t w[sizeof(T) * 2];
+    pack8<T>(v, w);
+#pragma unroll
+    for (int j = 0; j < pieces; ++j)
+      asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(
+                       base + (uint32_t)((c * pieces + j) * blockDim.x * 16)),
+                   "r"(w[4 * j]), "r"(w[4 * j + 1]), "r"(w[4 * j + 2]), "r"(w[4 * j + 3])
+                   : "memory");
+  }
+  MOE_DEV void get(int c, uint32_t stage, F2 (&v)[4]) const {
     uint32_t w[sizeof(T) * 2];
 #pragma unroll
     for (int j = 0; j < pieces; ++j)
@@ -221,7 +262,7 @@ struct Place {
   MOE_DEV int64_t step() const { return (int64_t)gridDim.x * teams; }
 };
 
-typedef float TeamBuf[2][3][kNormThreads / 32];
+typedef float TeamBuf[2][3][32];
 
 // Sums over a team of warps. Two buffers in turn: a thread writes one again
 // only after a barrier that every reader of its last use has passed.
@@ -248,143 +289,164 @@ MOE_DEV void team_sum(float (&v)[kN], const P& at, TeamBuf& buf, int& turn) {
 }
 
 // alpha * post * scale of a thread's columns (absent weights are 1, columns
-// beyond the row 0)
+// beyond the row anything finite: their values are zeros)
 template <typename Act, int kNC, bool kVec>
-MOE_DEV void branch_weights(const NormArgs& p, const Place<kNC, kVec>& at, float (&wq)[kNC][8]) {
+MOE_DEV void branch_weights(const NormArgs& p, const Place<kNC, kVec>& at, F2 (&wq)[kNC][4]) {
 #pragma unroll
   for (int c = 0; c < kNC; ++c) {
-    float w[8];
+    F2 w[4];
 #pragma unroll
-    for (int i = 0; i < 8; ++i) wq[c][i] = p.alpha;
+    for (int i = 0; i < 4; ++i) wq[c][i] = pack2(p.alpha, p.alpha);
     if (p.post) {
       load_w8<Act, kVec>(p.post, p.w_f32, at.col[c], at.n[c], at.stride, w);
 #pragma unroll
-      for (int i = 0; i < 8; ++i) wq[c][i] *= w[i];
+      for (int i = 0; i < 4; ++i) wq[c][i] = mul2(wq[c][i], w[i]);
     }
     if (p.scale) {
       load_w8<Act, kVec>(p.scale, p.w_f32, at.col[c], at.n[c], at.stride, w);
 #pragma unroll
-      for (int i = 0; i < 8; ++i) wq[c][i] *= w[i];
+      for (int i = 0; i < 4; ++i) wq[c][i] = mul2(wq[c][i], w[i]);
     }
   }
 }
 
 template <typename Act, int kNC, bool kVec>
-MOE_DEV void pre_weights(const NormArgs& p, const Place<kNC, kVec>& at, float (&w)[kNC][8]) {
+MOE_DEV void pre_weights(const NormArgs& p, const Place<kNC, kVec>& at, F2 (&w)[kNC][4]) {
 #pragma unroll
   for (int c = 0; c < kNC; ++c) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) w[c][i] = 0ull;
     if (p.pre) load_w8<Act, kVec>(p.pre, p.w_f32, at.col[c], at.n[c], at.stride, w[c]);
   }
 }
 
-template <typename Res, typename Act, int kNC, bool kVec>
-__global__ void __launch_bounds__(kNormThreads, 1) block_norm_kernel(const NormArgs p) {
+// kR rows a step: their sums meet at the same barriers, which leaves half of
+// the waiting of one row a step.
+template <typename Res, typename Act, int kNC, int kR, bool kVec>
+__global__ void __launch_bounds__(kNC == 1 ? kNormThreads : kBackThreads, 1)
+    block_norm_kernel(const NormArgs p) {
   __shared__ TeamBuf buf;
   extern __shared__ __align__(16) uint8_t ring[];
   const Place<kNC, kVec> at(p);
   const float inv_h = 1.0f / (float)p.H;
   const bool full = p.gate_kind == kGateFull;
   int turn = 0;
-  Slot<Res> sx{smem_u32(ring) + threadIdx.x * 16};
-  Slot<Act> sz{sx.base + Slot<Res>::bytes(blockDim.x, kNC)};
-  Slot<Act> sg{sz.base + Slot<Act>::bytes(blockDim.x, kNC)};
-  const uint32_t stage_bytes = (uint32_t)(Slot<Res>::bytes(blockDim.x, kNC) +
-                                          (p.z ? Slot<Act>::bytes(blockDim.x, kNC) : 0) +
-                                          (full ? Slot<Act>::bytes(blockDim.x, kNC) : 0));
+  const Slot<Res> sx{smem_u32(ring) + threadIdx.x * 16};
+  const Slot<Act> sz{sx.base + Slot<Res>::bytes(blockDim.x, kNC)};
+  const Slot<Act> sg{sz.base + Slot<Act>::bytes(blockDim.x, kNC)};
+  const uint32_t row_bytes = (uint32_t)(Slot<Res>::bytes(blockDim.x, kNC) +
+                                        (p.z ? Slot<Act>::bytes(blockDim.x, kNC) : 0) +
+                                        (full ? Slot<Act>::bytes(blockDim.x, kNC) : 0));
+  const uint32_t stage_bytes = kR * row_bytes;
+  // the kR rows of step i: i * step() apart, side by side over the teams
+  const int64_t step = at.step();
   auto ask = [&](int64_t row, int s) {
-    if (row < p.T) {
+#pragma unroll
+    for (int q = 0; q < kR; ++q, row += step) {
+      if (row >= p.T) break;
 #pragma unroll
       for (int c = 0; c < kNC; ++c) {
         if (at.n[c] == 0) continue;
         const int64_t e = row * p.H + at.col[c];
-        sx.ask(p.x, e, c, s * stage_bytes);
-        if (p.z) sz.ask(p.z, e, c, s * stage_bytes);
-        if (full) sg.ask(p.gate, e, c, s * stage_bytes);
+        const uint32_t stage = s * stage_bytes + q * row_bytes;
+        if (p.z) sz.ask(p.z, e, c, stage);
+        sx.ask(p.x, e, c, stage);
+        if (full) sg.ask(p.gate, e, c, stage);
       }
     }
     ask_commit();
   };
   if (kVec)
-    for (int s = 0; s < p.stages - 1; ++s) ask(at.first() + s * at.step(), s);
-  float pre[kNC][8], wq[kNC][8];
+    for (int s = 0; s < p.stages - 1; ++s) ask(at.first() + s * kR * step, s);
+  F2 pre[kNC][4], wq[kNC][4];
   pre_weights<Act>(p, at, pre);
   if (p.z) branch_weights<Act>(p, at, wq);
   int slot = 0;
-  for (int64_t row = at.first(); row < p.T; row += at.step()) {
-    const int64_t e = row * p.H;
+  for (int64_t row = at.first(); row < p.T; row += kR * step) {
     const uint32_t stage = slot * stage_bytes;
-    float gate = 1.0f;
-    if (p.gate_kind == kGateRow) gate = static_cast<const float*>(p.gate)[row];
+    float gate[kR], s[kR];
+#pragma unroll
+    for (int q = 0; q < kR; ++q) {
+      gate[q] = 1.0f;
+      s[q] = 0.0f;
+      if (p.gate_kind == kGateRow && row + q * step < p.T)
+        gate[q] = static_cast<const float*>(p.gate)[row + q * step];
+    }
     if (kVec) {
       const int ahead = p.stages - 1;
-      ask(row + ahead * at.step(), slot + ahead < p.stages ? slot + ahead : slot - 1);
+      ask(row + ahead * kR * step, slot + ahead < p.stages ? slot + ahead : slot - 1);
       ask_wait(ahead);
       slot = slot + 1 == p.stages ? 0 : slot + 1;
     }
-    // columns beyond the row hold zeros throughout
-    float r[kNC][8];
-    float s[1] = {0.0f};
-    if (p.z) {
-      float z[kNC][8];
+    // columns beyond the row, and rows beyond the last, hold zeros throughout
+    auto here = [&](int q, int c) { return at.n[c] > 0 && (kR == 1 || row + q * step < p.T); };
+    auto get_x = [&](int q, int c, F2 (&v)[4]) {
+      if (kVec) sx.get(c, stage + q * row_bytes, v);
+      else load8<Res, kVec>(p.x, (row + q * step) * p.H + at.col[c], at.n[c], at.stride, v);
+    };
+    auto get_act = [&](const Slot<Act>& sl, const void* g, int q, int c, F2 (&v)[4]) {
+      if (kVec) sl.get(c, stage + q * row_bytes, v);
+      else load8<Act, kVec>(g, (row + q * step) * p.H + at.col[c], at.n[c], at.stride, v);
+    };
+    if (p.post) {
 #pragma unroll
-      for (int c = 0; c < kNC; ++c) {
+      for (int q = 0; q < kR; ++q) {
+        F2 sum = 0ull;
 #pragma unroll
-        for (int i = 0; i < 8; ++i) z[c][i] = 0.0f;
-        if (at.n[c] > 0) {
-          if (kVec) sz.get(c, stage, z[c]);
-          else load8<Act, kVec>(p.z, e + at.col[c], at.n[c], at.stride, z[c]);
+        for (int c = 0; c < kNC; ++c) {
+          if (!here(q, c)) continue;
+          F2 z[4];
+          get_act(sz, p.z, q, c, z);
+#pragma unroll
+          for (int i = 0; i < 4; ++i) sum = fma2(z[i], z[i], sum);
         }
+        s[q] = lanes_sum(sum);
       }
-      if (p.post) {
-#pragma unroll
-        for (int c = 0; c < kNC; ++c)
-#pragma unroll
-          for (int i = 0; i < 8; ++i) s[0] = fmaf(z[c][i], z[c][i], s[0]);
-        team_sum(s, at, buf, turn);
-        gate *= rsqrtf(fmaf(s[0], inv_h, p.eps));
-        s[0] = 0.0f;
-      }
-#pragma unroll
-      for (int c = 0; c < kNC; ++c) {
-        if (full && at.n[c] > 0) {
-          float g[8];
-          if (kVec) sg.get(c, stage, g);
-          else load8<Act, kVec>(p.gate, e + at.col[c], at.n[c], at.stride, g);
-#pragma unroll
-          for (int i = 0; i < 8; ++i) z[c][i] *= g[i];
-        }
-#pragma unroll
-        for (int i = 0; i < 8; ++i) r[c][i] = 0.0f;
-        if (at.n[c] == 0) continue;
-        if (kVec) sx.get(c, stage, r[c]);
-        else load8<Res, kVec>(p.x, e + at.col[c], at.n[c], at.stride, r[c]);
-#pragma unroll
-        for (int i = 0; i < 8; ++i) r[c][i] = fmaf(gate * z[c][i], wq[c][i], r[c][i]);
-        store8<Res, kVec>(p.r, e + at.col[c], at.n[c], at.stride, r[c]);
-      }
-    } else {
-#pragma unroll
-      for (int c = 0; c < kNC; ++c) {
-#pragma unroll
-        for (int i = 0; i < 8; ++i) r[c][i] = 0.0f;
-        if (at.n[c] == 0) continue;
-        if (kVec) sx.get(c, stage, r[c]);
-        else load8<Res, kVec>(p.x, e + at.col[c], at.n[c], at.stride, r[c]);
-      }
-    }
-    if (p.pre) {
-#pragma unroll
-      for (int c = 0; c < kNC; ++c)
-#pragma unroll
-        for (int i = 0; i < 8; ++i) s[0] = fmaf(r[c][i], r[c][i], s[0]);
       team_sum(s, at, buf, turn);
-      const float f = rsqrtf(fmaf(s[0], inv_h, p.eps));
+#pragma unroll
+      for (int q = 0; q < kR; ++q) gate[q] *= rsqrtf(fmaf(s[q], inv_h, p.eps));
+    }
+    F2 r[kR][kNC][4];
+#pragma unroll
+    for (int q = 0; q < kR; ++q) {
+      F2 sum = 0ull;
+      const F2 g2 = pack2(gate[q], gate[q]);
 #pragma unroll
       for (int c = 0; c < kNC; ++c) {
-        if (at.n[c] == 0) continue;
 #pragma unroll
-        for (int i = 0; i < 8; ++i) r[c][i] *= f * pre[c][i];
-        store8<Act, kVec>(p.u, e + at.col[c], at.n[c], at.stride, r[c]);
+        for (int i = 0; i < 4; ++i) r[q][c][i] = 0ull;
+        if (!here(q, c)) continue;
+        get_x(q, c, r[q][c]);
+        if (p.z) {
+          F2 z[4];
+          get_act(sz, p.z, q, c, z);
+          if (full) {
+            F2 g[4];
+            get_act(sg, p.gate, q, c, g);
+#pragma unroll
+            for (int i = 0; i < 4; ++i) z[i] = mul2(z[i], g[i]);
+          }
+#pragma unroll
+          for (int i = 0; i < 4; ++i) r[q][c][i] = fma2(mul2(g2, z[i]), wq[c][i], r[q][c][i]);
+          store8<Res, kVec>(p.r, (row + q * step) * p.H + at.col[c], at.n[c], at.stride, r[q][c]);
+        }
+#pragma unroll
+        for (int i = 0; i < 4; ++i) sum = fma2(r[q][c][i], r[q][c][i], sum);
+      }
+      s[q] = lanes_sum(sum);
+    }
+    if (!p.pre) continue;
+    team_sum(s, at, buf, turn);
+#pragma unroll
+    for (int q = 0; q < kR; ++q) {
+      const float f = rsqrtf(fmaf(s[q], inv_h, p.eps));
+      const F2 f2 = pack2(f, f);
+#pragma unroll
+      for (int c = 0; c < kNC; ++c) {
+        if (!here(q, c)) continue;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) r[q][c][i] = mul2(r[q][c][i], mul2(f2, pre[c][i]));
+        store8<Act, kVec>(p.u, (row + q * step) * p.H + at.col[c], at.n[c], at.stride, r[q][c]);
       }
     }
   }
@@ -400,24 +462,26 @@ __global__ void __launch_bounds__(kNormThreads, 1) block_norm_kernel(const NormA
 // scale post, which gives both the row's gate gradient and the mean in dz.
 // Each thread keeps its columns' sums over the rows of its CTA in registers;
 // the CTAs' sums are added in a fixed order by a second kernel.
-template <typename Res, typename Act, int kNC, bool kVec>
+template <typename Res, typename Act, int kNC, bool kVec, bool kFull>
 __global__ void __launch_bounds__(kBackThreads, 1) block_norm_backward_kernel(const NormArgs p) {
   __shared__ TeamBuf buf;
   extern __shared__ __align__(16) uint8_t ring[];
   const Place<kNC, kVec> at(p);
   const int H = p.H;
   const float inv_h = 1.0f / (float)H;
-  const bool full = p.gate_kind == kGateFull;
   int turn = 0;
-  float s_pre[kNC][8], s_c[kNC][8];
+  F2 s_pre[kNC][4], s_c[kNC][4];
 #pragma unroll
   for (int c = 0; c < kNC; ++c)
 #pragma unroll
-    for (int i = 0; i < 8; ++i) s_pre[c][i] = s_c[c][i] = 0.0f;
+    for (int i = 0; i < 4; ++i) s_pre[c][i] = s_c[c][i] = 0ull;
 
   const uint32_t act_bytes = Slot<Act>::bytes(blockDim.x, kNC);
   const uint32_t res_bytes = Slot<Res>::bytes(blockDim.x, kNC);
   uint32_t next = smem_u32(ring) + threadIdx.x * 16;
+  // the first norm's weights stand in slots too: registers are short
+  const Slot<float> sw{next};
+  next += Slot<float>::bytes(blockDim.x, kNC);
   const uint32_t ring0 = next;
   const Slot<Res> sr{next};
   if (p.pre) next += res_bytes;
@@ -428,7 +492,7 @@ __global__ void __launch_bounds__(kBackThreads, 1) block_norm_backward_kernel(co
   const Slot<Act> sz{next};
   if (p.z) next += act_bytes;
   const Slot<Act> sg{next};
-  if (full) next += act_bytes;
+  if (kFull) next += act_bytes;
   const uint32_t stage_bytes = next - ring0;
   auto ask = [&](int64_t row, int s) {
     if (row < p.T) {
@@ -442,16 +506,19 @@ __global__ void __launch_bounds__(kBackThreads, 1) block_norm_backward_kernel(co
         }
         if (p.z) sz.ask(p.z, e, c, s * stage_bytes);
         if (p.dr) sd.ask(p.dr, e, c, s * stage_bytes);
-        if (full) sg.ask(p.gate, e, c, s * stage_bytes);
+        if (kFull) sg.ask(p.gate, e, c, s * stage_bytes);
       }
     }
     ask_commit();
   };
   if (kVec)
     for (int s = 0; s < p.stages - 1; ++s) ask(at.first() + s * at.step(), s);
-  float pre[kNC][8], wq[kNC][8];
-  pre_weights<Act>(p, at, pre);
-  if (p.z) branch_weights<Act>(p, at, wq);
+  F2 wq[kNC][4];
+  pre_weights<Act>(p, at, wq);
+#pragma unroll
+  for (int c = 0; c < kNC; ++c) sw.put(c, wq[c]);
+  branch_weights<Act>(p, at, wq);
+  cudaTriggerProgrammaticLaunchCompletion();
   int slot = 0;
   for (int64_t row = at.first(); row < p.T; row += at.step()) {
     const int64_t e0 = row * H;
@@ -464,41 +531,43 @@ __global__ void __launch_bounds__(kBackThreads, 1) block_norm_backward_kernel(co
       ask_wait(ahead);
       slot = slot + 1 == p.stages ? 0 : slot + 1;
     }
-    auto get = [&](auto s, const void* g, int c, float (&v)[8]) {
-      using S = decltype(s);
+    auto get = [&](const auto& s, const void* g, int c, F2 (&v)[4]) {
+      using S = std::decay_t<decltype(s)>;
       if (kVec) s.get(c, stage, v);
       else if constexpr (std::is_same_v<S, Slot<Res>>)
         load8<Res, kVec>(g, e0 + at.col[c], at.n[c], at.stride, v);
       else
         load8<Act, kVec>(g, e0 + at.col[c], at.n[c], at.stride, v);
     };
-    float s[3] = {0.0f, 0.0f, 0.0f};
+    F2 sum[3] = {0ull, 0ull, 0ull};
 #pragma unroll
     for (int c = 0; c < kNC; ++c) {
       if (at.n[c] == 0) continue;
       if (p.pre) {
-        float r[8], du[8];
+        F2 r[4], du[4], w[4];
         get(sr, p.x, c, r);
         get(su, p.du, c, du);
+        sw.get(c, 0, w);
 #pragma unroll
-        for (int i = 0; i < 8; ++i) {
-          s[0] = fmaf(r[i], r[i], s[0]);
-          s[1] = fmaf(du[i] * pre[c][i], r[i], s[1]);
+        for (int i = 0; i < 4; ++i) {
+          sum[0] = fma2(r[i], r[i], sum[0]);
+          sum[1] = fma2(mul2(du[i], w[i]), r[i], sum[1]);
         }
       }
       if (p.post) {
-        float z[8];
+        F2 z[4];
         get(sz, p.z, c, z);
 #pragma unroll
-        for (int i = 0; i < 8; ++i) s[2] = fmaf(z[i], z[i], s[2]);
+        for (int i = 0; i < 4; ++i) sum[2] = fma2(z[i], z[i], sum[2]);
       }
     }
+    float s[3] = {lanes_sum(sum[0]), lanes_sum(sum[1]), lanes_sum(sum[2])};
     if (p.pre || p.post) team_sum(s, at, buf, turn);
     const float R = rsqrtf(fmaf(s[0], inv_h, p.eps));
     const float r_part = -R * R * R * (s[1] * inv_h);  // of r in dx
     const float Z = p.post ? rsqrtf(fmaf(s[2], inv_h, p.eps)) : 1.0f;
-    float e[kNC][8];  // dx, then w e (times a full gate)
-    float t[1] = {0.0f};
+    F2 e[kNC][4];  // dx, then w e (times a full gate)
+    F2 t2 = 0ull;
 #pragma unroll
     for (int c = 0; c < kNC; ++c) {
       if (at.n[c] == 0) continue;
@@ -506,61 +575,66 @@ __global__ void __launch_bounds__(kBackThreads, 1) block_norm_backward_kernel(co
         get(sd, p.dr, c, e[c]);
       } else {
 #pragma unroll
-        for (int i = 0; i < 8; ++i) e[c][i] = 0.0f;
+        for (int i = 0; i < 4; ++i) e[c][i] = 0ull;
       }
       if (p.pre) {
-        float r[8], du[8];
+        const F2 R2 = pack2(R, R), rp2 = pack2(r_part, r_part);
+        F2 r[4], du[4], w[4];
         get(sr, p.x, c, r);
         get(su, p.du, c, du);
+        sw.get(c, 0, w);
 #pragma unroll
-        for (int i = 0; i < 8; ++i) {
-          s_pre[c][i] = fmaf(du[i], r[i] * R, s_pre[c][i]);
-          e[c][i] = fmaf(du[i] * pre[c][i], R, fmaf(r[i], r_part, e[c][i]));
+        for (int i = 0; i < 4; ++i) {
+          const F2 d = mul2(du[i], R2);
+          s_pre[c][i] = fma2(d, r[i], s_pre[c][i]);
+          e[c][i] = fma2(d, w[i], fma2(r[i], rp2, e[c][i]));
         }
         store8<Res, kVec>(p.dx, e0 + at.col[c], at.n[c], at.stride, e[c]);
       }
       if (!p.z) continue;
-      float z[8];
+      F2 z[4];
       get(sz, p.z, c, z);
-      if (full) {
-        float g[8], dg[8];
+      if (kFull) {
+        const F2 Z2 = pack2(Z, Z);
+        F2 g[4], dg[4];
         get(sg, p.gate, c, g);
 #pragma unroll
-        for (int i = 0; i < 8; ++i) {
-          const float y = z[i] * Z;
-          s_c[c][i] = fmaf(e[c][i] * g[i], y, s_c[c][i]);
-          e[c][i] *= wq[c][i];
-          dg[i] = e[c][i] * y;
-          e[c][i] *= g[i];
-          t[0] = fmaf(e[c][i], z[i], t[0]);
+        for (int i = 0; i < 4; ++i) {
+          const F2 y = mul2(z[i], Z2);
+          s_c[c][i] = fma2(mul2(e[c][i], g[i]), y, s_c[c][i]);
+          e[c][i] = mul2(e[c][i], wq[c][i]);
+          dg[i] = mul2(e[c][i], y);
+          e[c][i] = mul2(e[c][i], g[i]);
+          t2 = fma2(e[c][i], z[i], t2);
         }
         store8<Act, kVec>(p.dgate, e0 + at.col[c], at.n[c], at.stride, dg);
       } else {
-        const float zg = Z * row_gate;
+        const F2 zg2 = pack2(Z * row_gate, Z * row_gate);
 #pragma unroll
-        for (int i = 0; i < 8; ++i) {
-          s_c[c][i] = fmaf(e[c][i], z[i] * zg, s_c[c][i]);
-          e[c][i] *= wq[c][i];
-          t[0] = fmaf(e[c][i], z[i], t[0]);
+        for (int i = 0; i < 4; ++i) {
+          s_c[c][i] = fma2(e[c][i], mul2(z[i], zg2), s_c[c][i]);
+          e[c][i] = mul2(e[c][i], wq[c][i]);
+          t2 = fma2(e[c][i], z[i], t2);
         }
       }
     }
     if (!p.z) continue;
     float z_part = 0.0f;  // of z in dz
     if (p.post || p.gate_kind == kGateRow) {
+      float t[1] = {lanes_sum(t2)};
       team_sum(t, at, buf, turn);
       if (p.gate_kind == kGateRow && at.wid == 0 && at.lane == 0)
         static_cast<float*>(p.dgate)[row] = t[0] * Z;
       if (p.post) z_part = -Z * Z * Z * row_gate * (t[0] * inv_h);
     }
-    const float zg = Z * row_gate;
+    const F2 zp2 = pack2(z_part, z_part), zg2 = pack2(Z * row_gate, Z * row_gate);
 #pragma unroll
     for (int c = 0; c < kNC; ++c) {
       if (at.n[c] == 0) continue;
-      float z[8];
+      F2 z[4];
       get(sz, p.z, c, z);
 #pragma unroll
-      for (int i = 0; i < 8; ++i) e[c][i] = fmaf(e[c][i], zg, z[i] * z_part);
+      for (int i = 0; i < 4; ++i) e[c][i] = fma2(e[c][i], zg2, mul2(z[i], zp2));
       store8<Act, kVec>(p.dz, e0 + at.col[c], at.n[c], at.stride, e[c]);
     }
   }
@@ -577,8 +651,11 @@ __global__ void __launch_bounds__(kBackThreads, 1) block_norm_backward_kernel(co
         for (int i = 0; i < 8; ++i)
           if (i < at.n[c]) {
             const int h = at.col[c] + i * at.stride;
-            sum[h] = s_pre[c][i] + (t > 0 ? sum[h] : 0.0f);
-            sum[H + h] = s_c[c][i] + (t > 0 ? sum[H + h] : 0.0f);
+            float a[2], b[2];
+            unpack_f32x2(s_pre[c][i / 2], a[0], a[1]);
+            unpack_f32x2(s_c[c][i / 2], b[0], b[1]);
+            sum[h] = a[i % 2] + (t > 0 ? sum[h] : 0.0f);
+            sum[H + h] = b[i % 2] + (t > 0 ? sum[H + h] : 0.0f);
           }
     }
     __syncthreads();
@@ -605,6 +682,7 @@ __global__ void __launch_bounds__(1024) block_norm_columns_kernel(const ColumnAr
   const int x = threadIdx.x & 31, y = threadIdx.x >> 5;
   int h = blockIdx.x * 32 + x;
   float a = 0.0f, b = 0.0f;
+  cudaGridDependencySynchronize();
   if (h < p.H) {
 #pragma unroll 4
     for (int i = y; i < p.parts; i += 32) {
@@ -636,20 +714,22 @@ __global__ void __launch_bounds__(1024) block_norm_columns_kernel(const ColumnAr
 
 // How rows are spread over threads, and the rows asked for ahead.
 struct Plan {
-  int nc, team_warps, teams, threads, stages;
+  int nc, rows, team_warps, teams, threads, stages;
   bool vec;
   size_t smem;
 };
 
-// 8 columns a thread up to 8192 columns, 16 above: the weights and column sums
-// of so many fit in registers beside the row's. One CTA per SM of up to 1024
-// threads, with fewer teams where there are not rows enough for every SM's.
-// per_column: bytes of the row tensors per column.
+// 8 columns a thread up to 7168 columns (the backward: 4096), 16 up to 8192
+// and 32 above: the weights and column sums of so many fit in registers
+// beside the row's. One CTA per SM, with fewer teams where there are not rows
+// enough for every SM's; the forward takes two rows a step where every team
+// has more. per_column: bytes of the row tensors per column.
 Plan plan_of(int64_t T, int H, int per_column, bool vec, int sms, bool backward) {
   Plan q;
   const int chunks = (H + 7) / 8;
-  const int threads = backward ? kBackThreads : kNormThreads;
-  q.nc = chunks <= threads ? 1 : chunks <= 2 * threads ? 2 : 4;
+  const int most1 = backward ? kBackThreads : kNormThreads;
+  q.nc = chunks <= most1 ? 1 : chunks <= 2 * kBackThreads ? 2 : 4;
+  const int threads = q.nc == 1 ? most1 : kBackThreads;
   q.team_warps = (chunks + 32 * q.nc - 1) / (32 * q.nc);
   const int fit = threads / 32 / q.team_warps;
   // teams of more than a warp meet at a barrier of their own, of which there are 15
@@ -657,10 +737,14 @@ Plan plan_of(int64_t T, int H, int per_column, bool vec, int sms, bool backward)
   const int64_t want = (T + sms - 1) / sms;
   q.teams = (int)(want < most ? want : most);
   q.threads = 32 * q.team_warps * q.teams;
-  const size_t stage = (size_t)q.threads * q.nc * 8 * per_column;
-  q.vec = vec && stage <= kRing;
-  q.stages = q.vec ? (int)(kRing / stage < kMaxStages ? kRing / stage : kMaxStages) : 0;
-  q.smem = q.stages * stage;
+  const size_t row = (size_t)q.threads * q.nc * 8 * per_column;
+  q.rows = !backward && vec && T > (int64_t)q.teams * sms && 4 * row <= kRing && q.nc < 4 ? 2 : 1;
+  const size_t stage = q.rows * row;
+  // the backward's first weights are in shared memory as well
+  const size_t fixed = backward ? (size_t)q.threads * q.nc * 8 * 4 : 0, room = kRing - fixed;
+  q.vec = vec && stage <= room;
+  q.stages = q.vec ? (int)(room / stage < kMaxStages ? room / stage : kMaxStages) : 0;
+  q.smem = fixed + q.stages * stage;
   // the backward's column sums of the teams meet in the same memory
   if (backward && q.smem < (size_t)8 * H) q.smem = (size_t)8 * H;
   return q;
@@ -681,15 +765,13 @@ cudaError_t by_types(int res, int act, F&& f) {
   return cudaErrorInvalidValue;
 }
 
-template <bool kBackward, typename F>
+template <typename F>
 cudaError_t by_plan(const Plan& q, F&& f) {
   using std::integral_constant;
   auto go = [&](auto v) {
     if (q.nc == 1) return f(integral_constant<int, 1>{}, v);
-    if constexpr (kBackward) {
-      if (q.nc == 4) return f(integral_constant<int, 4>{}, v);
-    }
-    return f(integral_constant<int, 2>{}, v);
+    if (q.nc == 2) return f(integral_constant<int, 2>{}, v);
+    return f(integral_constant<int, 4>{}, v);
   };
   return q.vec ? go(std::true_type{}) : go(std::false_type{});
 }
@@ -773,15 +855,22 @@ int moe_block_norm(int64_t T, int32_t H, int32_t res_type, int32_t act_type, int
   const cudaError_t e = by_types(res_type, act_type, [&](auto res, auto act) {
     using Res = decltype(res);
     using Act = decltype(act);
-    return by_plan<false>(q, [&](auto nc, auto vec) {
-      auto* kernel = block_norm_kernel<Res, Act, decltype(nc)::value, decltype(vec)::value>;
-      static DeviceOnce once;
-      const cudaError_t r0 = allow_smem(once, kernel);
-      if (r0 != cudaSuccess) return r0;
-      const int64_t need = (T + q.teams - 1) / q.teams;
-      kernel<<<(unsigned)(need < sms ? need : sms), q.threads, q.smem,
-               static_cast<cudaStream_t>(stream)>>>(a);
-      return cudaGetLastError();
+    return by_plan(q, [&](auto nc, auto vec) {
+      constexpr int kNC = decltype(nc)::value;
+      constexpr bool kVec = decltype(vec)::value;
+      auto go = [&](auto* kernel, DeviceOnce& once) {
+        const cudaError_t r0 = allow_smem(once, kernel);
+        if (r0 != cudaSuccess) return r0;
+        const int64_t need = (T + q.teams - 1) / q.teams;
+        kernel<<<(unsigned)(need < sms ? need : sms), q.threads, q.smem,
+                 static_cast<cudaStream_t>(stream)>>>(a);
+        return cudaGetLastError();
+      };
+      static DeviceOnce once1, once2;
+      if constexpr (kVec && kNC < 4) {
+        if (q.rows == 2) return go(block_norm_kernel<Res, Act, kNC, 2, kVec>, once2);
+      }
+      return go(block_norm_kernel<Res, Act, kNC, 1, kVec>, once1);
     });
   });
   return cuda_status(e);
@@ -854,11 +943,14 @@ int moe_block_norm_backward(int64_t T, int32_t H, int32_t res_type, int32_t act_
   const cudaError_t e = by_types(res_type, act_type, [&](auto res, auto act) {
     using Res = decltype(res);
     using Act = decltype(act);
-    return by_plan<true>(q, [&](auto nc, auto vec) {
-      auto* kernel = block_norm_backward_kernel<Res, Act, decltype(nc)::value,
-                                                decltype(vec)::value>;
-      static DeviceOnce once;
-      const cudaError_t r0 = allow_smem(once, kernel);
+    return by_plan(q, [&](auto nc, auto vec) {
+      constexpr int kNC = decltype(nc)::value;
+      constexpr bool kVec = decltype(vec)::value;
+      const bool full = gate_kind == kGateFull;
+      auto* kernel = full ? block_norm_backward_kernel<Res, Act, kNC, kVec, true>
+                          : block_norm_backward_kernel<Res, Act, kNC, kVec, false>;
+      static DeviceOnce once[2];
+      const cudaError_t r0 = allow_smem(once[full], kernel);
       if (r0 != cudaSuccess) return r0;
       int64_t grid = (T + q.teams - 1) / q.teams;
       if (grid > sms) grid = sms;
@@ -868,8 +960,7 @@ int moe_block_norm_backward(int64_t T, int32_t H, int32_t res_type, int32_t act_
       if (r1 != cudaSuccess || (!pre && !post && !scale)) return r1;
       const ColumnArgs c{a.part, (int32_t)grid, H, a.w_f32, alpha, post, scale,
                          pre ? dpre : nullptr, post ? dpost : nullptr, scale ? dscale : nullptr};
-      block_norm_columns_kernel<Act><<<(H + 31) / 32, 1024, 0, s>>>(c);
-      return cudaGetLastError();
+      return launch_dependent(block_norm_columns_kernel<Act>, (unsigned)((H + 31) / 32), 1024, 0, s, c);
     });
   });
   return cuda_status(e);

@@ -34,6 +34,7 @@ constexpr int kMaxTensors = 1024;  // per launch: the table travels as kernel ar
 // elements before its first 128-byte boundary.
 template <int kCap>
 struct GradTable {
+  static constexpr int cap = kCap;
   const void* g[kCap];
   void* out[kCap];
   int64_t size[kCap];
@@ -187,6 +188,7 @@ __global__ void __launch_bounds__(kClipThreads, kCtasPerSm)
   __shared__ double red[kClipThreads / 32];
   const int total = t.chunk0[t.n];
   double sum = 0.0;
+  cudaTriggerProgrammaticLaunchCompletion();
   int i = (int)blockIdx.x < total ? tensor_of(t, blockIdx.x) : 0;
   for (int c = blockIdx.x; c < total; c += gridDim.x) {
     while (c >= t.chunk0[i + 1]) ++i;
@@ -242,6 +244,7 @@ __global__ void __launch_bounds__(kClipThreads, kCtasPerSm)
   __shared__ double red[kClipThreads / 32];
   __shared__ float factor;
   double sum = 0.0;
+  cudaGridDependencySynchronize();
   for (int j = threadIdx.x; j < kParts; j += kClipThreads) sum += partials[j];
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
@@ -385,8 +388,9 @@ int moe_grad_clip(const moe_grad_list* list, const double* partials, float max_n
   auto go = [&](const auto& t, bool) {
     const int total = t.chunk0[t.n];
     const int grid = total < 1 ? 1 : std::min(most, total);
-    grad_clip_kernel<<<grid, kClipThreads, 0, s>>>(t, partials, max_norm, norm);
-    return cudaGetLastError();
+    using Table = std::decay_t<decltype(t)>;
+    void (*kernel)(const Table, const double*, float, float*) = grad_clip_kernel<Table::cap>;
+    return launch_dependent(kernel, (unsigned)grid, kClipThreads, 0, s, t, partials, max_norm, norm);
   };
   return cuda_status(over_list(*list, most, go));
 }

@@ -39,6 +39,27 @@ struct Carver {
   }
 };
 
+// Launches a kernel that may start while the one before it on the stream ends
+// (programmatic dependent launch): it must call cudaGridDependencySynchronize()
+// before it touches memory that the earlier kernel writes, and the earlier
+// one may let it start with cudaTriggerProgrammaticLaunchCompletion(). Saves
+// the launch latency between two short kernels; graphs capture it as well.
+template <typename... P, typename... A>
+inline cudaError_t launch_dependent(void (*kernel)(P...), unsigned grid, unsigned block, size_t smem,
+                                    cudaStream_t stream, A&&... args) {
+  cudaLaunchAttribute attr{};
+  attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr.val.programmaticStreamSerializationAllowed = 1;
+  cudaLaunchConfig_t cfg{};
+  cfg.gridDim = dim3(grid);
+  cfg.blockDim = dim3(block);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = stream;
+  cfg.attrs = &attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, kernel, P(args)...);
+}
+
 // An NVTX range over a host scope (entry points and the forward's stages), for
 // timeline profilers; without a profiler attached the calls do nothing. The
 // range covers the host-side enqueue, not the kernels' execution.
