@@ -342,9 +342,10 @@ def _need(t: torch.Tensor | None, dtype: torch.dtype, shape: tuple, device: int,
 
 
 def _device(t: torch.Tensor, name: str) -> int:
-    if not t.is_cuda:
+    dev = t.get_device()
+    if dev < 0:
         raise ValueError(f"{name} must be a CUDA tensor")
-    return t.get_device()
+    return dev
 
 
 def _run(name: str, device: int, stream, *args) -> None:
@@ -420,26 +421,16 @@ def moe_grouped_wgrad(dy, x, group_rows, group_start, dw, accumulate: bool = Fal
          1 if accumulate else 0, st)
 
 
-def _norm_common(x, act, z, gate, weights):
-    """(T, H, device, res type, act type, weight type, gate kind, pointers of
-    z, gate, pre, post, scale) of a block norm's common arguments; `act`: a
-    tensor of the block's type."""
-    if x.dim() != 2:
-        raise ValueError("the rows must be two-dimensional")
-    T, H = x.shape
-    dev = _device(x, "x")
-    zp = _need(z, act.dtype, (T, H), dev, "z")
-    kind, gp = 0, None
-    if gate is not None:
-        if gate.dim() == 1:
-            kind, gp = 1, _need(gate, torch.float32, (T,), dev, "gate")
-        else:
-            kind, gp = 2, _need(gate, act.dtype, (T, H), dev, "gate")
-    given = [(n, w) for n, w in weights if w is not None]
-    wtype = given[0][1].dtype if given else act.dtype
-    wp = [_need(w, wtype, (H,), dev, n) for n, w in weights]
-    wt = _type(given[0][1], given[0][0]) if given else _type(act, "z")
-    return T, H, dev, _type(x, "x"), _type(act, "z"), wt, kind, [zp, gp] + wp
+def _norm_types(x, act, pre, post, scale):
+    """Type codes of the residual stream, the block and the weights, which must
+    agree among themselves."""
+    w = pre if pre is not None else post if post is not None else scale
+    wt = act.dtype if w is None else w.dtype
+    try:
+        return wt, TYPES[x.dtype], TYPES[act.dtype], TYPES[wt]
+    except KeyError:
+        raise ValueError(f"bfloat16, float16 or float32 tensors are needed, got {x.dtype}, "
+                         f"{act.dtype} and weights of {wt}") from None
 
 
 def moe_block_norm(x, eps: float, pre_weight=None, u=None, z=None, post_weight=None, gate=None,
@@ -451,16 +442,27 @@ def moe_block_norm(x, eps: float, pre_weight=None, u=None, z=None, post_weight=N
     weights and scale [H] of z's type or float32. r may be x and u may be z."""
     if (z is None) != (r is None) or (pre_weight is None) != (u is None):
         raise ValueError("r goes with z, and u with pre_weight")
-    act = z if z is not None else u
+    act = u if z is None else z
     if act is None:
         raise ValueError("nothing to compute: give z and r, pre_weight and u, or both")
-    T, H, dev, rt, at, wt, kind, (zp, gp, pre, post, sc) = _norm_common(
-        x, act, z, gate, [("pre_weight", pre_weight), ("post_weight", post_weight),
-                          ("scale", scale)])
-    xp = _need(x, x.dtype, (T, H), dev, "x")
-    _run("moe_block_norm", dev, stream, T, H, rt, at, wt, kind, float(alpha), float(eps), xp, zp,
-         gp, pre, post, sc, _need(r, x.dtype, (T, H), dev, "r"),
-         _need(u, act.dtype, (T, H), dev, "u"))
+    shape = x.shape
+    if len(shape) != 2:
+        raise ValueError("the rows must be two-dimensional")
+    dev = _device(x, "x")
+    wt, rc, ac, wc = _norm_types(x, act, pre_weight, post_weight, scale)
+    T, H = shape
+    kind = 0 if gate is None else 1 if gate.dim() == 1 else 2
+    res, at, cols = x.dtype, act.dtype, (H,)
+    _run("moe_block_norm", dev, stream, T, H, rc, ac, wc, kind, alpha, eps,
+         _need(x, res, shape, dev, "x"),
+         None if z is None else _need(z, at, shape, dev, "z"),
+         None if gate is None else _need(gate, torch.float32, (T,), dev, "gate") if kind == 1
+         else _need(gate, at, shape, dev, "gate"),
+         None if pre_weight is None else _need(pre_weight, wt, cols, dev, "pre_weight"),
+         None if post_weight is None else _need(post_weight, wt, cols, dev, "post_weight"),
+         None if scale is None else _need(scale, wt, cols, dev, "scale"),
+         None if r is None else _need(r, res, shape, dev, "r"),
+         None if u is None else _need(u, at, shape, dev, "u"))
 
 
 def moe_block_norm_backward_workspace_size(H: int) -> int:
@@ -475,30 +477,43 @@ def moe_block_norm_backward(r, eps: float, ws, dr=None, du=None, pre_weight=None
     pre_weight; without it the gradient of x is dr itself), dz like z, dgate
     like gate, dpre, dpost and dscale float32 [H]. ws: uint8, at least
     moe_block_norm_backward_workspace_size(H) bytes."""
-    for a, b, what in ((z, dz, "dz goes with z"), (gate, dgate, "dgate with gate"),
-                       (scale, dscale, "dscale with scale"), (pre_weight, dpre, "dpre with pre_weight"),
-                       (post_weight, dpost, "dpost with post_weight"), (pre_weight, dx, "dx with pre_weight"),
-                       (pre_weight, du, "du with pre_weight")):
-        if (a is None) != (b is None):
-            raise ValueError(what)
-    act = z if z is not None else du
+    if (z is None) != (dz is None) or (gate is None) != (dgate is None):
+        raise ValueError("dz goes with z, and dgate with gate")
+    if (scale is None) != (dscale is None) or (post_weight is None) != (dpost is None):
+        raise ValueError("dscale goes with scale, and dpost with post_weight")
+    given = pre_weight is not None
+    if (dpre is not None) != given or (dx is not None) != given or (du is not None) != given:
+        raise ValueError("du, dx and dpre go with pre_weight")
+    act = du if z is None else z
     if act is None:
         raise ValueError("nothing to compute: give z, du or both")
-    T, H, dev, rt, at, wt, kind, (zp, gp, pre, post, sc) = _norm_common(
-        r, act, z, gate, [("pre_weight", pre_weight), ("post_weight", post_weight),
-                          ("scale", scale)])
-    f32 = torch.float32
-    gate_t, gate_s = (None, None) if gate is None else (gate.dtype, tuple(gate.shape))
-    rp = _need(r, r.dtype, (T, H), dev, "r")
-    wsp = _ptr(ws, torch.uint8, "ws")
+    shape = r.shape
+    if len(shape) != 2:
+        raise ValueError("the rows must be two-dimensional")
+    dev = _device(r, "r")
+    wt, rc, ac, wc = _norm_types(r, act, pre_weight, post_weight, scale)
+    T, H = shape
+    kind = 0 if gate is None else 1 if gate.dim() == 1 else 2
+    res, at, cols, f32 = r.dtype, act.dtype, (H,), torch.float32
+    gt, gs = (f32, (T,)) if kind == 1 else (at, shape)
     if ws.get_device() != dev:
         raise ValueError(f"ws must be on cuda:{dev}, got {ws.device}")
-    _run("moe_block_norm_backward", dev, stream, T, H, rt, at, wt, kind, float(alpha), float(eps),
-         rp, zp, gp, pre, post, sc, _need(dr, r.dtype, (T, H), dev, "dr"),
-         _need(du, act.dtype, (T, H), dev, "du"), _need(dx, r.dtype, (T, H), dev, "dx"),
-         _need(dz, act.dtype, (T, H), dev, "dz"), _need(dgate, gate_t, gate_s, dev, "dgate"),
-         _need(dpre, f32, (H,), dev, "dpre"), _need(dpost, f32, (H,), dev, "dpost"),
-         _need(dscale, f32, (H,), dev, "dscale"), wsp, ws.numel())
+    _run("moe_block_norm_backward", dev, stream, T, H, rc, ac, wc, kind, alpha, eps,
+         _need(r, res, shape, dev, "r"),
+         None if z is None else _need(z, at, shape, dev, "z"),
+         None if gate is None else _need(gate, gt, gs, dev, "gate"),
+         _need(pre_weight, wt, cols, dev, "pre_weight") if given else None,
+         None if post_weight is None else _need(post_weight, wt, cols, dev, "post_weight"),
+         None if scale is None else _need(scale, wt, cols, dev, "scale"),
+         None if dr is None else _need(dr, res, shape, dev, "dr"),
+         _need(du, at, shape, dev, "du") if given else None,
+         _need(dx, res, shape, dev, "dx") if given else None,
+         None if dz is None else _need(dz, at, shape, dev, "dz"),
+         None if dgate is None else _need(dgate, gt, gs, dev, "dgate"),
+         _need(dpre, f32, cols, dev, "dpre") if given else None,
+         None if dpost is None else _need(dpost, f32, cols, dev, "dpost"),
+         None if dscale is None else _need(dscale, f32, cols, dev, "dscale"),
+         _ptr(ws, torch.uint8, "ws"), ws.numel())
 
 
 GRAD_PARTIALS = 1024

@@ -325,8 +325,11 @@ cudaError_t over_tables(const moe_grad_list& l, int ctas, F&& f) {
 
 template <typename F>
 cudaError_t over_list(const moe_grad_list& l, int ctas, F&& f) {
-  return l.n <= 16 ? over_tables<16>(l, ctas, f)
-         : l.n <= 128 ? over_tables<128>(l, ctas, f) : over_tables<kMaxTensors>(l, ctas, f);
+  // the table is copied to the device with every launch: no larger than needed
+  if (l.n <= 16) return over_tables<16>(l, ctas, f);
+  if (l.n <= 128) return over_tables<128>(l, ctas, f);
+  if (l.n <= 512) return over_tables<512>(l, ctas, f);
+  return over_tables<kMaxTensors>(l, ctas, f);
 }
 
 int clip_grid(int sms) { return std::min(kParts, kCtasPerSm * sms); }
