@@ -318,3 +318,35 @@ def test_binding_refuses(capi):
         capi.moe_grouped_matmul(z(10, 60), z(2, 32, 60), i, i, out)
     with pytest.raises(capi.MoeError):  # rows that start off a 16-byte boundary
         capi.moe_grouped_matmul(z(641)[1:].view(10, 64), b, i, i, out)
+
+
+@pytest.mark.parametrize("trans", [True, False])
+@pytest.mark.parametrize("N", [72, 136, 256, 264, 520, 776])
+@pytest.mark.parametrize("out", [None, FP32])
+def test_matmul_long_groups(capi, trans, N, out):
+    # pairs of CTAs, with one and with two accumulators, and tiles of every size
+    check_matmul(capi, [256, 257, 0, 511, 1, 770, 16, 300], 200, N, out_dtype=out, trans=trans,
+                 lead=2, tail=3)
+
+
+def test_matmul_each_row_count(capi):
+    # every number of rows of a group from 0 to 140, all in one call and alone
+    check_matmul(capi, list(range(141)), 72, 136)
+    for rows in (15, 16, 17, 31, 32, 33, 127, 128, 129, 255, 256, 257):
+        check_matmul(capi, [rows], 72, 264)
+
+
+def test_wgrad_long_groups_keep_fp32(capi):
+    """Sums over many rows: segments of 512 rows added in fp32. A segment is off
+    by at most its 32 steps' 2^-22 of its sum of magnitudes in the worst case and
+    far less in the norm; over the whole gradient 2^-20 of its norm is allowed
+    (the plain fp32 product has about 2^-22), however many rows there are."""
+    gen = torch.Generator(device="cuda").manual_seed(6)
+    for counts in ([20000], [513, 3000, 512, 9001]):
+        gr, gs, starts, rows = layout(counts)
+        dy, x = randn(gen, rows, 264), randn(gen, rows, 520)
+        dw = torch.empty(len(counts), 264, 520, device="cuda")
+        capi.moe_grouped_wgrad(dy, x, gr, gs, dw)
+        for g, (s, c) in enumerate(zip(starts, counts)):
+            ref = dy[s:s + c].double().T @ x[s:s + c].double()
+            assert float((dw[g] - ref).norm() / ref.norm()) < 2.0 ** -20
