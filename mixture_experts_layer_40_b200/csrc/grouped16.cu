@@ -233,12 +233,55 @@ MOE_DEV uint64_t smem_desc_mn_sw128(uint32_t smem_addr) {
 constexpr uint64_t kStepK = 32 >> 4;
 constexpr uint64_t kStepMN = 16 * 128 >> 4;
 
+// The producer and the MMA issuer run as whole warps of which one elected lane
+// issues: so their loops stay uniform, and addresses, coordinates and
+// descriptors in uniform registers, which the copy and MMA instructions take
+// (run by a single lane, their instructions bounded small tiles: 620 cycles a
+// k-block).
+MOE_DEV bool elect_one() {
+  uint32_t one;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "elect.sync _|p, 0xffffffff;\n\t"
+      "selp.u32 %0, 1, 0, p;\n\t}"
+      : "=r"(one));
+  return one != 0;
+}
+MOE_DEV int uniform(int v) { return __shfl_sync(0xffffffffu, v, 0); }
+MOE_DEV bool warp_wait(uint32_t bar, uint32_t parity, volatile int* abort, uint32_t* status) {
+  return __all_sync(0xffffffffu, mbar_wait(bar, parity, abort, status));
+}
+
+// A place in the ring of stages.
+template <int kStages, int kStageBytes>
+struct Cursor {
+  uint32_t full, empty;   // this stage's barriers
+  uint32_t offset = 0;    // and its bytes
+  uint32_t phase = 0;
+  int left = kStages;
+  MOE_DEV Cursor(uint32_t full0, uint32_t empty0) : full(full0), empty(empty0) {}
+  MOE_DEV void next() {
+    full += 8;
+    empty += 8;
+    offset += kStageBytes;
+    if (--left == 0) {
+      left = kStages;
+      full -= 8 * kStages;
+      empty -= 8 * kStages;
+      offset = 0;
+      phase ^= 1u;
+    }
+  }
+  MOE_DEV int stage() const { return kStages - left; }
+};
+
 struct TileAt {
   int g, m, n;
 };
 
 // tile -> (group, row tile of the group, column tile), columns fastest: the
-// column tiles of one row tile run side by side and share its rows in L2
+// column tiles of one row tile run side by side and share its rows in L2.
+// Called by whole warps.
 MOE_DEV TileAt tile_at(int tile, const int* prefix, int n_groups, int n_tiles) {
   int lo = 0, hi = n_groups;
   while (hi - lo > 1) {
@@ -247,9 +290,9 @@ MOE_DEV TileAt tile_at(int tile, const int* prefix, int n_groups, int n_tiles) {
   }
   const int local = tile - prefix[lo] * n_tiles;
   TileAt t;
-  t.g = lo;
-  t.m = local / n_tiles;
-  t.n = local - t.m * n_tiles;
+  t.g = uniform(lo);
+  t.m = uniform(local / n_tiles);
+  t.n = uniform(local - t.m * n_tiles);
   return t;
 }
 
@@ -329,7 +372,26 @@ struct MatCfg {
   // accumulators: two tiles of one (the next tile's MMAs run while one is
   // read), or the two of one tile
   static constexpr int tmem_cols = 2 * kNT;
+  // rows of the boxes that fetch less than 128 rows of the groups
+  static constexpr int x_box = kNT >= 128 ? 32 : 16;
+  // a single CTA's tiles may be lower than 128 columns of the output
+  static constexpr bool low = kCtas == 1 && kSub == 1;
 };
+
+// Rates for choosing tiles, per ns: what one SM takes in, and all of HBM (both
+// measured with these kernels).
+constexpr float kSmIn = 60.0f, kHbm = 6450.0f;
+
+// Time of a k-block of a round of `tiles` single-CTA tiles of height h, up to
+// a factor: the SM's own intake, or the share of HBM that the weights need.
+__host__ __device__ inline float low_tile_ns(int h, int x_rows, int64_t tiles, int units) {
+  const float w = (float)(h * kBK * 2), x = (float)(x_rows * kBK * 2);
+  const float active = (float)(tiles < units ? tiles : units);
+  const float in = (w + x) / kSmIn, hbm = w * active / kHbm;
+  return in > hbm ? in : hbm;
+}
+// heights that the loads come in: boxes of 32 weight rows, or of 64 columns
+__host__ __device__ constexpr int low_step(bool k_major) { return k_major ? 32 : 64; }
 static_assert(16 * (32 * 4 + 16) <= 32 * (32 * 2 + 16), "fp32 rows in the turn buffer");
 
 struct RowTile {
@@ -342,8 +404,8 @@ MOE_DEV RowTile row_tile(int start, int rows, int m) {
   const int tiles = (rows + kNT - 1) / kNT;
   const int size = ((rows + tiles - 1) / tiles + 15) & ~15;
   RowTile t;
-  t.first = start + m * size;
-  t.live = min(size, rows - m * size);
+  t.first = uniform(start + m * size);
+  t.live = uniform(min(size, rows - m * size));
   t.cols = (max(t.live, 1) + 15) & ~15;
   return t;
 }
@@ -389,19 +451,21 @@ __global__ void __cluster_dims__(kCtas, 1, 1) __launch_bounds__(128 + 128 * kSub
   const uint32_t tmem_base = sh.tmem_base;
   const int row_tiles = sh.prefix[p.n_groups];
   const int team = blockIdx.x / kCtas, teams = gridDim.x / kCtas;
-  // Output columns per tile. With few tiles the last round would leave most
-  // CTAs idle: tiles of a smaller height, whose loads overlap their
-  // neighbour's rows in L2, fill it.
+  // Output columns per tile. With few tiles a round of tiles of 128 would
+  // leave SMs idle, and each SM takes in only so much: lower tiles spread the
+  // weights over more of them.
   int height = kBM * kCtas * kSub;
-  if (kCtas == 1 && kSub == 1) {
-    int64_t best = -1;
-    for (int h = kBM; h >= kBM / 2; h -= 8) {
-      const int64_t rounds = ((int64_t)row_tiles * ((p.N + h - 1) / h) + teams - 1) / teams;
-      if (rounds > 8) break;  // an idle share under an eighth
-      if (best < 0 || rounds * h < best) {
-        best = rounds * h;
+  if (C::low) {
+    float best = 0.0f;
+    for (int h = kBM; h > 0; h -= low_step(kWay == kForward)) {
+      const int64_t tiles = (int64_t)row_tiles * ((p.N + h - 1) / h);
+      const int64_t rounds = (tiles + teams - 1) / teams;
+      const float cost = (float)rounds * low_tile_ns(h, C::x_box, tiles, teams);
+      if (h == kBM || cost < best) {
+        best = cost;
         height = h;
       }
+      if (rounds > 16) break;  // an idle share under a sixteenth
     }
   }
   const int n_tiles = (p.N + height - 1) / height;
@@ -410,48 +474,57 @@ __global__ void __cluster_dims__(kCtas, 1, 1) __launch_bounds__(128 + 128 * kSub
   const int kb_n = p.kblocks;
 
   if (warp == 0) {
-    if (lane == 0) {
+    {
       // ------------------------------------------------------------ producer
+      const bool elected = elect_one();
       int it = 0;
       bool ok = true;
+      Cursor<C::stages, C::stage_bytes> at(smem_u32(sh.full), smem_u32(sh.empty));
+      // a pair's loads all count on its first CTA's barrier
+      const uint32_t to_leader = kCtas == 2 ? in_leader(at.full) - at.full : 0;
       for (int64_t tile = team; ok && tile < total; tile += teams) {
         const TileAt t = tile_at((int)tile, sh.prefix, p.n_groups, n_tiles);
         const RowTile rt = row_tile<kNT>(sh.start[t.g], sh.rows[t.g], t.m);
         const int half = rt.cols / kCtas;
-        const int pieces = (half + 31) / 32;
+        const int pieces = (half + C::x_box - 1) / C::x_box;
         const bool whole = kNT / kCtas >= 128 && pieces == 4;
+        // the weights' boxes: all of 128 rows, or as many as the height takes
+        const int w_pieces = !C::low ? 1 : kWay == kForward ? (height + 31) / 32 : (height + 63) / 64;
+        const int w_bytes = !C::low ? C::a_bytes : w_pieces * (kWay == kForward ? 32 : 64) * kBK * 2;
         const int row = rt.first + rank * half;
         const int n0 = t.n * height + rank * kBM;
-        const uint32_t bytes = kCtas * (C::a_bytes + pieces * 32 * kBK * 2);
-        for (int kb = 0; kb < kb_n; ++kb, ++it) {
-          const int s = it % C::stages;
-          if (!mbar_wait(smem_u32(&sh.empty[s]), ((uint32_t)(it / C::stages) & 1u) ^ 1u, abort,
-                         p.status)) {
+        const uint32_t bytes = kCtas * (w_bytes + pieces * C::x_box * kBK * 2);
+        for (int k = 0; k < kb_n * kBK; k += kBK, ++it, at.next()) {
+          if (!warp_wait(at.empty, at.phase ^ 1u, abort, p.status)) {
             ok = false;
             break;
           }
-          // a pair's loads all count on its first CTA's barrier
-          uint32_t full = smem_u32(&sh.full[s]);
-          if (rank == 0) mbar_arrive_expect_tx(full, bytes);
-          if (kCtas == 2) full = in_leader(full);
-          const uint32_t sa = ring + s * C::stage_bytes, sb = sa + C::a_bytes;
+          if (!elected) continue;
+          if (rank == 0) mbar_arrive_expect_tx(at.full, bytes);
+          const uint32_t full = at.full + to_leader;
+          const uint32_t sa = ring + at.offset, sb = sa + C::a_bytes;
 #pragma unroll
           for (int u = 0; u < kSub; ++u) {
             const int n = n0 + u * kBM * kCtas;
-            if (kWay == kForward) {
-              load_3d<kCtas>(sa + u * kABytes, &tm_w, kb * kBK, n, t.g, full);
+            if (C::low && kWay == kForward) {
+              for (int i = 0; i < w_pieces; ++i)
+                load_3d<kCtas>(sa + i * 32 * kBK * 2, &tm_w, k, n + i * 32, t.g, full);
+            } else if (C::low) {
+              for (int i = 0; i < w_pieces; ++i)
+                load_3d<kCtas>(sa + i * kBK * 128, &tm_w, n + i * 64, k, t.g, full);
+            } else if (kWay == kForward) {
+              load_3d<kCtas>(sa + u * kABytes, &tm_w, k, n, t.g, full);
             } else {
 #pragma unroll
               for (int i = 0; i < kBM / 64; ++i)
-                load_3d<kCtas>(sa + u * kABytes + i * kBK * 128, &tm_w, n + i * 64, kb * kBK, t.g,
-                               full);
+                load_3d<kCtas>(sa + u * kABytes + i * kBK * 128, &tm_w, n + i * 64, k, t.g, full);
             }
           }
           if (whole) {
-            load_2d<kCtas>(sb, &tm_x, kb * kBK, row, full);
+            load_2d<kCtas>(sb, &tm_x, k, row, full);
           } else {
             for (int i = 0; i < pieces; ++i)
-              load_2d<kCtas>(sb + i * 32 * kBK * 2, &tm_x32, kb * kBK, row + 32 * i, full);
+              load_2d<kCtas>(sb + i * C::x_box * kBK * 2, &tm_x32, k, row + C::x_box * i, full);
           }
         }
       }
@@ -464,10 +537,15 @@ __global__ void __cluster_dims__(kCtas, 1, 1) __launch_bounds__(128 + 128 * kSub
       }
     }
   } else if (warp == 1) {
-    if (lane == 0 && rank == 0) {
+    if (rank == 0) {
       // ------------------------------------------------------------ MMA issuer
+      const bool elected = elect_one();
       int it = 0, used = 0;
       bool ok = true;
+      Cursor<C::stages, C::stage_bytes> at(smem_u32(sh.full), smem_u32(sh.empty));
+      const uint64_t desc_w = kWay == kForward ? smem_desc_sw128(ring) : smem_desc_mn_sw128(ring);
+      const uint64_t desc_x = smem_desc_sw128(ring + C::a_bytes);
+      constexpr uint64_t step_w = kWay == kForward ? kStepK : kStepMN;
       for (int64_t tile = team; ok && tile < total; tile += teams, ++used) {
         const TileAt t = tile_at((int)tile, sh.prefix, p.n_groups, n_tiles);
         const RowTile rt = row_tile<kNT>(sh.start[t.g], sh.rows[t.g], t.m);
@@ -475,36 +553,34 @@ __global__ void __cluster_dims__(kCtas, 1, 1) __launch_bounds__(128 + 128 * kSub
         // accumulators in use: tile by tile in turn, or both by each tile
         const int buf = kSub == 1 ? used & 1 : 0;
         const uint32_t free_phase = ((uint32_t)(kSub == 1 ? used >> 1 : used) & 1u) ^ 1u;
-        for (int kb = 0; ok && kb < kb_n; ++kb, ++it) {
-          const int s = it % C::stages;
-          ok = mbar_wait(smem_u32(&sh.full[s]), (uint32_t)(it / C::stages) & 1u, abort, p.status);
+        const uint32_t d0 = tmem_base + (uint32_t)(buf * kNT);
+        for (int kb = 0; kb < kb_n; ++kb, ++it, at.next()) {
+          ok = warp_wait(at.full, at.phase, abort, p.status);
           if (!ok) break;
           tc_fence_after();
-          const uint32_t sa = ring + s * C::stage_bytes;
-          const uint64_t db = smem_desc_sw128(sa + C::a_bytes);
-          constexpr uint64_t step_a = kWay == kForward ? kStepK : kStepMN;
+          const uint64_t off = at.offset >> 4;
 #pragma unroll
           for (int u = 0; u < kSub; ++u) {
             if (kb == 0) {
-              ok = mbar_wait(smem_u32(&sh.tempty[buf + u]), free_phase, abort, p.status);
+              ok = warp_wait(smem_u32(&sh.tempty[buf + u]), free_phase, abort, p.status);
               if (!ok) break;
               tc_fence_after();
             }
-            const uint32_t sw = sa + u * kABytes;
-            const uint64_t da = kWay == kForward ? smem_desc_sw128(sw) : smem_desc_mn_sw128(sw);
-            const uint32_t d = tmem_base + (uint32_t)((buf + u) * kNT);
+            if (!elected) continue;
+            const uint64_t dw = desc_w + off + (uint64_t)(u * (kABytes >> 4)), dx = desc_x + off;
 #pragma unroll
             for (int i = 0; i < kBK / 16; ++i)
-              mma16<kCtas>(d, da + step_a * i, db + kStepK * i, idesc, (kb | i) > 0 ? 1u : 0u);
+              mma16<kCtas>(d0 + (uint32_t)(u * kNT), dw + step_w * i, dx + kStepK * i, idesc,
+                           i > 0 ? 1u : (uint32_t)kb);
             if (kb == kb_n - 1) commit16<kCtas>(smem_u32(&sh.tfull[buf + u]));
           }
           if (!ok) break;
-          commit16<kCtas>(smem_u32(&sh.empty[s]));
+          if (elected) commit16<kCtas>(at.empty);
         }
       }
       if (!ok && it > 0) {
         // every issued MMA has completed before TMEM is released
-        commit16<kCtas>(smem_u32(&sh.drained));
+        if (elected) commit16<kCtas>(smem_u32(&sh.drained));
         mbar_wait(smem_u32(&sh.drained), 0u, nullptr, p.status);
       }
     }
@@ -766,38 +842,41 @@ __global__ void __cluster_dims__(kCtas, 1, 1) __launch_bounds__(kWThreads, 1)
 
   if (warp < 4) asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kWRegsCtl));
   if (warp == 0) {
-    if (lane == 0) {
+    {
       // ------------------------------------------------------------ producer
+      const bool elected = elect_one();
       int it = 0;
       uint32_t part_phase = 0;  // a bit per stage
       bool ok = true;
+      Cursor<C::stages, C::stage_bytes> at(smem_u32(sh.full), smem_u32(sh.empty));
+      const uint32_t to_leader = kCtas == 2 ? in_leader(at.full) - at.full : 0;
       for (int64_t tile = team; ok && tile < total; tile += teams) {
         const TileAt t = tile_at((int)tile, sh.prefix, p.n_groups, p.n_tiles);
-        const int rows = sh.rows[t.g];
+        const int rows = uniform(sh.rows[t.g]);
         const int kb_n = (rows + kBK - 1) / kBK;
         const int a0 = (t.m * kCtas + rank) * kBM, b0 = t.n * kBN + rank * kHalf;
-        for (int kb = 0; kb < kb_n; ++kb, ++it) {
-          const int s = it % C::stages;
-          if (!mbar_wait(smem_u32(&sh.empty[s]), ((uint32_t)(it / C::stages) & 1u) ^ 1u, abort,
-                         p.status)) {
+        int r = uniform(sh.start[t.g]);
+        for (int kb = 0; kb < kb_n; ++kb, ++it, at.next(), r += kBK) {
+          if (!warp_wait(at.empty, at.phase ^ 1u, abort, p.status)) {
             ok = false;
             break;
           }
           // A pair's loads count on its first CTA's barrier. Each CTA's loads
           // of a block to be cleared count on a barrier of its own, and the
           // first CTA's full barrier completes at once.
-          uint32_t bar = smem_u32(&sh.full[s]);
-          if (to_clear(rows, kb)) {
+          uint32_t bar = at.full;
+          const bool clear = kb == kb_n - 1 && to_clear(rows, kb);
+          if (clear) part_phase ^= 1u << at.stage();
+          if (!elected) continue;
+          if (clear) {
             if (rank == 0) mbar_arrive(bar);
-            bar = smem_u32(&sh.part[s]);
+            bar = smem_u32(&sh.part[at.stage()]);
             mbar_arrive_expect_tx(bar, C::stage_bytes);
-            part_phase ^= 1u << s;
           } else {
             if (rank == 0) mbar_arrive_expect_tx(bar, kCtas * C::stage_bytes);
-            if (kCtas == 2) bar = in_leader(bar);
+            bar += to_leader;
           }
-          const uint32_t sa = ring + s * C::stage_bytes, sb = sa + kABytes;
-          const int r = sh.start[t.g] + kb * kBK;
+          const uint32_t sa = ring + at.offset, sb = sa + kABytes;
 #pragma unroll
           for (int i = 0; i < kBM / 64; ++i)
             load_2d<kCtas>(sa + i * kBK * 128, &tm_a, a0 + i * 64, r, bar);
@@ -851,49 +930,59 @@ __global__ void __cluster_dims__(kCtas, 1, 1) __launch_bounds__(kWThreads, 1)
       }
     }
   } else if (warp == 1) {
-    if (lane == 0 && rank == 0) {
+    if (rank == 0) {
       // ------------------------------------------------------------ MMA issuer
+      const bool elected = elect_one();
       int it = 0, used = 0;
       uint32_t ready_phase = 0;
       bool ok = true;
+      Cursor<C::stages, C::stage_bytes> at(smem_u32(sh.full), smem_u32(sh.empty));
+      const uint64_t desc_a = smem_desc_mn_sw128(ring), desc_b = smem_desc_mn_sw128(ring + kABytes);
       for (int64_t tile = team; ok && tile < total; tile += teams) {
         const TileAt t = tile_at((int)tile, sh.prefix, p.n_groups, p.n_tiles);
-        const int rows = sh.rows[t.g];
+        const int rows = uniform(sh.rows[t.g]);
         const int kb_n = (rows + kBK - 1) / kBK;
-        for (int kb = 0; kb < kb_n; ++kb, ++it) {
+        int in_segment = 0;
+        for (int kb = 0; kb < kb_n; ++kb, ++it, at.next()) {
           const int buf = used & 1;
-          if (kb % kSegment == 0) {
-            ok = mbar_wait(smem_u32(&sh.tempty[buf]), ((uint32_t)(used >> 1) & 1u) ^ 1u, abort,
+          if (in_segment == 0) {
+            ok = warp_wait(smem_u32(&sh.tempty[buf]), ((uint32_t)(used >> 1) & 1u) ^ 1u, abort,
                            p.status);
             if (!ok) break;
             tc_fence_after();
           }
           const uint32_t d = tmem_base + (uint32_t)(buf * kBN);
-          const int s = it % C::stages;
-          ok = mbar_wait(smem_u32(&sh.full[s]), (uint32_t)(it / C::stages) & 1u, abort, p.status);
-          if (ok && to_clear(rows, kb)) {
-            ok = mbar_wait_pair<kCtas>(smem_u32(&sh.ready[s]), (ready_phase >> s) & 1u, abort,
-                                       p.status);
-            ready_phase ^= 1u << s;
+          ok = warp_wait(at.full, at.phase, abort, p.status);
+          const bool last = kb == kb_n - 1;
+          int steps = kBK / 16;
+          if (ok && last) {
+            steps = (rows - kb * kBK + 15) / 16;
+            if (to_clear(rows, kb)) {
+              ok = __all_sync(0xffffffffu,
+                              mbar_wait_pair<kCtas>(smem_u32(&sh.ready[at.stage()]),
+                                                    (ready_phase >> at.stage()) & 1u, abort, p.status));
+              ready_phase ^= 1u << at.stage();
+            }
           }
           if (!ok) break;
           tc_fence_after();
-          const uint32_t sa = ring + s * C::stage_bytes;
-          const uint64_t da = smem_desc_mn_sw128(sa), db = smem_desc_mn_sw128(sa + kABytes);
-          const int steps = (min(rows - kb * kBK, kBK) + 15) / 16;
-          for (int i = 0; i < steps; ++i)
-            mma16<kCtas>(d, da + kStepMN * i, db + kStepMN * i, p.idesc,
-                         (kb % kSegment) > 0 || i > 0 ? 1u : 0u);
-          commit16<kCtas>(smem_u32(&sh.empty[s]));
-          if (kb % kSegment == kSegment - 1 || kb == kb_n - 1) {
-            commit16<kCtas>(smem_u32(&sh.tfull[buf]));
+          const uint64_t off = at.offset >> 4;
+#pragma unroll
+          for (int i = 0; i < kBK / 16; ++i)
+            if (i < steps && elected)
+              mma16<kCtas>(d, desc_a + off + kStepMN * i, desc_b + off + kStepMN * i, p.idesc,
+                           i > 0 ? 1u : (uint32_t)in_segment);
+          if (elected) commit16<kCtas>(at.empty);
+          if (++in_segment == kSegment || last) {
+            if (elected) commit16<kCtas>(smem_u32(&sh.tfull[buf]));
             ++used;
+            in_segment = 0;
           }
         }
       }
       if (!ok && it > 0) {
         // every issued MMA has completed before TMEM is released
-        commit16<kCtas>(smem_u32(&sh.drained));
+        if (elected) commit16<kCtas>(smem_u32(&sh.drained));
         mbar_wait(smem_u32(&sh.drained), 0u, nullptr, p.status);
       }
     }
@@ -996,8 +1085,9 @@ cudaError_t launch_mat(Args16 a, const CUtensorMap& mw, const CUtensorMap& mx,
   });
   if (e != cudaSuccess) return e;
   a.idesc = make_idesc(kBM * kCtas, 0, a.idesc, a.idesc) | (kWay == kInputGrad ? 1u << 15 : 0u);
-  // tiles of half height at the least
-  const int64_t tiles = row_tiles * ((a.N + kBM / 2 - 1) / (kBM / 2));
+  // the most tiles there can be
+  const int lowest = C::low ? low_step(kWay == kForward) : kBM * kCtas * kSub;
+  const int64_t tiles = row_tiles * ((a.N + lowest - 1) / lowest);
   if (tiles >= (1ll << 31)) return cudaErrorInvalidValue;
   const int64_t grid = tiles * kCtas < sms ? tiles * kCtas : sms / kCtas * kCtas;
   grouped_matmul_kernel<kWay, kCtas, kNT, kSub><<<(unsigned)grid, C::threads, C::dyn_smem, stream>>>(mw, mx, mx32, a);
@@ -1046,18 +1136,58 @@ cudaError_t launch_grouped_matmul(const Groups16& gr, bool f16, int out_type, in
   p.out_type = out_type;
   p.idesc = f16 ? 0u : 1u;
   p.status = gr.status;
+  // The kernel whose rounds of tiles take the least time, if the groups were
+  // alike: each k-block costs an SM what it takes in or its MMAs, whichever is
+  // longer. Measured against this model (us, K-major): 16 groups of 400 rows,
+  // 1024 x 1024: 2x256x2 18.9, 2x256 21.2, 2x128 31.6, 1x32 76.9; 2 of 821,
+  // 920 x 1184: 18.6, 14.1, 13.6, 32.7; 32 of 8, 4096 x 4096: 183.9, 178.6,
+  // 172.9, 168.2.
+  const int64_t busy = gr.rows < gr.n_groups ? gr.rows : gr.n_groups;
+  const int64_t each = (gr.rows + busy - 1) / busy;
+  auto cost = [&](int ctas, int nt, int sub) {
+    const int64_t split = (each + nt - 1) / nt, rows = (each + split - 1) / split;
+    const int units = sms / ctas;
+    const float x = (float)((rows + 15) / 16 * 16 / ctas * kBK * 2);
+    float best = 0.0f;
+    const int step = ctas == 1 ? low_step(trans_b) : kBM * ctas * sub;
+    for (int h = kBM * ctas * sub; h > 0; h -= step) {
+      const int64_t tiles = busy * split * ((N + h - 1) / h), rounds = (tiles + units - 1) / units;
+      const float w = (float)(h / ctas * kBK * 2);
+      const float active = (float)(tiles < units ? tiles : units) * ctas;
+      const float in = (w + x) / kSmIn, hbm = w * active / (float)split / kHbm;
+      const float mma = 2.0f * (float)(rows * sub) / 1.4f;  // cycles at the clock under load
+      const float kb = in > hbm ? in : hbm;
+      // a tile with both accumulators is not read while the next one's MMAs run
+      const float t = (float)rounds * ((float)p.kblocks * (kb > mma ? kb : mma) +
+                                       (sub == 2 ? 8.0f * (float)rows : 0.0f)) + 8.0f * (float)rows;
+      if (best == 0.0f || t < best) best = t;
+    }
+    return best;
+  };
+  struct Choice {
+    int ctas, nt, sub;
+  };
+  constexpr Choice all[] = {{2, 256, 2}, {2, 256, 1}, {2, 128, 1}, {1, 32, 1}};
+  int pick = 0;
+  float least = 0.0f;
+  for (int i = 0; i < 4; ++i) {
+    const float t = cost(all[i].ctas, all[i].nt, all[i].sub);
+    if (i == 0 || t < least) {
+      least = t;
+      pick = i;
+    }
+  }
   CUtensorMap mw, mx, mx32;
   cudaError_t e = make_tmap_bf16(&mx, a, K, gr.rows, 1, kBK, kBM);
-  if (e == cudaSuccess) e = make_tmap_bf16(&mx32, a, K, gr.rows, 1, kBK, 32);
+  if (e == cudaSuccess) e = make_tmap_bf16(&mx32, a, K, gr.rows, 1, kBK, pick == 3 ? 16 : 32);
   if (e == cudaSuccess)
-    e = trans_b ? make_tmap_16b_3d(&mw, b, K, N, gr.n_groups, kBK, kBM)
+    e = trans_b ? make_tmap_16b_3d(&mw, b, K, N, gr.n_groups, kBK, pick == 3 ? 32 : kBM)
                 : make_tmap_16b_3d(&mw, b, N, K, gr.n_groups, 64, kBK);
   if (e != cudaSuccess) return e;
-  const int64_t busy = gr.rows < gr.n_groups ? gr.rows : gr.n_groups;
-  const int64_t each = gr.rows / busy;  // rows of a group, if they were alike
   auto go = [&](auto ctas, auto nt, auto sub) {
     constexpr int kCtas = decltype(ctas)::value, kNT = decltype(nt)::value;
     constexpr int kSub = decltype(sub)::value;
+    static_assert(MatCfg<kCtas, kNT, kSub>::x_box == (kNT == 32 ? 16 : 32), "boxes of the maps");
     const int64_t row_tiles = gr.rows / kNT + busy;
     return trans_b ? launch_mat<kForward, kCtas, kNT, kSub>(p, mw, mx, mx32, row_tiles, stream, sms)
                    : launch_mat<kInputGrad, kCtas, kNT, kSub>(p, mw, mx, mx32, row_tiles, stream, sms);
@@ -1065,9 +1195,9 @@ cudaError_t launch_grouped_matmul(const Groups16& gr, bool f16, int out_type, in
   using std::integral_constant;
   constexpr integral_constant<int, 1> one{};
   constexpr integral_constant<int, 2> two{};
-  if (each > 160 && N > 2 * kBM) return go(two, integral_constant<int, 256>{}, two);
-  if (each > 160 && N > kBM) return go(two, integral_constant<int, 256>{}, one);
-  if (each > 24) return go(one, integral_constant<int, 128>{}, one);
+  if (pick == 0) return go(two, integral_constant<int, 256>{}, two);
+  if (pick == 1) return go(two, integral_constant<int, 256>{}, one);
+  if (pick == 2) return go(two, integral_constant<int, 128>{}, one);
   return go(one, integral_constant<int, 32>{}, one);
 }
 
