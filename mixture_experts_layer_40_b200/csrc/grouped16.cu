@@ -359,8 +359,12 @@ MOE_DEV uint32_t pack_f16x2(float lo, float hi) {
 template <int kCtas, int kNT, int kSub>
 struct MatCfg {
   static constexpr int threads = 128 + 128 * kSub;  // an epilogue warpgroup for each accumulator
-  static constexpr int a_bytes = kSub * kABytes;
-  static constexpr int b_bytes = kNT / kCtas * kBK * 2;
+  // k-blocks of a stage: two where the tile is so small that waiting and
+  // issuing for one (400 cycles) would take longer than its copies and MMAs
+  static constexpr int depth = kNT >= 256 ? 1 : 2;
+  static constexpr int x_bytes = kNT / kCtas * kBK * 2;  // one k-block of rows
+  static constexpr int a_bytes = depth * kSub * kABytes;
+  static constexpr int b_bytes = depth * x_bytes;
   static constexpr int stage_bytes = a_bytes + b_bytes;
   // a warp's 32 (fp32: 16) rows x 32 columns of the output, each row padded
   // by 16 bytes against bank conflicts
@@ -381,6 +385,7 @@ struct MatCfg {
 // Rates for choosing tiles, per ns: what one SM takes in, and all of HBM (both
 // measured with these kernels).
 constexpr float kSmIn = 60.0f, kHbm = 6450.0f;
+constexpr float kIssue = 115.0f;  // ns to wait and issue for one k-block of a small tile
 
 // Time of a k-block of a round of `tiles` single-CTA tiles of height h, up to
 // a factor: the SM's own intake, or the share of HBM that the weights need.
@@ -388,7 +393,8 @@ __host__ __device__ inline float low_tile_ns(int h, int x_rows, int64_t tiles, i
   const float w = (float)(h * kBK * 2), x = (float)(x_rows * kBK * 2);
   const float active = (float)(tiles < units ? tiles : units);
   const float in = (w + x) / kSmIn, hbm = w * active / kHbm;
-  return in > hbm ? in : hbm;
+  const float most = in > hbm ? in : hbm;
+  return most > kIssue ? most : kIssue;
 }
 // heights that the loads come in: boxes of 32 weight rows, or of 64 columns
 __host__ __device__ constexpr int low_step(bool k_major) { return k_major ? 32 : 64; }
@@ -471,7 +477,7 @@ __global__ void __cluster_dims__(kCtas, 1, 1) __launch_bounds__(128 + 128 * kSub
   const int n_tiles = (p.N + height - 1) / height;
   const int64_t total = (int64_t)row_tiles * n_tiles;
   volatile int* abort = &sh.abort;
-  const int kb_n = p.kblocks;
+  const int kb_n = (p.kblocks + C::depth - 1) / C::depth;
 
   if (warp == 0) {
     {
@@ -490,11 +496,12 @@ __global__ void __cluster_dims__(kCtas, 1, 1) __launch_bounds__(128 + 128 * kSub
         const bool whole = kNT / kCtas >= 128 && pieces == 4;
         // the weights' boxes: all of 128 rows, or as many as the height takes
         const int w_pieces = !C::low ? 1 : kWay == kForward ? (height + 31) / 32 : (height + 63) / 64;
-        const int w_bytes = !C::low ? C::a_bytes : w_pieces * (kWay == kForward ? 32 : 64) * kBK * 2;
+        const int w_bytes = !C::low ? kSub * kABytes : w_pieces * (kWay == kForward ? 32 : 64) * kBK * 2;
         const int row = rt.first + rank * half;
         const int n0 = t.n * height + rank * kBM;
-        const uint32_t bytes = kCtas * (w_bytes + pieces * C::x_box * kBK * 2);
-        for (int k = 0; k < kb_n * kBK; k += kBK, ++it, at.next()) {
+        const uint32_t bytes = kCtas * C::depth * (w_bytes + pieces * C::x_box * kBK * 2);
+        // (a second k-block may lie beyond K: zeros)
+        for (int k0 = 0; k0 < kb_n * C::depth * kBK; k0 += C::depth * kBK, ++it, at.next()) {
           if (!warp_wait(at.empty, at.phase ^ 1u, abort, p.status)) {
             ok = false;
             break;
@@ -502,29 +509,34 @@ __global__ void __cluster_dims__(kCtas, 1, 1) __launch_bounds__(128 + 128 * kSub
           if (!elected) continue;
           if (rank == 0) mbar_arrive_expect_tx(at.full, bytes);
           const uint32_t full = at.full + to_leader;
-          const uint32_t sa = ring + at.offset, sb = sa + C::a_bytes;
 #pragma unroll
-          for (int u = 0; u < kSub; ++u) {
-            const int n = n0 + u * kBM * kCtas;
-            if (C::low && kWay == kForward) {
-              for (int i = 0; i < w_pieces; ++i)
-                load_3d<kCtas>(sa + i * 32 * kBK * 2, &tm_w, k, n + i * 32, t.g, full);
-            } else if (C::low) {
-              for (int i = 0; i < w_pieces; ++i)
-                load_3d<kCtas>(sa + i * kBK * 128, &tm_w, n + i * 64, k, t.g, full);
-            } else if (kWay == kForward) {
-              load_3d<kCtas>(sa + u * kABytes, &tm_w, k, n, t.g, full);
-            } else {
+          for (int j = 0; j < C::depth; ++j) {
+            const int k = k0 + j * kBK;
+            const uint32_t sa = ring + at.offset + j * kSub * kABytes;
+            const uint32_t sb = ring + at.offset + C::a_bytes + j * C::x_bytes;
 #pragma unroll
-              for (int i = 0; i < kBM / 64; ++i)
-                load_3d<kCtas>(sa + u * kABytes + i * kBK * 128, &tm_w, n + i * 64, k, t.g, full);
+            for (int u = 0; u < kSub; ++u) {
+              const int n = n0 + u * kBM * kCtas;
+              if (C::low && kWay == kForward) {
+                for (int i = 0; i < w_pieces; ++i)
+                  load_3d<kCtas>(sa + i * 32 * kBK * 2, &tm_w, k, n + i * 32, t.g, full);
+              } else if (C::low) {
+                for (int i = 0; i < w_pieces; ++i)
+                  load_3d<kCtas>(sa + i * kBK * 128, &tm_w, n + i * 64, k, t.g, full);
+              } else if (kWay == kForward) {
+                load_3d<kCtas>(sa + u * kABytes, &tm_w, k, n, t.g, full);
+              } else {
+#pragma unroll
+                for (int i = 0; i < kBM / 64; ++i)
+                  load_3d<kCtas>(sa + u * kABytes + i * kBK * 128, &tm_w, n + i * 64, k, t.g, full);
+              }
             }
-          }
-          if (whole) {
-            load_2d<kCtas>(sb, &tm_x, k, row, full);
-          } else {
-            for (int i = 0; i < pieces; ++i)
-              load_2d<kCtas>(sb + i * C::x_box * kBK * 2, &tm_x32, k, row + C::x_box * i, full);
+            if (whole) {
+              load_2d<kCtas>(sb, &tm_x, k, row, full);
+            } else {
+              for (int i = 0; i < pieces; ++i)
+                load_2d<kCtas>(sb + i * C::x_box * kBK * 2, &tm_x32, k, row + C::x_box * i, full);
+            }
           }
         }
       }
@@ -567,11 +579,15 @@ __global__ void __cluster_dims__(kCtas, 1, 1) __launch_bounds__(128 + 128 * kSub
               tc_fence_after();
             }
             if (!elected) continue;
-            const uint64_t dw = desc_w + off + (uint64_t)(u * (kABytes >> 4)), dx = desc_x + off;
 #pragma unroll
-            for (int i = 0; i < kBK / 16; ++i)
-              mma16<kCtas>(d0 + (uint32_t)(u * kNT), dw + step_w * i, dx + kStepK * i, idesc,
-                           i > 0 ? 1u : (uint32_t)kb);
+            for (int j = 0; j < C::depth; ++j) {
+              const uint64_t dw = desc_w + off + (uint64_t)((j * kSub + u) * (kABytes >> 4));
+              const uint64_t dx = desc_x + off + (uint64_t)(j * (C::x_bytes >> 4));
+#pragma unroll
+              for (int i = 0; i < kBK / 16; ++i)
+                mma16<kCtas>(d0 + (uint32_t)(u * kNT), dw + step_w * i, dx + kStepK * i, idesc,
+                             j + i > 0 ? 1u : (uint32_t)kb);
+            }
             if (kb == kb_n - 1) commit16<kCtas>(smem_u32(&sh.tfull[buf + u]));
           }
           if (!ok) break;
@@ -1156,7 +1172,8 @@ cudaError_t launch_grouped_matmul(const Groups16& gr, bool f16, int out_type, in
       const float active = (float)(tiles < units ? tiles : units) * ctas;
       const float in = (w + x) / kSmIn, hbm = w * active / (float)split / kHbm;
       const float mma = 2.0f * (float)(rows * sub) / 1.4f;  // cycles at the clock under load
-      const float kb = in > hbm ? in : hbm;
+      float kb = in > hbm ? in : hbm;
+      kb = kb > kIssue ? kb : kIssue;
       // a tile with both accumulators is not read while the next one's MMAs run
       const float t = (float)rounds * ((float)p.kblocks * (kb > mma ? kb : mma) +
                                        (sub == 2 ? 8.0f * (float)rows : 0.0f)) + 8.0f * (float)rows;
