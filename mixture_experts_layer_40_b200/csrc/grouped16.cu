@@ -730,6 +730,20 @@ MOE_DEV void store_3d(const CUtensorMap* map, uint32_t src, int32_t x, int32_t y
         : "memory");
 }
 
+// 16 consecutive TMEM columns of this warp's 32 lanes
+MOE_DEV void tmem_ld16(uint32_t taddr, float (&v)[16]) {
+  uint32_t r[16];
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x16.b32 "
+      "{%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15}, [%16];"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]),
+        "=r"(r[7]), "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]),
+        "=r"(r[14]), "=r"(r[15])
+      : "r"(taddr));
+#pragma unroll
+  for (int i = 0; i < 16; ++i) v[i] = __uint_as_float(r[i]);
+}
+
 // 32 consecutive columns of a warp's 32 rows (one row a lane) of dw, out
 // through shared memory and a TMA store that clips at dw's edges; 16-bit
 // outputs gather two calls' 32 columns in one 128-byte row.
@@ -777,14 +791,12 @@ struct DwOut {
   }
 };
 
-// 32 consecutive columns of one row added to the 16-bit values there, rounded
-// once (a TMA add would round the addend first)
-MOE_DEV void add16(const Args16& p, const float (&v)[32], int x, int64_t at, bool live) {
-  const bool f16 = p.out_type == MOE_FP16;
-#pragma unroll
-  for (int c = 0; c < 4; ++c) {
-    if (!live || x + 8 * c >= p.N) continue;
-    uint4* dst = reinterpret_cast<uint4*>(static_cast<uint16_t*>(p.out) + at + 8 * c);
+// 32 consecutive columns of one row added to the 16-bit values at dst, rounded
+// once (a TMA add would round the addend first); out of line, since its
+// registers would be taken from the sums of the common paths
+__device__ __noinline__ void add16(uint16_t* out, bool f16, const float* v, int columns) {
+  for (int c = 0; c < 4 && 8 * c < columns; ++c) {
+    uint4* dst = reinterpret_cast<uint4*>(out + 8 * c);
     const uint4 q = *dst;
     uint32_t w[4] = {q.x, q.y, q.z, q.w};
 #pragma unroll
@@ -813,6 +825,8 @@ template <int kCtas, int kBN>
 __global__ void __cluster_dims__(kCtas, 1, 1) __launch_bounds__(kWThreads, 1)
     grouped_wgrad_kernel(const __grid_constant__ CUtensorMap tm_a,
                          const __grid_constant__ CUtensorMap tm_b,
+                         const __grid_constant__ CUtensorMap tm_a16,
+                         const __grid_constant__ CUtensorMap tm_b16,
                          const __grid_constant__ CUtensorMap tm_out, const Args16 p) {
   using C = WgCfg<kCtas, kBN>;
   constexpr int kHalf = kBN / kCtas;     // columns of x this CTA loads
@@ -884,21 +898,35 @@ __global__ void __cluster_dims__(kCtas, 1, 1) __launch_bounds__(kWThreads, 1)
           const bool clear = kb == kb_n - 1 && to_clear(rows, kb);
           if (clear) part_phase ^= 1u << at.stage();
           if (!elected) continue;
+          // the last block only as far as its 16-row steps go
+          const int steps = min((rows - kb * kBK + 15) / 16, kBK / 16);
+          const uint32_t bytes = (uint32_t)(C::stage_bytes / (kBK / 16) * steps);
           if (clear) {
             if (rank == 0) mbar_arrive(bar);
             bar = smem_u32(&sh.part[at.stage()]);
-            mbar_arrive_expect_tx(bar, C::stage_bytes);
+            mbar_arrive_expect_tx(bar, bytes);
           } else {
-            if (rank == 0) mbar_arrive_expect_tx(bar, kCtas * C::stage_bytes);
+            if (rank == 0) mbar_arrive_expect_tx(bar, kCtas * bytes);
             bar += to_leader;
           }
           const uint32_t sa = ring + at.offset, sb = sa + kABytes;
+          if (steps == kBK / 16) {
 #pragma unroll
-          for (int i = 0; i < kBM / 64; ++i)
-            load_2d<kCtas>(sa + i * kBK * 128, &tm_a, a0 + i * 64, r, bar);
+            for (int i = 0; i < kBM / 64; ++i)
+              load_2d<kCtas>(sa + i * kBK * 128, &tm_a, a0 + i * 64, r, bar);
 #pragma unroll
-          for (int i = 0; i < kHalf / 64; ++i)
-            load_2d<kCtas>(sb + i * kBK * 128, &tm_b, b0 + i * 64, r, bar);
+            for (int i = 0; i < kHalf / 64; ++i)
+              load_2d<kCtas>(sb + i * kBK * 128, &tm_b, b0 + i * 64, r, bar);
+          } else {
+            for (int j = 0; j < steps; ++j) {
+#pragma unroll
+              for (int i = 0; i < kBM / 64; ++i)
+                load_2d<kCtas>(sa + i * kBK * 128 + j * 16 * 128, &tm_a16, a0 + i * 64, r + 16 * j, bar);
+#pragma unroll
+              for (int i = 0; i < kHalf / 64; ++i)
+                load_2d<kCtas>(sb + i * kBK * 128 + j * 16 * 128, &tm_b16, b0 + i * 64, r + 16 * j, bar);
+            }
+          }
         }
       }
       if (!ok) {
@@ -941,7 +969,7 @@ __global__ void __cluster_dims__(kCtas, 1, 1) __launch_bounds__(kWThreads, 1)
       fence_proxy_async_smem();
       __syncwarp();
       if (lane == 0) {
-        if (kCtas == 2) mbar_arrive_release(in_leader(smem_u32(&sh.ready[s])));
+        if (rank > 0) mbar_arrive_release(in_leader(smem_u32(&sh.ready[s])));
         else mbar_arrive(smem_u32(&sh.ready[s]));
       }
     }
@@ -1024,10 +1052,16 @@ __global__ void __cluster_dims__(kCtas, 1, 1) __launch_bounds__(kWThreads, 1)
         // a 16-bit row is stored when its second half is in: beyond the last
         // column both halves are skipped, or neither
         if (y >= p.M || (p.out_type == MOE_FP32 ? x : x & ~63) >= p.N) return;
-        if (direct)
-          add16(p, v, x, ((int64_t)t.g * p.M + y + lane) * p.N + x, y + lane < p.M);
-        else
+        if (direct) {
+          float w[32];
+#pragma unroll
+          for (int i = 0; i < 32; ++i) w[i] = v[i];
+          if (y + lane < p.M)
+            add16(static_cast<uint16_t*>(p.out) + ((int64_t)t.g * p.M + y + lane) * p.N + x,
+                  p.out_type == MOE_FP16, w, p.N - x);
+        } else {
           out.put(p, v, x, y, t.g, lane);
+        }
       };
       auto wait_segment = [&] {
         ok = __all_sync(0xffffffffu, mbar_wait(smem_u32(&sh.tfull[used & 1]),
@@ -1062,15 +1096,19 @@ __global__ void __cluster_dims__(kCtas, 1, 1) __launch_bounds__(kWThreads, 1)
         if (segments == 1) release_segment();
       } else {
         float sum[kEpiCols / 32][32];
+#pragma unroll
+        for (int c = 0; c < kEpiCols / 32; ++c)
+#pragma unroll
+          for (int i = 0; i < 32; ++i) sum[c][i] = 0.0f;
         for (int seg = 0; seg < segments; ++seg) {
           if (!wait_segment()) break;
 #pragma unroll
-          for (int c = 0; c < kEpiCols / 32; ++c) {
-            float v[32];
-            tmem_ld32(lane_addr + (uint32_t)((used & 1) * kBN + 32 * c), v);
+          for (int c = 0; c < kEpiCols / 16; ++c) {
+            float v[16];
+            tmem_ld16(lane_addr + (uint32_t)((used & 1) * kBN + 16 * c), v);
             tmem_wait_ld();
 #pragma unroll
-            for (int i = 0; i < 32; ++i) sum[c][i] = seg == 0 ? v[i] : sum[c][i] + v[i];
+            for (int i = 0; i < 16; ++i) sum[c / 2][(c & 1) * 16 + i] += v[i];
           }
           release_segment();
         }
@@ -1112,7 +1150,8 @@ cudaError_t launch_mat(Args16 a, const CUtensorMap& mw, const CUtensorMap& mx,
 
 template <int kCtas, int kBN>
 cudaError_t launch_wg(Args16 a, const CUtensorMap& ma, const CUtensorMap& mb,
-                      const CUtensorMap& mo, cudaStream_t stream, int sms) {
+                      const CUtensorMap& ma16, const CUtensorMap& mb16, const CUtensorMap& mo,
+                      cudaStream_t stream, int sms) {
   using C = WgCfg<kCtas, kBN>;
   static DeviceOnce once;
   cudaError_t e = once.run([] {
@@ -1131,7 +1170,7 @@ cudaError_t launch_wg(Args16 a, const CUtensorMap& ma, const CUtensorMap& mb,
   const int64_t tiles = (int64_t)a.n_groups * a.m_tiles * a.n_tiles;
   if (tiles >= (1ll << 31)) return cudaErrorInvalidValue;
   const int64_t grid = tiles * kCtas < sms ? tiles * kCtas : sms / kCtas * kCtas;
-  grouped_wgrad_kernel<kCtas, kBN><<<(unsigned)grid, kWThreads, C::dyn_smem, stream>>>(ma, mb, mo, a);
+  grouped_wgrad_kernel<kCtas, kBN><<<(unsigned)grid, kWThreads, C::dyn_smem, stream>>>(ma, mb, ma16, mb16, mo, a);
   return cudaGetLastError();
 }
 
@@ -1233,17 +1272,19 @@ cudaError_t launch_grouped_wgrad(const Groups16& gr, bool f16, int out_type, int
   p.accumulate = accumulate ? 1 : 0;
   p.idesc = f16 ? 0u : 1u;
   p.status = gr.status;
-  CUtensorMap ma, mb, mo;
+  CUtensorMap ma, mb, ma16, mb16, mo;
   // without rows nothing is loaded, and the row buffers may be NULL
   cudaError_t e = make_tmap_bf16(&ma, gr.rows > 0 ? dy : dw, N, gr.rows, 1, 64, kBK);
   if (e == cudaSuccess) e = make_tmap_bf16(&mb, gr.rows > 0 ? x : dw, K, gr.rows, 1, 64, kBK);
+  if (e == cudaSuccess) e = make_tmap_bf16(&ma16, gr.rows > 0 ? dy : dw, N, gr.rows, 1, 64, 16);
+  if (e == cudaSuccess) e = make_tmap_bf16(&mb16, gr.rows > 0 ? x : dw, K, gr.rows, 1, 64, 16);
   if (e == cudaSuccess)
     e = out_type == MOE_FP32 ? make_tmap_f32_3d(&mo, dw, K, N, gr.n_groups, 32, 32)
                              : make_tmap_16b_3d(&mo, dw, K, N, gr.n_groups, 64, 32);
   if (e != cudaSuccess) return e;
   const int64_t pairs = (int64_t)gr.n_groups * ((N + 255) / 256) * ((K + 255) / 256);
-  if (N > kBM && pairs >= sms / 2) return launch_wg<2, 256>(p, ma, mb, mo, stream, sms);
-  return launch_wg<1, 128>(p, ma, mb, mo, stream, sms);
+  if (N > kBM && pairs >= sms / 2) return launch_wg<2, 256>(p, ma, mb, ma16, mb16, mo, stream, sms);
+  return launch_wg<1, 128>(p, ma, mb, ma16, mb16, mo, stream, sms);
 }
 
 }  // namespace moe
