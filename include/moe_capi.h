@@ -503,7 +503,12 @@ int moe_block_norm_backward(int64_t T, int32_t H, int32_t res_type, int32_t act_
  * and type, or out NULL to scale in place. The arrays are read during the
  * call only. Elements of their own size's alignment; tensors may be empty and
  * may differ in type. Outputs must not overlap one another, nor another
- * tensor's gradients.
+ * tensor's gradients. A list of more than MOE_GRAD_SMALL tensors needs its
+ * table in device memory: moe_grad_table checks the list, fills
+ * moe_grad_table_size(list) bytes of HOST memory (0 for shorter lists, or bad
+ * ones) and the list's plan; the caller copies the bytes to the device once
+ * (16-byte aligned) and gives them as `table`. The list must not change after
+ * that, and its arrays are not read again.
  *
  * moe_grad_sumsq leaves MOE_GRAD_PARTIALS partial sums of squares (double);
  *   their sum is the squared norm. With the experts sharded over several GPUs
@@ -521,8 +526,14 @@ typedef struct {
   void* const* out;
   const int64_t* sizes;
   const int32_t* types;
+  const void* table;
+  int32_t plan[4];  /* set by moe_grad_table */
 } moe_grad_list;
 #define MOE_GRAD_PARTIALS 1024
+#define MOE_GRAD_SMALL 32
+size_t moe_grad_table_size(const moe_grad_list* list);
+int moe_grad_table(moe_grad_list* list, void* host_table);
+
 int moe_grad_sumsq(const moe_grad_list* list, double* partials, void* stream);
 
 int moe_grad_clip(const moe_grad_list* list, const double* partials, float max_norm, float* norm,

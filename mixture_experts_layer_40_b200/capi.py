@@ -43,7 +43,8 @@ class moe_weights(ctypes.Structure):
 class moe_grad_list(ctypes.Structure):
     _fields_ = [("n", ctypes.c_int32), ("grads", ctypes.POINTER(ctypes.c_void_p)),
                 ("out", ctypes.POINTER(ctypes.c_void_p)), ("sizes", ctypes.POINTER(ctypes.c_int64)),
-                ("types", ctypes.POINTER(ctypes.c_int32))]
+                ("types", ctypes.POINTER(ctypes.c_int32)), ("table", ctypes.c_void_p),
+                ("plan", ctypes.c_int32 * 4)]
 
 
 _LAYOUT_FIELDS = ["status", "counts", "offsets", "group_rows", "row_start", "row_token",
@@ -94,6 +95,8 @@ SIGNATURES = {
     "moe_block_norm_backward": (ctypes.c_int, [_I64, _I32, _I32, _I32, _I32, _I32, _F32, _F32, _P,
                                                _P, _P, _P, _P, _P, _P, _P, _P, _P, _P, _P, _P, _P,
                                                _P, _SZ, _P]),
+    "moe_grad_table_size": (_SZ, [ctypes.POINTER(moe_grad_list)]),
+    "moe_grad_table": (ctypes.c_int, [ctypes.POINTER(moe_grad_list), _P]),
     "moe_grad_sumsq": (ctypes.c_int, [ctypes.POINTER(moe_grad_list), _P, _P]),
     "moe_grad_clip": (ctypes.c_int, [ctypes.POINTER(moe_grad_list), _P, _F32, _P, _P]),
     "moe_ep_row_bytes": (_I64, [moe_shape]),
@@ -521,8 +524,8 @@ GRAD_PARTIALS = 1024
 
 class GradList:
     """A moe_grad_list over a program's gradient tensors, made once by
-    make_grad_list and used in every step that writes new gradients into
-    them; it keeps the tensors."""
+    make_grad_list (outside a graph capture) and used in every step that writes
+    new gradients into them; it keeps the tensors."""
 
     def __init__(self, grads, out):
         self.grads, self.out = list(grads), None if out is None else list(out)
@@ -548,7 +551,15 @@ class GradList:
         vpp = ctypes.POINTER(ctypes.c_void_p)
         self.struct = moe_grad_list(n, cast(g, vpp), None if o is None else cast(o, vpp),
                                     cast(s, ctypes.POINTER(ctypes.c_int64)),
-                                    cast(t, ctypes.POINTER(ctypes.c_int32)))
+                                    cast(t, ctypes.POINTER(ctypes.c_int32)), None)
+        # longer lists read their table from device memory
+        nbytes = int(LIB.moe_grad_table_size(ctypes.byref(self.struct)))
+        if nbytes:
+            host = torch.empty(nbytes, dtype=torch.uint8)
+            _check("moe_grad_table", LIB.moe_grad_table(ctypes.byref(self.struct), host.data_ptr()))
+            self._table = host.to(torch.device("cuda", self.device))
+            torch.cuda.current_stream(self.device).synchronize()  # for every later stream
+            self.struct.table = self._table.data_ptr()
 
     @staticmethod
     def _refuse_overlap(grads, out, nbytes):

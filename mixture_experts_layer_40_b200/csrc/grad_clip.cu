@@ -28,21 +28,33 @@ constexpr int kVectors = 8;       // 16-byte vectors of a chunk per thread
 constexpr int kAtOnce = 4;        // of them in flight
 constexpr int kCtasPerSm = 6;
 constexpr int kParts = MOE_GRAD_PARTIALS;
-constexpr int kMaxTensors = 1024;  // per launch: the table travels as kernel arguments
+constexpr int kSmall = MOE_GRAD_SMALL;  // lists that travel as kernel arguments
+constexpr int kSearch = 4096;           // tensors whose first chunks fit in shared memory
 
-// `chunk0[i]` is the tensor's first chunk. Its first chunk also holds the
-// elements before its first 128-byte boundary.
-template <int kCap>
-struct GradTable {
-  static constexpr int cap = kCap;
-  const void* g[kCap];
-  void* out[kCap];
-  int64_t size[kCap];
-  int32_t chunk0[kCap + 1];
-  uint8_t type[kCap];
+// One tensor: `chunk0` is its first chunk in the list. That chunk also holds
+// the elements before the tensor's first 128-byte boundary.
+struct Entry {
+  const void* g;
+  void* out;
+  int64_t size;
+  int32_t chunk0;
+  int32_t type;
+};
+static_assert(sizeof(Entry) == 32, "table entry");
+
+// A list's tensors (those with elements), in the kernel's arguments, or in
+// device memory for longer lists: a table of some hundred entries as arguments
+// would cost more than the launch, and its look-ups, which go through the
+// constant cache, more than the work (22 us against 5 for 471 tensors).
+struct Small {
+  Entry e[kSmall];
+};
+struct Table {
+  const Entry* entries;  // device, or NULL: `small`
   int32_t n;
-  int32_t in_place;  // every tensor's output is the tensor itself
-  int32_t vectors;   // 16-byte vectors per thread and chunk, 1 to kVectors
+  int32_t chunks;
+  int32_t in_place;      // every tensor's output is the tensor itself
+  int32_t vectors;       // 16-byte vectors per thread and chunk, 1 to kVectors
 };
 
 struct Span {
@@ -53,25 +65,47 @@ MOE_DEV int elements_to_boundary(const void* p, int es, uint32_t boundary = 16u)
   return (int)((0u - (uint32_t)reinterpret_cast<uintptr_t>(p)) & (boundary - 1u)) / es;
 }
 
-template <int kCap>
-MOE_DEV Span span_of(const GradTable<kCap>& t, int i, int chunk) {
-  const int es = t.type[i] == MOE_FP32 ? 4 : 2;
-  const int64_t head = elements_to_boundary(t.g[i], es, 128u);
-  const int64_t k = chunk - t.chunk0[i], len = t.vectors * (kClipThreads * 16 / es);
+MOE_DEV Span span_of(const Table& t, const Entry& e, int chunk) {
+  const int es = e.type == MOE_FP32 ? 4 : 2;
+  const int64_t head = elements_to_boundary(e.g, es, 128u);
+  const int64_t k = chunk - e.chunk0, len = t.vectors * (kClipThreads * 16 / es);
   Span s;
   s.begin = k == 0 ? 0 : head + k * len;
-  s.end = min(head + (k + 1) * len, t.size[i]);
+  s.end = min(head + (k + 1) * len, e.size);
   return s;
 }
 
-template <int kCap>
-MOE_DEV int tensor_of(const GradTable<kCap>& t, int chunk) {
-  int lo = 0, hi = t.n;
-  while (hi - lo > 1) {
-    const int mid = (lo + hi) >> 1;
-    if (t.chunk0[mid] <= chunk) lo = mid; else hi = mid;
+// Finds a chunk's tensor: the last one whose first chunk is not after it.
+template <bool kInArgs>
+struct Finder {
+  const Small& small;
+  const Table& t;
+  const int32_t* first;  // shared copy of the first chunks, or NULL
+  MOE_DEV int chunk0(int i) const {
+    if (kInArgs) return small.e[i].chunk0;
+    return first != nullptr ? first[i] : t.entries[i].chunk0;
   }
-  return lo;
+  MOE_DEV Entry find(int chunk) const {
+    int lo = 0, hi = t.n;
+    while (hi - lo > 1) {
+      const int mid = (lo + hi) >> 1;
+      if (chunk0(mid) <= chunk) lo = mid; else hi = mid;
+    }
+    return kInArgs ? small.e[lo] : t.entries[lo];
+  }
+};
+
+// the first chunks into shared memory (lists of up to kSearch tensors)
+template <bool kInArgs>
+MOE_DEV const int32_t* load_first(const Table& t, int32_t* shared) {
+  if constexpr (kInArgs) {
+    return nullptr;
+  } else {
+    if (t.n > kSearch) return nullptr;
+    for (int i = threadIdx.x; i < t.n; i += kClipThreads) shared[i] = t.entries[i].chunk0;
+    __syncthreads();
+    return shared;
+  }
 }
 
 template <typename T>
@@ -182,20 +216,20 @@ MOE_DEV double span_squares(const T* g, const Span& s) {
   return sum;
 }
 
-template <int kCap>
+template <bool kInArgs>
 __global__ void __launch_bounds__(kClipThreads, kCtasPerSm)
-    grad_sumsq_kernel(const __grid_constant__ GradTable<kCap> t, double* partials, int add) {
+    grad_sumsq_kernel(const __grid_constant__ Small small, const Table t, double* partials) {
   __shared__ double red[kClipThreads / 32];
-  const int total = t.chunk0[t.n];
+  extern __shared__ int32_t first[];
   double sum = 0.0;
   cudaTriggerProgrammaticLaunchCompletion();
-  int i = (int)blockIdx.x < total ? tensor_of(t, blockIdx.x) : 0;
-  for (int c = blockIdx.x; c < total; c += gridDim.x) {
-    while (c >= t.chunk0[i + 1]) ++i;
-    const Span s = span_of(t, i, c);
-    if (t.type[i] == MOE_FP32) sum += span_squares(static_cast<const float*>(t.g[i]), s);
-    else if (t.type[i] == MOE_BF16) sum += span_squares(static_cast<const __nv_bfloat16*>(t.g[i]), s);
-    else sum += span_squares(static_cast<const __half*>(t.g[i]), s);
+  const Finder<kInArgs> finder{small, t, load_first<kInArgs>(t, first)};
+  for (int c = blockIdx.x; c < t.chunks; c += gridDim.x) {
+    const Entry e = finder.find(c);
+    const Span s = span_of(t, e, c);
+    if (e.type == MOE_FP32) sum += span_squares(static_cast<const float*>(e.g), s);
+    else if (e.type == MOE_BF16) sum += span_squares(static_cast<const __nv_bfloat16*>(e.g), s);
+    else sum += span_squares(static_cast<const __half*>(e.g), s);
   }
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
@@ -203,10 +237,10 @@ __global__ void __launch_bounds__(kClipThreads, kCtasPerSm)
   __syncthreads();
   if (threadIdx.x == 0) {
     for (int w = 1; w < kClipThreads / 32; ++w) sum += red[w];
-    partials[blockIdx.x] = add ? partials[blockIdx.x] + sum : sum;
+    partials[blockIdx.x] = sum;
   }
   // the places that no CTA has are zero
-  if (blockIdx.x == 0 && !add)
+  if (blockIdx.x == 0)
     for (int j = gridDim.x + threadIdx.x; j < kParts; j += kClipThreads) partials[j] = 0.0;
 }
 
@@ -237,13 +271,15 @@ MOE_DEV void span_scale(const T* g, T* out, const Span& s, float c) {
   if (rest < s.end) out[rest] = grad_t<T>(grad_f<T>(g[rest]) * c);
 }
 
-template <int kCap>
+template <bool kInArgs>
 __global__ void __launch_bounds__(kClipThreads, kCtasPerSm)
-    grad_clip_kernel(const __grid_constant__ GradTable<kCap> t, const double* partials,
+    grad_clip_kernel(const __grid_constant__ Small small, const Table t, const double* partials,
                      float max_norm, float* norm) {
   __shared__ double red[kClipThreads / 32];
   __shared__ float factor;
+  extern __shared__ int32_t first[];
   double sum = 0.0;
+  const Finder<kInArgs> finder{small, t, load_first<kInArgs>(t, first)};
   cudaGridDependencySynchronize();
   for (int j = threadIdx.x; j < kParts; j += kClipThreads) sum += partials[j];
 #pragma unroll
@@ -260,79 +296,52 @@ __global__ void __launch_bounds__(kClipThreads, kCtasPerSm)
   __syncthreads();
   const float c = factor;
   if (c == 1.0f && t.in_place) return;
-  const int total = t.chunk0[t.n];
   // backwards: the last chunks that the norm read are still in L2
-  int k = total - 1 - (int)blockIdx.x;
-  int i = k >= 0 ? tensor_of(t, k) : 0;
-  for (; k >= 0; k -= gridDim.x) {
-    while (k < t.chunk0[i]) --i;
-    const Span s = span_of(t, i, k);
-    if (t.type[i] == MOE_FP32)
-      span_scale(static_cast<const float*>(t.g[i]), static_cast<float*>(t.out[i]), s, c);
-    else if (t.type[i] == MOE_BF16)
-      span_scale(static_cast<const __nv_bfloat16*>(t.g[i]), static_cast<__nv_bfloat16*>(t.out[i]), s, c);
+  for (int k = t.chunks - 1 - (int)blockIdx.x; k >= 0; k -= gridDim.x) {
+    const Entry e = finder.find(k);
+    const Span s = span_of(t, e, k);
+    if (e.type == MOE_FP32)
+      span_scale(static_cast<const float*>(e.g), static_cast<float*>(e.out), s, c);
+    else if (e.type == MOE_BF16)
+      span_scale(static_cast<const __nv_bfloat16*>(e.g), static_cast<__nv_bfloat16*>(e.out), s, c);
     else
-      span_scale(static_cast<const __half*>(t.g[i]), static_cast<__half*>(t.out[i]), s, c);
+      span_scale(static_cast<const __half*>(e.g), static_cast<__half*>(e.out), s, c);
   }
 }
 
 int element_size(int type) { return type == MOE_FP32 ? 4 : 2; }
 
-int chunks_of(const void* g, int64_t size, int es, int vectors) {
-  if (size == 0) return 0;
-  const int64_t head = (int64_t)((0 - reinterpret_cast<uintptr_t>(g)) & 127) / es;
-  const int64_t rest = size > head ? size - head : 1, len = vectors * (kClipThreads * 16 / es);
-  return (int)((rest + len - 1) / len);
-}
+int clip_grid() { return std::min(kParts, kCtasPerSm * moe_device_sm_count()); }
 
 // Vectors per thread and chunk: fewer where the tensors are small, so that
-// the chunks still go round the CTAs that fit on the device.
-int vectors_of(const moe_grad_list& l, int ctas) {
+// the chunks still go round the CTAs that fit on a device.
+int vectors_of(const moe_grad_list& l) {
   int64_t bytes = 0;
   for (int i = 0; i < l.n; ++i) bytes += l.sizes[i] * element_size(l.types[i]);
-  const int64_t each = bytes / ((int64_t)ctas * kClipThreads * 16);
+  const int64_t each = bytes / ((int64_t)kParts * kClipThreads * 16);
   return each >= kVectors ? kVectors : each < 1 ? 1 : (int)each;
 }
 
-// Runs f(table) over the list's tensors, kCap at a time; tensors without
-// elements are left out.
-template <int kCap, typename F>
-cudaError_t over_tables(const moe_grad_list& l, int ctas, F&& f) {
-  int at = 0;
-  bool first = true;
-  do {
-    GradTable<kCap> t;
-    t.n = 0;
-    t.chunk0[0] = 0;
-    t.in_place = 1;
-    t.vectors = vectors_of(l, ctas);
-    for (; at < l.n && t.n < kCap; ++at) {
-      if (l.sizes[at] == 0) continue;
-      const int i = t.n++;
-      t.g[i] = l.grads[at];
-      t.out[i] = l.out ? l.out[at] : const_cast<void*>(l.grads[at]);
-      if (t.out[i] != t.g[i]) t.in_place = 0;
-      t.size[i] = l.sizes[at];
-      t.type[i] = (uint8_t)l.types[at];
-      t.chunk0[i + 1] = t.chunk0[i] + chunks_of(t.g[i], t.size[i], element_size(l.types[at]), t.vectors);
-    }
-    const cudaError_t e = f(t, first);
-    if (e != cudaSuccess) return e;
-    first = false;
-  } while (at < l.n);
-  return cudaSuccess;
-}
-
+// Runs over the list's tensors with elements: put(entry index, entry). Fills
+// the sizes of *t.
 template <typename F>
-cudaError_t over_list(const moe_grad_list& l, int ctas, F&& f) {
-  // the table is copied to the device with every launch: no larger than needed
-  if (l.n <= 16) return over_tables<16>(l, ctas, f);
-  if (l.n <= 128) return over_tables<128>(l, ctas, f);
-  if (l.n <= 512) return over_tables<512>(l, ctas, f);
-  return over_tables<kMaxTensors>(l, ctas, f);
+void entries_of(const moe_grad_list& l, Table* t, F&& put) {
+  t->n = 0;
+  t->chunks = 0;
+  t->in_place = 1;
+  t->vectors = vectors_of(l);
+  for (int i = 0; i < l.n; ++i) {
+    if (l.sizes[i] == 0) continue;
+    const int es = element_size(l.types[i]);
+    void* const out = l.out ? l.out[i] : const_cast<void*>(l.grads[i]);
+    if (out != l.grads[i]) t->in_place = 0;
+    put(t->n++, Entry{l.grads[i], out, l.sizes[i], t->chunks, l.types[i]});
+    const int64_t head = (int64_t)((0 - reinterpret_cast<uintptr_t>(l.grads[i])) & 127) / es;
+    const int64_t rest = l.sizes[i] > head ? l.sizes[i] - head : 1;
+    const int64_t len = t->vectors * (kClipThreads * 16 / es);
+    t->chunks += (int)((rest + len - 1) / len);
+  }
 }
-
-int clip_grid(int sms) { return std::min(kParts, kCtasPerSm * sms); }
 
 int check_list(const moe_grad_list* l) {
   if (!l) return MOE_ERR_NULL;
@@ -353,6 +362,28 @@ int check_list(const moe_grad_list* l) {
   return MOE_OK;
 }
 
+// The kernels' arguments for a list. A table was checked when it was made.
+struct Launch {
+  Small small;
+  Table t;
+  size_t smem;
+};
+int launch_of(const moe_grad_list& l, Launch* a) {
+  if (l.n <= kSmall) {
+    const int bad = check_list(&l);
+    if (bad != MOE_OK) return bad;
+    a->t.entries = nullptr;
+    entries_of(l, &a->t, [&](int i, const Entry& e) { a->small.e[i] = e; });
+    a->smem = 0;
+    return MOE_OK;
+  }
+  if (!l.table) return MOE_ERR_NULL;
+  if (!aligned(l.table, 16)) return MOE_ERR_ALIGN;
+  a->t = Table{static_cast<const Entry*>(l.table), l.plan[0], l.plan[1], l.plan[2], l.plan[3]};
+  a->smem = a->t.n <= kSearch ? (size_t)a->t.n * 4 : 0;
+  return MOE_OK;
+}
+
 }  // namespace
 
 }  // namespace moe
@@ -361,41 +392,57 @@ using namespace moe;
 
 extern "C" {
 
-int moe_grad_sumsq(const moe_grad_list* list, double* partials, void* stream) {
+size_t moe_grad_table_size(const moe_grad_list* list) {
+  if (check_list(list) != MOE_OK || list->n <= kSmall) return 0;
+  return (size_t)list->n * sizeof(Entry);
+}
+
+int moe_grad_table(moe_grad_list* list, void* host_table) {
   const int bad = check_list(list);
   if (bad != MOE_OK) return bad;
-  if (!partials) return MOE_ERR_NULL;
+  if (list->n <= kSmall) return MOE_OK;
+  if (!host_table) return MOE_ERR_NULL;
+  Entry* const e = static_cast<Entry*>(host_table);
+  Table t{};
+  entries_of(*list, &t, [&](int i, const Entry& x) { e[i] = x; });
+  list->plan[0] = t.n;
+  list->plan[1] = t.chunks;
+  list->plan[2] = t.in_place;
+  list->plan[3] = t.vectors;
+  return MOE_OK;
+}
+
+int moe_grad_sumsq(const moe_grad_list* list, double* partials, void* stream) {
+  if (!list || !partials) return MOE_ERR_NULL;
   if (!aligned(partials, 8)) return MOE_ERR_ALIGN;
+  Launch a;
+  const int r = launch_of(*list, &a);
+  if (r != MOE_OK) return r;
   NvtxRange range("moe_grad_sumsq");
   cudaStream_t s = static_cast<cudaStream_t>(stream);
-  const int most = clip_grid(moe_device_sm_count());
-  auto go = [&](const auto& t, bool first) {
-    const int total = t.chunk0[t.n];
-    const int grid = total < 1 ? 1 : std::min(most, total);
-    grad_sumsq_kernel<<<grid, kClipThreads, 0, s>>>(t, partials, first ? 0 : 1);
-    return cudaGetLastError();
-  };
-  return cuda_status(over_list(*list, most, go));
+  const int grid = std::max(1, std::min(clip_grid(), a.t.chunks));
+  if (a.t.entries)
+    grad_sumsq_kernel<false><<<grid, kClipThreads, a.smem, s>>>(a.small, a.t, partials);
+  else
+    grad_sumsq_kernel<true><<<grid, kClipThreads, a.smem, s>>>(a.small, a.t, partials);
+  return cuda_status(cudaGetLastError());
 }
 
 int moe_grad_clip(const moe_grad_list* list, const double* partials, float max_norm, float* norm,
                   void* stream) {
-  const int bad = check_list(list);
-  if (bad != MOE_OK) return bad;
   if (!(max_norm >= 0.0f)) return MOE_ERR_SHAPE;
-  if (!partials || !norm) return MOE_ERR_NULL;
+  if (!list || !partials || !norm) return MOE_ERR_NULL;
   if (!aligned(partials, 8) || !aligned(norm, 4)) return MOE_ERR_ALIGN;
+  Launch a;
+  const int r = launch_of(*list, &a);
+  if (r != MOE_OK) return r;
   NvtxRange range("moe_grad_clip");
   cudaStream_t s = static_cast<cudaStream_t>(stream);
-  const int most = clip_grid(moe_device_sm_count());
-  auto go = [&](const auto& t, bool) {
-    const int total = t.chunk0[t.n];
-    const int grid = total < 1 ? 1 : std::min(most, total);
-    using Table = std::decay_t<decltype(t)>;
-    void (*kernel)(const Table, const double*, float, float*) = grad_clip_kernel<Table::cap>;
-    return launch_dependent(kernel, (unsigned)grid, kClipThreads, 0, s, t, partials, max_norm, norm);
-  };
-  return cuda_status(over_list(*list, most, go));
+  const int grid = std::max(1, std::min(clip_grid(), a.t.chunks));
+  void (*kernel)(const Small, const Table, const double*, float, float*) =
+      a.t.entries ? grad_clip_kernel<false> : grad_clip_kernel<true>;
+  return cuda_status(launch_dependent(kernel, (unsigned)grid, kClipThreads, a.smem, s, a.small, a.t,
+                                      partials, max_norm, norm));
 }
 
 }  // extern "C"

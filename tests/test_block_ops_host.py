@@ -111,7 +111,7 @@ def grad_struct(c, ptrs, sizes, types, out=None):
     cast, pp = ctypes.cast, ctypes.POINTER(ctypes.c_void_p)
     st = c.moe_grad_list(n, cast(arr, pp), None if oarr is None else cast(oarr, pp),
                          cast(s, ctypes.POINTER(ctypes.c_int64)),
-                         cast(t, ctypes.POINTER(ctypes.c_int32)))
+                         cast(t, ctypes.POINTER(ctypes.c_int32)), None)
     st.keep = (arr, oarr, s, t)
     return st
 
@@ -140,6 +140,42 @@ def test_clip_arguments_refused(capi):
     bad = capi.moe_grad_list(-1)
     assert lib.moe_grad_sumsq(ctypes.byref(bad), P, None) == SHAPE
     assert lib.moe_grad_sumsq(ctypes.byref(capi.moe_grad_list(1)), P, None) == NULL
+
+
+def test_gradient_tables(capi):
+    """The table of a longer list: entries of 32 bytes (address, output, size,
+    first chunk, type) of the tensors with elements, chunks in order."""
+    import struct
+    lib = capi.LIB
+    n = 40
+    sizes = [0 if i % 7 == 3 else 100000 * i + 5 for i in range(n)]
+    ptrs = [P + (i << 24) + 4 * (i % 3) for i in range(n)]
+    types = [2 if i % 2 else 0 for i in range(n)]
+    st = grad_struct(capi, ptrs, sizes, types)
+    nbytes = lib.moe_grad_table_size(ctypes.byref(st))
+    assert nbytes == 32 * n
+    buf = ctypes.create_string_buffer(nbytes)
+    assert lib.moe_grad_table(ctypes.byref(st), buf) == 0
+    assert lib.moe_grad_table(ctypes.byref(st), None) == NULL
+    kept = [i for i in range(n) if sizes[i]]
+    at = 0
+    for k, i in enumerate(kept):
+        g, out, size, chunk0, kind = struct.unpack_from("<QQqii", buf, 32 * k)
+        assert (g, out, size, kind) == (ptrs[i], ptrs[i], sizes[i], types[i])
+        assert chunk0 == at
+        es = 4 if types[i] == 2 else 2
+        total = sum(s * (4 if t == 2 else 2) for s, t in zip(sizes, types))
+        length = max(1, min(8, total // (1024 * 256 * 16))) * 256 * 16 // es
+        head = -g % 128 // es
+        at += max(1, -(-(size - head) // length))
+    # without its table a longer list is refused; a short one needs none
+    assert lib.moe_grad_sumsq(ctypes.byref(st), P, None) == NULL
+    assert lib.moe_grad_clip(ctypes.byref(st), P, 1.0, P, None) == NULL
+    st.table = P + 8
+    assert lib.moe_grad_sumsq(ctypes.byref(st), P, None) == ALIGN
+    short = grad_struct(capi, ptrs[:32], sizes[:32], types[:32])
+    assert lib.moe_grad_table_size(ctypes.byref(short)) == 0
+    assert lib.moe_grad_table(ctypes.byref(short), None) == 0
 
 
 def test_gradient_overlaps(capi):

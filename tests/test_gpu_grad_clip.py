@@ -76,7 +76,7 @@ def test_clip(capi, sizes, types, out_of_place):
         check(capi, grads_of(sizes, types), max_norm, out_of_place)
 
 
-@pytest.mark.parametrize("n", [33, 256, 257, 700])
+@pytest.mark.parametrize("n", [31, 32, 33, 256, 257, 700, 5000])
 def test_many_tensors(capi, n):
     sizes = [(i * 37) % 1000 for i in range(n)]
     check(capi, grads_of(sizes, [FP32, BF16]), 1.0, False)
