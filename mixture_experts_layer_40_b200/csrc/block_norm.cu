@@ -638,30 +638,45 @@ __global__ void __launch_bounds__(kBackThreads, 1) block_norm_backward_kernel(co
       store8<Act, kVec>(p.dz, e0 + at.col[c], at.n[c], at.stride, e[c]);
     }
   }
-  // the CTA's column sums: its teams' in turn, through the ring's memory
-  // (every thread has read its own slots; the others' are behind the barrier)
+  // the CTA's column sums: each team's through shared memory, over the slots
+  // (every thread has read its own; the others' are behind the barrier)
   if (kVec) ask_wait(0);
   __syncthreads();
   float* const sum = reinterpret_cast<float*>(ring);
-  for (int t = 0; t < at.teams; ++t) {
-    if (at.team == t) {
 #pragma unroll
-      for (int c = 0; c < kNC; ++c)
+  for (int c = 0; c < kNC; ++c) {
+    float a[8], b[8];
 #pragma unroll
-        for (int i = 0; i < 8; ++i)
-          if (i < at.n[c]) {
-            const int h = at.col[c] + i * at.stride;
-            float a[2], b[2];
-            unpack_f32x2(s_pre[c][i / 2], a[0], a[1]);
-            unpack_f32x2(s_c[c][i / 2], b[0], b[1]);
-            sum[h] = a[i % 2] + (t > 0 ? sum[h] : 0.0f);
-            sum[H + h] = b[i % 2] + (t > 0 ? sum[H + h] : 0.0f);
-          }
+    for (int i = 0; i < 4; ++i) {
+      unpack_f32x2(s_pre[c][i], a[2 * i], a[2 * i + 1]);
+      unpack_f32x2(s_c[c][i], b[2 * i], b[2 * i + 1]);
     }
-    __syncthreads();
+    float* const dst = sum + at.team * 2 * H + at.col[c];
+    if (kVec) {
+      if (at.n[c] > 0) {
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+          reinterpret_cast<float4*>(dst)[i] =
+              make_float4(a[4 * i], a[4 * i + 1], a[4 * i + 2], a[4 * i + 3]);
+          reinterpret_cast<float4*>(dst + H)[i] =
+              make_float4(b[4 * i], b[4 * i + 1], b[4 * i + 2], b[4 * i + 3]);
+        }
+      }
+    } else {
+#pragma unroll
+      for (int i = 0; i < 8; ++i)
+        if (i < at.n[c]) {
+          dst[i * at.stride] = a[i];
+          dst[H + i * at.stride] = b[i];
+        }
+    }
   }
-  for (int h = threadIdx.x; h < 2 * H; h += blockDim.x)
-    p.part[(int64_t)blockIdx.x * 2 * H + h] = sum[h];
+  __syncthreads();
+  for (int h = threadIdx.x; h < 2 * H; h += blockDim.x) {
+    float v = sum[h];
+    for (int t = 1; t < at.teams; ++t) v += sum[t * 2 * H + h];
+    p.part[(int64_t)blockIdx.x * 2 * H + h] = v;
+  }
 }
 
 struct ColumnArgs {
@@ -746,7 +761,8 @@ Plan plan_of(int64_t T, int H, int per_column, bool vec, int sms, bool backward)
   q.stages = q.vec ? (int)(room / stage < kMaxStages ? room / stage : kMaxStages) : 0;
   q.smem = fixed + q.stages * stage;
   // the backward's column sums of the teams meet in the same memory
-  if (backward && q.smem < (size_t)8 * H) q.smem = (size_t)8 * H;
+  const size_t sums = (size_t)q.teams * 2 * H * 4;
+  if (backward && q.smem < sums) q.smem = sums;
   return q;
 }
 
