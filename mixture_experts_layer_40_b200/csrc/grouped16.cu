@@ -282,23 +282,30 @@ struct TileAt {
 // tile -> (group, row tile of the group, column tile), columns fastest: the
 // column tiles of one row tile run side by side and share its rows in L2.
 // Called by whole warps.
-MOE_DEV TileAt tile_at(int tile, const int* prefix, int n_groups, int n_tiles) {
+MOE_DEV TileAt tile_at(uint32_t tile, const int* prefix, int n_groups, int n_tiles) {
+  const int row_tile = (int)(tile / (uint32_t)n_tiles);
   int lo = 0, hi = n_groups;
   while (hi - lo > 1) {
     const int mid = (lo + hi) >> 1;
-    if ((int64_t)prefix[mid] * n_tiles <= tile) lo = mid; else hi = mid;
+    if (prefix[mid] <= row_tile) lo = mid; else hi = mid;
   }
-  const int local = tile - prefix[lo] * n_tiles;
   TileAt t;
   t.g = uniform(lo);
-  t.m = uniform(local / n_tiles);
-  t.n = uniform(local - t.m * n_tiles);
+  t.m = uniform(row_tile - prefix[lo]);
+  t.n = uniform((int)(tile - (uint32_t)row_tile * (uint32_t)n_tiles));
   return t;
 }
 
-// Group table into shared memory, by one warp: each group's rows and start
-// (zero rows for a group that fails its check, which is flagged), and the
-// running number of row tiles (tile_rows rows each; 0: m_tiles for every
+// The groups' rows and starts into shared memory, by the whole CTA
+MOE_DEV void load_groups(const Args16& p, Shared16& sh) {
+  for (int g = threadIdx.x; g < p.n_groups; g += blockDim.x) {
+    sh.rows[g] = p.group_rows[g];
+    sh.start[g] = p.group_start[g];
+  }
+}
+
+// Checks them, by one warp (a group that fails is flagged and gets no rows),
+// and adds up the row tiles (tile_rows rows each; 0: m_tiles for every
 // group). Starts must ascend without overlap, so that no row of the output
 // has two writers.
 MOE_DEV void scan_groups(const Args16& p, Shared16& sh, int lane, int tile_rows) {
@@ -309,8 +316,8 @@ MOE_DEV void scan_groups(const Args16& p, Shared16& sh, int lane, int tile_rows)
     const int g = base + lane;
     int r = 0, st = 0;
     if (g < p.n_groups) {
-      r = p.group_rows[g];
-      st = p.group_start[g];
+      r = sh.rows[g];
+      st = sh.start[g];
     }
     bool ok = r >= 0 && (r == 0 || (st >= 0 && (int64_t)st + r <= p.rows));
     // the largest end before this group
@@ -339,7 +346,6 @@ MOE_DEV void scan_groups(const Args16& p, Shared16& sh, int lane, int tile_rows)
     }
     if (g < p.n_groups) {
       sh.rows[g] = r;
-      sh.start[g] = st;
       sh.prefix[g + 1] = carry + incl;
     }
     carry += __shfl_sync(0xffffffffu, incl, 31);
@@ -445,8 +451,10 @@ __global__ void __cluster_dims__(kCtas, 1, 1) __launch_bounds__(128 + 128 * kSub
     prefetch_tensormap(&tm_x);
     prefetch_tensormap(&tm_x32);
   }
+  if (warp == 2) alloc16<kCtas>(smem_u32(&sh.tmem_base), C::tmem_cols);
+  load_groups(p, sh);
+  __syncthreads();
   if (warp == 2) {
-    alloc16<kCtas>(smem_u32(&sh.tmem_base), C::tmem_cols);
     scan_groups(p, sh, lane, kNT);
   }
   tc_fence_before();
@@ -464,8 +472,8 @@ __global__ void __cluster_dims__(kCtas, 1, 1) __launch_bounds__(128 + 128 * kSub
   if (C::low) {
     float best = 0.0f;
     for (int h = kBM; h > 0; h -= low_step(kWay == kForward)) {
-      const int64_t tiles = (int64_t)row_tiles * ((p.N + h - 1) / h);
-      const int64_t rounds = (tiles + teams - 1) / teams;
+      const uint32_t tiles = (uint32_t)row_tiles * (uint32_t)((p.N + h - 1) / h);
+      const uint32_t rounds = (tiles + teams - 1) / (uint32_t)teams;
       const float cost = (float)rounds * low_tile_ns(h, C::x_box, tiles, teams);
       if (h == kBM || cost < best) {
         best = cost;
@@ -475,7 +483,7 @@ __global__ void __cluster_dims__(kCtas, 1, 1) __launch_bounds__(128 + 128 * kSub
     }
   }
   const int n_tiles = (p.N + height - 1) / height;
-  const int64_t total = (int64_t)row_tiles * n_tiles;
+  const uint32_t total = (uint32_t)row_tiles * (uint32_t)n_tiles;  // checked by the host
   volatile int* abort = &sh.abort;
   const int kb_n = (p.kblocks + C::depth - 1) / C::depth;
 
@@ -488,8 +496,8 @@ __global__ void __cluster_dims__(kCtas, 1, 1) __launch_bounds__(128 + 128 * kSub
       Cursor<C::stages, C::stage_bytes> at(smem_u32(sh.full), smem_u32(sh.empty));
       // a pair's loads all count on its first CTA's barrier
       const uint32_t to_leader = kCtas == 2 ? in_leader(at.full) - at.full : 0;
-      for (int64_t tile = team; ok && tile < total; tile += teams) {
-        const TileAt t = tile_at((int)tile, sh.prefix, p.n_groups, n_tiles);
+      for (uint32_t tile = team; ok && tile < total; tile += teams) {
+        const TileAt t = tile_at(tile, sh.prefix, p.n_groups, n_tiles);
         const RowTile rt = row_tile<kNT>(sh.start[t.g], sh.rows[t.g], t.m);
         const int half = rt.cols / kCtas;
         const int pieces = (half + C::x_box - 1) / C::x_box;
@@ -558,8 +566,8 @@ __global__ void __cluster_dims__(kCtas, 1, 1) __launch_bounds__(128 + 128 * kSub
       const uint64_t desc_w = kWay == kForward ? smem_desc_sw128(ring) : smem_desc_mn_sw128(ring);
       const uint64_t desc_x = smem_desc_sw128(ring + C::a_bytes);
       constexpr uint64_t step_w = kWay == kForward ? kStepK : kStepMN;
-      for (int64_t tile = team; ok && tile < total; tile += teams, ++used) {
-        const TileAt t = tile_at((int)tile, sh.prefix, p.n_groups, n_tiles);
+      for (uint32_t tile = team; ok && tile < total; tile += teams, ++used) {
+        const TileAt t = tile_at(tile, sh.prefix, p.n_groups, n_tiles);
         const RowTile rt = row_tile<kNT>(sh.start[t.g], sh.rows[t.g], t.m);
         const uint32_t idesc = p.idesc | ((uint32_t)(rt.cols >> 3) << 17);
         // accumulators in use: tile by tile in turn, or both by each tile
@@ -613,8 +621,8 @@ __global__ void __cluster_dims__(kCtas, 1, 1) __launch_bounds__(128 + 128 * kSub
     const int per_row = 32 * es / 16;  // 16-byte pieces of a row's 32 columns
     const int piece = lane % per_row, row0 = lane / per_row, row_step = 32 / per_row;
     int used = 0;
-    for (int64_t tile = team; tile < total; tile += teams, ++used) {
-      const TileAt t = tile_at((int)tile, sh.prefix, p.n_groups, n_tiles);
+    for (uint32_t tile = team; tile < total; tile += teams, ++used) {
+      const TileAt t = tile_at(tile, sh.prefix, p.n_groups, n_tiles);
       const RowTile rt = row_tile<kNT>(sh.start[t.g], sh.rows[t.g], t.m);
       const int buf = kSub == 1 ? used & 1 : sub;
       const uint32_t full_phase = (uint32_t)(kSub == 1 ? used >> 1 : used) & 1u;
@@ -856,8 +864,10 @@ __global__ void __cluster_dims__(kCtas, 1, 1) __launch_bounds__(kWThreads, 1)
     prefetch_tensormap(&tm_b);
     prefetch_tensormap(&tm_out);
   }
+  if (warp == 2) alloc16<kCtas>(smem_u32(&sh.tmem_base), 2 * kBN);
+  load_groups(p, sh);
+  __syncthreads();
   if (warp == 2) {
-    alloc16<kCtas>(smem_u32(&sh.tmem_base), 2 * kBN);
     scan_groups(p, sh, lane, 0);
   }
   tc_fence_before();
@@ -867,7 +877,7 @@ __global__ void __cluster_dims__(kCtas, 1, 1) __launch_bounds__(kWThreads, 1)
 
   const uint32_t tmem_base = sh.tmem_base;
   const int team = blockIdx.x / kCtas, teams = gridDim.x / kCtas;
-  const int64_t total = (int64_t)sh.prefix[p.n_groups] * p.n_tiles;
+  const uint32_t total = (uint32_t)sh.prefix[p.n_groups] * (uint32_t)p.n_tiles;  // checked by the host
   volatile int* abort = &sh.abort;
 
   if (warp < 4) asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kWRegsCtl));
@@ -880,8 +890,8 @@ __global__ void __cluster_dims__(kCtas, 1, 1) __launch_bounds__(kWThreads, 1)
       bool ok = true;
       Cursor<C::stages, C::stage_bytes> at(smem_u32(sh.full), smem_u32(sh.empty));
       const uint32_t to_leader = kCtas == 2 ? in_leader(at.full) - at.full : 0;
-      for (int64_t tile = team; ok && tile < total; tile += teams) {
-        const TileAt t = tile_at((int)tile, sh.prefix, p.n_groups, p.n_tiles);
+      for (uint32_t tile = team; ok && tile < total; tile += teams) {
+        const TileAt t = tile_at(tile, sh.prefix, p.n_groups, p.n_tiles);
         const int rows = uniform(sh.rows[t.g]);
         const int kb_n = (rows + kBK - 1) / kBK;
         const int a0 = (t.m * kCtas + rank) * kBM, b0 = t.n * kBN + rank * kHalf;
@@ -943,8 +953,8 @@ __global__ void __cluster_dims__(kCtas, 1, 1) __launch_bounds__(kWThreads, 1)
     // ---------------------------------------------- rows behind a group cleared
     int it = 0;
     uint32_t part_phase = 0;
-    for (int64_t tile = team; tile < total; tile += teams) {
-      const TileAt t = tile_at((int)tile, sh.prefix, p.n_groups, p.n_tiles);
+    for (uint32_t tile = team; tile < total; tile += teams) {
+      const TileAt t = tile_at(tile, sh.prefix, p.n_groups, p.n_tiles);
       const int rows = sh.rows[t.g];
       const int kb_n = (rows + kBK - 1) / kBK;
       it += kb_n;
@@ -982,8 +992,8 @@ __global__ void __cluster_dims__(kCtas, 1, 1) __launch_bounds__(kWThreads, 1)
       bool ok = true;
       Cursor<C::stages, C::stage_bytes> at(smem_u32(sh.full), smem_u32(sh.empty));
       const uint64_t desc_a = smem_desc_mn_sw128(ring), desc_b = smem_desc_mn_sw128(ring + kABytes);
-      for (int64_t tile = team; ok && tile < total; tile += teams) {
-        const TileAt t = tile_at((int)tile, sh.prefix, p.n_groups, p.n_tiles);
+      for (uint32_t tile = team; ok && tile < total; tile += teams) {
+        const TileAt t = tile_at(tile, sh.prefix, p.n_groups, p.n_tiles);
         const int rows = uniform(sh.rows[t.g]);
         const int kb_n = (rows + kBK - 1) / kBK;
         int in_segment = 0;
@@ -1041,8 +1051,8 @@ __global__ void __cluster_dims__(kCtas, 1, 1) __launch_bounds__(kWThreads, 1)
     const bool direct = p.accumulate && p.out_type != MOE_FP32;
     int used = 0;
     bool ok = true;
-    for (int64_t tile = team; ok && tile < total; tile += teams) {
-      const TileAt t = tile_at((int)tile, sh.prefix, p.n_groups, p.n_tiles);
+    for (uint32_t tile = team; ok && tile < total; tile += teams) {
+      const TileAt t = tile_at(tile, sh.prefix, p.n_groups, p.n_tiles);
       const int kb_n = (sh.rows[t.g] + kBK - 1) / kBK;
       if (kb_n == 0 && p.accumulate) continue;
       const int segments = (kb_n + kSegment - 1) / kSegment;
