@@ -1292,8 +1292,20 @@ cudaError_t launch_grouped_wgrad(const Groups16& gr, bool f16, int out_type, int
     e = out_type == MOE_FP32 ? make_tmap_f32_3d(&mo, dw, K, N, gr.n_groups, 32, 32)
                              : make_tmap_16b_3d(&mo, dw, K, N, gr.n_groups, 64, 32);
   if (e != cudaSuccess) return e;
-  const int64_t pairs = (int64_t)gr.n_groups * ((N + 255) / 256) * ((K + 255) / 256);
-  if (N > kBM && pairs >= sms / 2) return launch_wg<2, 256>(p, ma, mb, ma16, mb16, mo, stream, sms);
+  // Pairs of CTAs on 256 x 256 of dw, or single ones on 128 x 128, by the time
+  // of their rounds: either takes in 32 KB a k-block and SM, but the pair's
+  // covers four times as much for two SMs; dw goes out at the SM's share of
+  // HBM while the next tile's blocks come in.
+  const float blocks = (float)((gr.rows / gr.n_groups + kBK - 1) / kBK);
+  auto cost = [&](int side, int units, int bytes) {
+    const int64_t tiles = (int64_t)gr.n_groups * ((N + side - 1) / side) * ((K + side - 1) / side);
+    const int64_t rounds = (tiles + units - 1) / units;
+    const float in = blocks * 32768.0f / kSmIn, out = (float)bytes / (kHbm / 148.0f);
+    return (float)rounds * (in > out ? in : out) + out;
+  };
+  const int es = out_type == MOE_FP32 ? 4 : 2;
+  if (N > kBM && cost(256, sms / 2, 128 * 256 * es) < cost(128, sms, 128 * 128 * es))
+    return launch_wg<2, 256>(p, ma, mb, ma16, mb16, mo, stream, sms);
   return launch_wg<1, 128>(p, ma, mb, ma16, mb16, mo, stream, sms);
 }
 
