@@ -744,6 +744,11 @@ Plan plan_of(int64_t T, int H, int per_column, bool vec, int sms, bool backward)
   const int chunks = (H + 7) / 8;
   const int most1 = backward ? kBackThreads : kNormThreads;
   q.nc = chunks <= most1 ? 1 : chunks <= 2 * kBackThreads ? 2 : 4;
+  // Where the backward has many rows, 16 columns a thread from 264 columns on:
+  // twice the rows in flight (8192 rows of 512, 2048, 4096 columns: 16.7, 47.2,
+  // 85.1 us against 18.8, 58.1, 109.1; at 148 rows 8 columns take 7.0, 7.6,
+  // 9.2 against 8.4, 9.0, 9.6).
+  if (backward && q.nc == 1 && chunks > 32 && T > 6 * sms) q.nc = 2;
   const int threads = q.nc == 1 ? most1 : kBackThreads;
   q.team_warps = (chunks + 32 * q.nc - 1) / (32 * q.nc);
   const int fit = threads / 32 / q.team_warps;
