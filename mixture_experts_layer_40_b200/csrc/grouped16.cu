@@ -364,7 +364,10 @@ MOE_DEV uint32_t pack_f16x2(float lo, float hi) {
 // kSub: tiles of kSub x 128 columns of the output a CTA, one accumulator each.
 template <int kCtas, int kNT, int kSub>
 struct MatCfg {
-  static constexpr int threads = 128 + 128 * kSub;  // an epilogue warpgroup for each accumulator
+  // epilogue warpgroups: one for each accumulator, or two that share the rows
+  // of one (a group alone takes as long as 10 k-blocks of its tile)
+  static constexpr int groups = kSub == 2 || kNT >= 128 ? 2 : 1;
+  static constexpr int threads = 128 + 128 * groups;
   // k-blocks of a stage: two where the tile is so small that waiting and
   // issuing for one (400 cycles) would take longer than its copies and MMAs
   static constexpr int depth = kNT >= 256 ? 1 : 2;
@@ -375,10 +378,10 @@ struct MatCfg {
   // a warp's 32 (fp32: 16) rows x 32 columns of the output, each row padded
   // by 16 bytes against bank conflicts
   static constexpr int turn_bytes = 32 * (32 * 2 + 16);
-  static constexpr int room = 213 * 1024 - 4 * kSub * turn_bytes;
+  static constexpr int room = 213 * 1024 - 4 * groups * turn_bytes;
   static constexpr int stages =
       room / stage_bytes < kMaxStages16 ? room / stage_bytes : kMaxStages16;
-  static constexpr size_t dyn_smem = (size_t)stages * stage_bytes + 4 * kSub * turn_bytes + 1024;
+  static constexpr size_t dyn_smem = (size_t)stages * stage_bytes + 4 * groups * turn_bytes + 1024;
   // accumulators: two tiles of one (the next tile's MMAs run while one is
   // read), or the two of one tile
   static constexpr int tmem_cols = 2 * kNT;
@@ -388,19 +391,23 @@ struct MatCfg {
   static constexpr bool low = kCtas == 1 && kSub == 1;
 };
 
-// Rates for choosing tiles, per ns: what one SM takes in, and all of HBM (both
-// measured with these kernels).
-constexpr float kSmIn = 60.0f, kHbm = 6450.0f;
-constexpr float kIssue = 115.0f;  // ns to wait and issue for one k-block of a small tile
+// Rates for choosing tiles, in bytes per ns, measured with these kernels: what
+// one SM takes in, what all take in from L2 together, and HBM; and the least
+// time of a k-block, ns, that a single-CTA kernel needs from its few KB in flight.
+constexpr float kSmIn = 100.0f, kL2 = 8900.0f, kHbm = 6450.0f, kLowBlock = 225.0f;
 
-// Time of a k-block of a round of `tiles` single-CTA tiles of height h, up to
-// a factor: the SM's own intake, or the share of HBM that the weights need.
-__host__ __device__ inline float low_tile_ns(int h, int x_rows, int64_t tiles, int units) {
-  const float w = (float)(h * kBK * 2), x = (float)(x_rows * kBK * 2);
-  const float active = (float)(tiles < units ? tiles : units);
-  const float in = (w + x) / kSmIn, hbm = w * active / kHbm;
-  const float most = in > hbm ? in : hbm;
-  return most > kIssue ? most : kIssue;
+// Time of a k-block of which each of `active` SMs takes in w bytes of weights,
+// which `share` tiles need at the same time, and x bytes of rows.
+__host__ __device__ inline float block_ns(float w, float x, float active, float share) {
+  const float sm = (w + x) / kSmIn, l2 = (w + x) * active / kL2, hbm = w * active / (share * kHbm);
+  const float in = sm > l2 ? sm : l2;
+  return in > hbm ? in : hbm;
+}
+// the same for a round of `tiles` single-CTA tiles of height h
+__host__ __device__ inline float low_block_ns(int h, int x_rows, int64_t tiles, int units, int share) {
+  const float t = block_ns((float)(h * kBK * 2), (float)(x_rows * kBK * 2),
+                           (float)(tiles < units ? tiles : units), (float)share);
+  return t > kLowBlock ? t : kLowBlock;
 }
 // heights that the loads come in: boxes of 32 weight rows, or of 64 columns
 __host__ __device__ constexpr int low_step(bool k_major) { return k_major ? 32 : 64; }
@@ -423,8 +430,8 @@ MOE_DEV RowTile row_tile(int start, int rows, int m) {
 }
 
 template <int kWay, int kCtas, int kNT, int kSub>
-__global__ void __cluster_dims__(kCtas, 1, 1) __launch_bounds__(128 + 128 * kSub, 1)
-    grouped_matmul_kernel(const __grid_constant__ CUtensorMap tm_w,
+__global__ void __cluster_dims__(kCtas, 1, 1)
+    __launch_bounds__(MatCfg<kCtas, kNT, kSub>::threads, 1) grouped_matmul_kernel(const __grid_constant__ CUtensorMap tm_w,
                           const __grid_constant__ CUtensorMap tm_x,
                           const __grid_constant__ CUtensorMap tm_x32, const Args16 p) {
   using C = MatCfg<kCtas, kNT, kSub>;
@@ -442,7 +449,7 @@ __global__ void __cluster_dims__(kCtas, 1, 1) __launch_bounds__(128 + 128 * kSub
     }
     for (int b = 0; b < 2; ++b) {
       mbar_init(smem_u32(&sh.tfull[b]), 1);
-      mbar_init(smem_u32(&sh.tempty[b]), 4 * kCtas);
+      mbar_init(smem_u32(&sh.tempty[b]), 4 * kCtas * (C::groups / kSub));
     }
     mbar_init(smem_u32(&sh.drained), 1);
     sh.abort = 0;
@@ -474,7 +481,7 @@ __global__ void __cluster_dims__(kCtas, 1, 1) __launch_bounds__(128 + 128 * kSub
     for (int h = kBM; h > 0; h -= low_step(kWay == kForward)) {
       const uint32_t tiles = (uint32_t)row_tiles * (uint32_t)((p.N + h - 1) / h);
       const uint32_t rounds = (tiles + teams - 1) / (uint32_t)teams;
-      const float cost = (float)rounds * low_tile_ns(h, C::x_box, tiles, teams);
+      const float cost = (float)rounds * low_block_ns(h, C::x_box, tiles, teams, 1);
       if (h == kBM || cost < best) {
         best = cost;
         height = h;
@@ -611,7 +618,10 @@ __global__ void __cluster_dims__(kCtas, 1, 1) __launch_bounds__(128 + 128 * kSub
   } else if (warp >= 4) {
     // -------------------------------------------------------------- epilogue
     const int quarter = warp & 3;  // TMEM lanes 32 * quarter .. = output columns
-    const int sub = (warp - 4) >> 2;
+    const int group = (warp - 4) >> 2;
+    const int sub = kSub == 2 ? group : 0;
+    constexpr int kShare = C::groups / kSub;  // groups that share an accumulator
+    const int first = kShare == 2 ? 32 * group : 0;
     const uint32_t lane_addr = tmem_base + ((uint32_t)(quarter * 32) << 16);
     const uint32_t turn = ring + (uint32_t)(C::stages * C::stage_bytes + (warp - 4) * C::turn_bytes);
     const bool wide = p.out_type == MOE_FP32;
@@ -634,34 +644,42 @@ __global__ void __cluster_dims__(kCtas, 1, 1) __launch_bounds__(128 + 128 * kSub
       const int n_end = min(t.n * height + height, p.N);
       const int n = n0 + piece * (16 / es);
       uint8_t* const out = static_cast<uint8_t*>(p.out) + ((int64_t)rt.first * p.N + n) * es;
-      // the `count` rows from c on in the turn buffer, to global memory
-      auto copy_out = [&](int c, int count) {
+      // the rows from c on in the turn buffer, 32 or (fp32) 16, to global memory
+      auto copy_out = [&](int c) {
         __syncwarp();
         if (n < n_end) {
-          for (int j = row0; j < count && c + j < rt.live; j += row_step) {
-            uint32_t q[4];
+          // (count / row_step is 4 in both types)
+          uint32_t q[4][4];
+#pragma unroll
+          for (int k = 0; k < 4; ++k)
             asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];"
-                         : "=r"(q[0]), "=r"(q[1]), "=r"(q[2]), "=r"(q[3])
-                         : "r"(turn + j * pitch + piece * 16)
+                         : "=r"(q[k][0]), "=r"(q[k][1]), "=r"(q[k][2]), "=r"(q[k][3])
+                         : "r"(turn + (row0 + k * row_step) * pitch + piece * 16)
                          : "memory");
-            *reinterpret_cast<uint4*>(out + (int64_t)(c + j) * p.N * es) =
-                make_uint4(q[0], q[1], q[2], q[3]);
+#pragma unroll
+          for (int k = 0; k < 4; ++k) {
+            const int j = c + row0 + k * row_step;
+            if (j < rt.live)
+              *reinterpret_cast<uint4*>(out + (int64_t)j * p.N * es) =
+                  make_uint4(q[k][0], q[k][1], q[k][2], q[k][3]);
           }
         }
         __syncwarp();
       };
-      for (int c = 0; c < rt.live; c += 32) {
+      auto release = [&] {  // all read: the next MMAs may overwrite
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) {
+          if (kCtas == 2) mbar_arrive_relaxed(in_leader(smem_u32(&sh.tempty[buf])));
+          else mbar_arrive(smem_u32(&sh.tempty[buf]));
+        }
+      };
+      if (first >= rt.live) release();  // nothing for this group
+      for (int c = first; c < rt.live; c += 32 * kShare) {
         float v[32];
         tmem_ld32(lane_addr + (uint32_t)(buf * kNT + c), v);
         tmem_wait_ld();
-        if (c + 32 >= rt.live) {  // all read: the next MMAs may overwrite
-          tc_fence_before();
-          __syncwarp();
-          if (lane == 0) {
-            if (kCtas == 2) mbar_arrive_relaxed(in_leader(smem_u32(&sh.tempty[buf])));
-            else mbar_arrive(smem_u32(&sh.tempty[buf]));
-          }
-        }
+        if (c + 32 * kShare >= rt.live) release();
         if (n0 >= n_end) continue;
         if (wide) {
 #pragma unroll
@@ -671,7 +689,7 @@ __global__ void __cluster_dims__(kCtas, 1, 1) __launch_bounds__(128 + 128 * kSub
               asm volatile("st.shared.f32 [%0], %1;" ::"r"(turn + j * pitch + lane * 4),
                            "f"(v[16 * h + j])
                            : "memory");
-            copy_out(c + 16 * h, 16);
+            copy_out(c + 16 * h);
           }
         } else {
 #pragma unroll
@@ -684,7 +702,7 @@ __global__ void __cluster_dims__(kCtas, 1, 1) __launch_bounds__(128 + 128 * kSub
                          "h"((uint16_t)(w >> 16))
                          : "memory");
           }
-          copy_out(c, 32);
+          copy_out(c);
         }
       }
     }
@@ -1202,11 +1220,15 @@ cudaError_t launch_grouped_matmul(const Groups16& gr, bool f16, int out_type, in
   p.idesc = f16 ? 0u : 1u;
   p.status = gr.status;
   // The kernel whose rounds of tiles take the least time, if the groups were
-  // alike: each k-block costs an SM what it takes in or its MMAs, whichever is
-  // longer. Measured against this model (us, K-major): 16 groups of 400 rows,
-  // 1024 x 1024: 2x256x2 18.9, 2x256 21.2, 2x128 31.6, 1x32 76.9; 2 of 821,
-  // 920 x 1184: 18.6, 14.1, 13.6, 32.7; 32 of 8, 4096 x 4096: 183.9, 178.6,
-  // 172.9, 168.2.
+  // alike: CTAs x rows x accumulators of 2x256x2, 2x128, 2x256 and 1x32. Over 43
+  // shapes the choice was within 3% of the best of the four in the mean. Some
+  // of them (us, K-major weights; groups x rows, N x K):
+  //   32 x 384, 4096 x 4096    322   372   348  1669
+  //   16 x 800, 1024 x 1024     31    31    28   102
+  //   2 x 821, 920 x 1184     17.4  10.1  11.7  21.2
+  //   1 x 1, 4096 x 7168      35.8  20.2  28.8  29.7
+  //   8 x 1, 4096 x 7168      75.5  74.3  77.6  73.7
+  //   1 x 310, 728 x 936      15.3  10.5  11.3   9.2
   const int64_t busy = gr.rows < gr.n_groups ? gr.rows : gr.n_groups;
   const int64_t each = (gr.rows + busy - 1) / busy;
   auto cost = [&](int ctas, int nt, int sub) {
@@ -1217,15 +1239,17 @@ cudaError_t launch_grouped_matmul(const Groups16& gr, bool f16, int out_type, in
     const int step = ctas == 1 ? low_step(trans_b) : kBM * ctas * sub;
     for (int h = kBM * ctas * sub; h > 0; h -= step) {
       const int64_t tiles = busy * split * ((N + h - 1) / h), rounds = (tiles + units - 1) / units;
-      const float w = (float)(h / ctas * kBK * 2);
       const float active = (float)(tiles < units ? tiles : units) * ctas;
-      const float in = (w + x) / kSmIn, hbm = w * active / (float)split / kHbm;
+      float kb = block_ns((float)(h / ctas * kBK * 2), x, active, (float)split);
+      const float issue = ctas == 1 ? kLowBlock : nt == 128 ? 135.0f : sub == 1 ? 210.0f : 270.0f;
+      kb = kb > issue ? kb : issue;
       const float mma = 2.0f * (float)(rows * sub) / 1.4f;  // cycles at the clock under load
-      float kb = in > hbm ? in : hbm;
-      kb = kb > kIssue ? kb : kIssue;
-      // a tile with both accumulators is not read while the next one's MMAs run
-      const float t = (float)rounds * ((float)p.kblocks * (kb > mma ? kb : mma) +
-                                       (sub == 2 ? 8.0f * (float)rows : 0.0f)) + 8.0f * (float)rows;
+      const float main = (float)p.kblocks * (kb > mma ? kb : mma);
+      // the epilogue, beside the next tile's MMAs unless the tile has both
+      // accumulators
+      const float out = (sub == 1 && nt >= 128 ? 5.0f : 10.0f) * (float)rows + 500.0f;
+      const float t = sub == 2 ? (float)rounds * (main + out)
+                               : (float)rounds * (main > out ? main : out) + out;
       if (best == 0.0f || t < best) best = t;
     }
     return best;
@@ -1233,7 +1257,7 @@ cudaError_t launch_grouped_matmul(const Groups16& gr, bool f16, int out_type, in
   struct Choice {
     int ctas, nt, sub;
   };
-  constexpr Choice all[] = {{2, 256, 2}, {2, 256, 1}, {2, 128, 1}, {1, 32, 1}};
+  constexpr Choice all[] = {{2, 256, 2}, {2, 128, 1}, {2, 256, 1}, {1, 32, 1}};
   int pick = 0;
   float least = 0.0f;
   for (int i = 0; i < 4; ++i) {
@@ -1262,8 +1286,8 @@ cudaError_t launch_grouped_matmul(const Groups16& gr, bool f16, int out_type, in
   constexpr integral_constant<int, 1> one{};
   constexpr integral_constant<int, 2> two{};
   if (pick == 0) return go(two, integral_constant<int, 256>{}, two);
-  if (pick == 1) return go(two, integral_constant<int, 256>{}, one);
-  if (pick == 2) return go(two, integral_constant<int, 128>{}, one);
+  if (pick == 1) return go(two, integral_constant<int, 128>{}, one);
+  if (pick == 2) return go(two, integral_constant<int, 256>{}, one);
   return go(one, integral_constant<int, 32>{}, one);
 }
 
@@ -1300,7 +1324,7 @@ cudaError_t launch_grouped_wgrad(const Groups16& gr, bool f16, int out_type, int
   auto cost = [&](int side, int units, int bytes) {
     const int64_t tiles = (int64_t)gr.n_groups * ((N + side - 1) / side) * ((K + side - 1) / side);
     const int64_t rounds = (tiles + units - 1) / units;
-    const float in = blocks * 32768.0f / kSmIn, out = (float)bytes / (kHbm / 148.0f);
+    const float in = blocks * 32768.0f * 148.0f / kL2, out = (float)bytes / (kHbm / 148.0f);
     return (float)rounds * (in > out ? in : out) + out;
   };
   const int es = out_type == MOE_FP32 ? 4 : 2;
