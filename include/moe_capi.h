@@ -474,8 +474,9 @@ int moe_grouped_wgrad(int32_t type, int32_t out_type, int32_t n_groups, const in
  *   dpre, dpost, dscale: float [H], for those weights that are given
  *   ws: moe_block_norm_backward_workspace_size(H) bytes, 256-byte aligned; no
  *        other call that may run at the same time can use it.
- * Both statistics are recomputed from r and z. Column sums run in an order
- * that depends on T and H alone: results are reproducible. dx may be dr, and
+ * Both statistics are recomputed from r and z. Column sums run in a fixed
+ * order (by T, H, the types, the alignment and the GPU's SMs): the same call
+ * gives the same bits. dx may be dr, and
  * dz may be z or du; no other overlap. T = 0: dpre, dpost and dscale are zero.
  */
 #define MOE_BLOCK_NORM_MAX_H 16384

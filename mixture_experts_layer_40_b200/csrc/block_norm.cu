@@ -5,14 +5,20 @@
 //   N(v; w) = v * rsqrt(mean(v^2) + eps) * w
 //   r = x + alpha * scale * gate * N(z; post)     u = N(r; pre)
 //
-// One pass over the rows: a team of warps holds a row in registers, so x and
+// One pass over the rows: a team of warps holds a row on the SM, so x and
 // z are read once and r and u written once, whatever the number of norms.
 // The backward recomputes both statistics from the rows it has to read
 // anyway (one more term in a reduction it needs for the gradient), so the
 // forward saves nothing. All arithmetic is fp32; r is rounded when it is
 // stored, and u is computed from the unrounded row.
 //
-// Bound by HBM: a few operations per byte.
+// A few operations per byte, so HBM is the floor; what bounds it is the
+// latency of the row sums (two in the forward, which takes two rows a step;
+// three phases in the backward, one row a team at a time). 4096 rows of 7168
+// in bf16, x, z and gate to r and u: 47 us, 77% of the copy rate; backward of
+// 16384 rows with an fp32 residual stream: 493 to 498 us, 66%. Odd widths go
+// element by element and are bound by instructions: 777 rows of 1409 in fp16,
+// backward, 16.7 us (floor 2.7).
 #include <type_traits>
 
 #include "kernels.cuh"

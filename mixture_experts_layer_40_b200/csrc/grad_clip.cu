@@ -14,6 +14,8 @@
 //
 // Bound by HBM: one read for the norm, one read and one write for the
 // scaling, of which the second read finds in L2 what the first read last.
+// 0.7 G fp32 elements out of place take 1395 us (three passes at the copy
+// rate: 1302), 512 mixed tensors of 150 M elements below the limit 70 (70).
 #include <algorithm>
 #include <type_traits>
 
