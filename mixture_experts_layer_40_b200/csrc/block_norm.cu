@@ -15,7 +15,7 @@
 // A few operations per byte, so HBM is the floor; what bounds it is the
 // latency of the row sums (two in the forward, which takes two rows a step;
 // three phases in the backward, one row a team at a time). 4096 rows of 7168
-// in bf16, x, z and gate to r and u: 47 us, 77% of the copy rate; backward of
+// in bf16, x and z to r and u: 47 us, 77% of the copy rate; backward of
 // 16384 rows with an fp32 residual stream: 493 to 498 us, 66%. Odd widths go
 // element by element and are bound by instructions: 777 rows of 1409 in fp16,
 // backward, 16.7 us (floor 2.7).
