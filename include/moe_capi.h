@@ -431,7 +431,7 @@ typedef enum { MOE_BF16 = 0, MOE_FP16 = 1, MOE_FP32 = 2 } moe_type;
  * multiples of 8 up to 2^20; pointers 16-byte aligned; rows < 2^31 - 256
  * (rows = 0: the row buffers may be NULL). out and dw must not overlap the
  * inputs. status_ws: a device uint32 status word, or NULL (may be the forward
- * workspace); read by moe_get_status.
+ * workspace); read by moe_get_status, which also reports a wait that ran out.
  */
 int moe_grouped_matmul(int32_t type, int32_t out_type, int32_t n_groups, const int32_t* group_rows,
                        const int32_t* group_start, int64_t rows, int32_t K, int32_t N,
@@ -517,6 +517,7 @@ int moe_block_norm_backward(int64_t T, int32_t H, int32_t res_type, int32_t act_
  *   before they clip.
  * moe_grad_clip adds the partials, writes the norm (float [1]) and scales.
  *   max_norm >= 0, infinity allowed. In place nothing is touched when c = 1.
+ *   An infinite norm under an infinite max_norm makes c NaN.
  * Squares are summed in fp64, in a fixed order. A NaN in any gradient makes
  * the norm and every gradient NaN; an infinity makes the norm infinite, the
  * infinite gradients NaN and the others zero.

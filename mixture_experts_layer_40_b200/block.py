@@ -32,7 +32,9 @@ class MoEBlock:
                 r: torch.Tensor | None = None, next_weight: torch.Tensor | None = None,
                 stream=None):
         """r [T, H] like x; with next_weight also u = N(r; next_weight), the
-        next block's input, from the same pass: (r, u)."""
+        next block's input, from the same pass: (r, u). r may be x, in place;
+        there is no backward then, which reads x."""
+        self.x = self.gate = None  # the layer's state is a new forward's from here on
         with torch.cuda.stream(stream):  # None: the current one
             capi.moe_block_norm(x, self.eps, pre_weight=self.pre_weight, u=self.u, stream=stream)
             self.layer.forward(self.u, bias, self.z, stream)
@@ -42,7 +44,8 @@ class MoEBlock:
             capi.moe_block_norm(x, self.eps, pre_weight=next_weight, u=u, z=self.z,
                                 post_weight=self.post_weight, gate=gate, scale=self.scale,
                                 alpha=self.alpha, r=r, stream=stream)
-            self.x, self.gate = x, gate
+            if r.data_ptr() != x.data_ptr():
+                self.x, self.gate = x, gate
             return r if next_weight is None else (r, u)
 
     def backward(self, dr: torch.Tensor, weights: bool = True, stream=None) -> dict:
@@ -52,7 +55,7 @@ class MoEBlock:
         as they were given post_weight, scale and gate; with `weights` also w13
         and w2."""
         if self.x is None:
-            raise ValueError("backward needs a forward before it")
+            raise ValueError("backward needs a forward before it, and not one in place")
         with torch.cuda.stream(stream):  # None: the current one
             dev, H = self.layer.device, self.layer.H
             if self._ws is None:

@@ -242,3 +242,46 @@ def test_binding_refuses_host_tensors(capi):
         capi.make_grad_list([a])
     with pytest.raises(ValueError, match="outputs"):
         capi.make_grad_list([a], [])
+
+
+class FakeLayer:
+    T, H, device = 4, 64, "cpu"
+
+    def __init__(self):
+        self.fail = False
+
+    def forward(self, u, bias, z, stream):
+        if self.fail:
+            raise RuntimeError("layer")
+
+    def backward(self, dz, u, stream):
+        return torch.zeros(4, 64), torch.zeros(4, 2)
+
+
+def test_block_backward_needs_the_forwards_x(capi, monkeypatch):
+    """The backward reads the forward's x: after a forward in place, or one
+    that failed, there is none, and it says so."""
+    from mixture_experts_layer_40_b200.block import MoEBlock
+
+    monkeypatch.setattr(capi, "moe_block_norm", lambda *a, **k: None)
+    monkeypatch.setattr(capi, "moe_block_norm_backward", lambda *a, **k: None)
+    monkeypatch.setattr(capi, "moe_block_norm_backward_workspace_size", lambda H: 16)
+    layer = FakeLayer()
+    block = MoEBlock(layer, torch.ones(64))
+    both = torch.zeros(2, 4, 64)
+    x, r = both[0], both[1]
+
+    with pytest.raises(ValueError, match="forward"):
+        block.backward(r, weights=False)
+    block.forward(x, None, r=r)
+    assert "dx" in block.backward(r, weights=False)
+    assert block.forward(x, None, r=x) is x  # in place
+    with pytest.raises(ValueError, match="in place"):
+        block.backward(r, weights=False)
+    block.forward(x, None)
+    block.backward(r, weights=False)
+    layer.fail = True
+    with pytest.raises(RuntimeError):
+        block.forward(r, None)
+    with pytest.raises(ValueError, match="forward"):
+        block.backward(r, weights=False)

@@ -151,6 +151,17 @@ def test_non_finite(capi):
         assert math.isnan(float(norm)) and torch.isnan(g[0]).all() and torch.isnan(g[1]).all()
 
 
+def test_infinite_limit(capi):
+    """c = inf / (norm + 1e-6): 1 for a finite norm, NaN for an infinite one."""
+    g = grads_of([9000, 50], [FP32, BF16])
+    before = [t.clone() for t in g]
+    clip(capi, g, math.inf)
+    assert all(torch.equal(a, b) for a, b in zip(g, before))
+    g[0][0] = math.inf
+    assert float(clip(capi, g, math.inf)) == math.inf
+    assert all(bool(torch.isnan(t).all()) for t in g)
+
+
 def test_partials_add_over_shards(capi):
     """Two ranks' partials, added, clip both by the norm of all gradients."""
     a, b = grads_of([5000, 3], [FP32], 1), grads_of([70000], [FP32], 2)
