@@ -350,3 +350,40 @@ def test_wgrad_long_groups_keep_fp32(capi):
         for g, (s, c) in enumerate(zip(starts, counts)):
             ref = dy[s:s + c].double().T @ x[s:s + c].double()
             assert float((dw[g] - ref).norm() / ref.norm()) < 2.0 ** -20
+
+
+def test_calls_on_several_streams_at_once(capi):
+    """Each of the kernels beside itself and the others, on streams of their
+    own: the same bits as one call after another."""
+    gen = torch.Generator(device="cuda").manual_seed(8)
+    calls = []
+    for counts, K, N in (([1, 0, 3], 264, 520), ([300, 77, 450], 1032, 776), ([700, 900], 520, 1544),
+                         ([4000], 264, 264)):
+        gr = torch.tensor(counts, dtype=torch.int32, device="cuda")
+        gs = torch.cumsum(gr, 0, dtype=torch.int32) - gr
+        x, dy = randn(gen, sum(counts), K), randn(gen, sum(counts), N)
+        w = randn(gen, len(counts), N, K)
+        calls.append((x, dy, w, gr, gs))
+
+    def outputs():
+        return [(torch.zeros(x.shape[0], w.shape[1], dtype=BF16, device="cuda"),
+                 torch.zeros_like(x), torch.zeros(w.shape, device="cuda"))
+                for x, _, w, _, _ in calls]
+
+    def run(call, out, stream):
+        x, dy, w, gr, gs = call
+        capi.moe_grouped_matmul(x, w, gr, gs, out[0], True, stream=stream)
+        capi.moe_grouped_matmul(dy, w, gr, gs, out[1], False, stream=stream)
+        capi.moe_grouped_wgrad(dy, x, gr, gs, out[2], stream=stream)
+
+    alone, beside = outputs(), outputs()
+    for call, out in zip(calls, alone):
+        run(call, out, None)
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in calls]
+    for _ in range(10):
+        for call, out, stream in zip(calls, beside, streams):
+            run(call, out, stream)
+    torch.cuda.synchronize()
+    for a, b in zip(alone, beside):
+        assert all(torch.equal(p, q) for p, q in zip(a, b))
