@@ -86,6 +86,8 @@ struct alignas(8) Shared16 {
   uint64_t tfull[2];
   uint64_t tempty[2];
   uint64_t drained;
+  uint64_t joined;               // split sums: all parts of a chunk are written
+  uint64_t freed;                // and read
   uint32_t tmem_base;
   int abort;
   int prefix[kMaxGroups16 + 1];
@@ -108,6 +110,20 @@ MOE_DEV uint32_t in_leader(uint32_t addr) {
   uint32_t r;
   asm("mapa.shared::cluster.u32 %0, %1, 0;" : "=r"(r) : "r"(addr));
   return r;
+}
+// and in the cluster's CTA of this rank
+MOE_DEV uint32_t in_cta(uint32_t addr, int rank) {
+  uint32_t r;
+  asm("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(r) : "r"(addr), "r"(rank));
+  return r;
+}
+MOE_DEV float4 ld_cluster_f4(uint32_t addr) {
+  float4 v;
+  asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];"
+               : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w)
+               : "r"(addr)
+               : "memory");
+  return v;
 }
 // Arrival on a barrier of the pair's first CTA. The releasing form, which
 // also publishes the thread's stores to the other CTA, costs a memory barrier
@@ -395,12 +411,16 @@ struct MatCfg {
   static constexpr int x_box = kNT >= 128 ? 32 : 16;
   // a single CTA's tiles may be lower than 128 columns of the output
   static constexpr bool low = kCtas == 1 && kSub == 1;
+  // split sums: rows of a part that lie in the turn buffers at a time, fp32
+  static constexpr int part_rows = 16;
+  static_assert(!low || part_rows * kBM * 4 <= 4 * groups * turn_bytes, "a part's rows");
 };
 
 // Rates for choosing tiles, in bytes per ns, measured with these kernels: what
 // one SM takes in, what all take in from L2 together, and HBM; and the least
 // time of a k-block, ns, that a single-CTA kernel needs from its few KB in flight.
 constexpr float kSmIn = 100.0f, kL2 = 8900.0f, kHbm = 6450.0f, kLowBlock = 225.0f;
+constexpr float kJoin = 1500.0f;  // ns, joining a split sum's parts
 
 // Time of a k-block of which each of `active` SMs takes in w bytes of weights,
 // which `share` tiles need at the same time, and x bytes of rows.
@@ -417,6 +437,11 @@ __host__ __device__ inline float low_block_ns(int h, int x_rows, int64_t tiles, 
 }
 // heights that the loads come in: boxes of 32 weight rows, or of 64 columns
 __host__ __device__ constexpr int low_step(bool k_major) { return k_major ? 32 : 64; }
+// clusters of `split` CTAs that run at a time: those of 4 and 8 do not fill
+// every GPC (33 and 15 of 148 SMs' 37 and 18)
+inline int split_units(int sms, int split) {
+  return split <= 2 ? sms / split : sms * (split == 4 ? 33 : 15) / 148;
+}
 static_assert(16 * (32 * 4 + 16) <= 32 * (32 * 2 + 16), "fp32 rows in the turn buffer");
 
 struct RowTile {
@@ -435,18 +460,24 @@ MOE_DEV RowTile row_tile(int start, int rows, int m) {
   return t;
 }
 
-template <int kWay, int kCtas, int kNT, int kSub>
-__global__ void __cluster_dims__(kCtas, 1, 1)
+// kSplit (single CTAs): a tile's sum over K is split over a cluster of that
+// many CTAs, for few tiles over a long K: each takes its share of the
+// k-blocks, leaves its fp32 part in shared memory, and adds its share of the
+// outputs up from all parts, in the order of the ranks.
+template <int kWay, int kCtas, int kNT, int kSub, int kSplit>
+__global__ void __cluster_dims__(kCtas * kSplit, 1, 1)
     __launch_bounds__(MatCfg<kCtas, kNT, kSub>::threads, 1) grouped_matmul_kernel(const __grid_constant__ CUtensorMap tm_w,
                           const __grid_constant__ CUtensorMap tm_x,
                           const __grid_constant__ CUtensorMap tm_x32, const Args16 p) {
   using C = MatCfg<kCtas, kNT, kSub>;
+  static_assert(kSplit == 1 || (C::low && C::groups == 1 && kNT <= 32), "split tiles");
   __shared__ Shared16 sh;
   extern __shared__ uint8_t dyn_smem[];
   const uint32_t ring = (smem_u32(dyn_smem) + 1023u) & ~1023u;
   const int warp = threadIdx.x >> 5;
   const int lane = threadIdx.x & 31;
   const int rank = kCtas == 1 ? 0 : (int)cluster_rank();
+  const int part = kSplit == 1 ? 0 : (int)cluster_rank();
 
   if (threadIdx.x == 0) {
     for (int s = 0; s < C::stages; ++s) {
@@ -458,6 +489,10 @@ __global__ void __cluster_dims__(kCtas, 1, 1)
       mbar_init(smem_u32(&sh.tempty[b]), 4 * kCtas * (C::groups / kSub));
     }
     mbar_init(smem_u32(&sh.drained), 1);
+    if (kSplit > 1) {
+      mbar_init(smem_u32(&sh.joined), 4 * kSplit);
+      mbar_init(smem_u32(&sh.freed), 4 * kSplit);
+    }
     sh.abort = 0;
     fence_mbar_init();
     prefetch_tensormap(&tm_w);
@@ -471,13 +506,13 @@ __global__ void __cluster_dims__(kCtas, 1, 1)
     scan_groups(p, sh, lane, kNT);
   }
   tc_fence_before();
-  if constexpr (kCtas == 2) cluster_sync();
+  if constexpr (kCtas * kSplit > 1) cluster_sync();
   else __syncthreads();
   tc_fence_after();
 
   const uint32_t tmem_base = sh.tmem_base;
   const int row_tiles = sh.prefix[p.n_groups];
-  const int team = blockIdx.x / kCtas, teams = gridDim.x / kCtas;
+  const int team = blockIdx.x / (kCtas * kSplit), teams = gridDim.x / (kCtas * kSplit);
   // Output columns per tile. With few tiles a round of tiles of 128 would
   // leave SMs idle, and each SM takes in only so much: lower tiles spread the
   // weights over more of them.
@@ -487,7 +522,7 @@ __global__ void __cluster_dims__(kCtas, 1, 1)
     for (int h = kBM; h > 0; h -= low_step(kWay == kForward)) {
       const uint32_t tiles = (uint32_t)row_tiles * (uint32_t)((p.N + h - 1) / h);
       const uint32_t rounds = (tiles + teams - 1) / (uint32_t)teams;
-      const float cost = (float)rounds * low_block_ns(h, C::x_box, tiles, teams, 1);
+      const float cost = (float)rounds * low_block_ns(h, C::x_box, (int64_t)tiles * kSplit, teams * kSplit, 1);
       if (h == kBM || cost < best) {
         best = cost;
         height = h;
@@ -498,7 +533,8 @@ __global__ void __cluster_dims__(kCtas, 1, 1)
   const int n_tiles = (p.N + height - 1) / height;
   const uint32_t total = (uint32_t)row_tiles * (uint32_t)n_tiles;  // checked by the host
   volatile int* abort = &sh.abort;
-  const int kb_n = (p.kblocks + C::depth - 1) / C::depth;
+  const int kb_all = (p.kblocks + C::depth - 1) / C::depth;  // (at least kSplit: the host)
+  const int kb_0 = part * kb_all / kSplit, kb_n = (part + 1) * kb_all / kSplit - kb_0;
 
   if (warp == 0) {
     {
@@ -522,7 +558,8 @@ __global__ void __cluster_dims__(kCtas, 1, 1)
         const int n0 = t.n * height + rank * kBM;
         const uint32_t bytes = kCtas * C::depth * (w_bytes + pieces * C::x_box * kBK * 2);
         // (a second k-block may lie beyond K: zeros)
-        for (int k0 = 0; k0 < kb_n * C::depth * kBK; k0 += C::depth * kBK, ++it, at.next()) {
+        const int k_end = (kb_0 + kb_n) * C::depth * kBK;
+        for (int k0 = kb_0 * C::depth * kBK; k0 < k_end; k0 += C::depth * kBK, ++it, at.next()) {
           if (!warp_wait(at.empty, at.phase ^ 1u, abort, p.status)) {
             ok = false;
             break;
@@ -637,6 +674,7 @@ __global__ void __cluster_dims__(kCtas, 1, 1)
     const int per_row = 32 * es / 16;  // 16-byte pieces of a row's 32 columns
     const int piece = lane % per_row, row0 = lane / per_row, row_step = 32 / per_row;
     int used = 0;
+    uint32_t chunks = 0;  // of split sums
     for (uint32_t tile = team; tile < total; tile += teams, ++used) {
       const TileAt t = tile_at(tile, sh.prefix, p.n_groups, n_tiles);
       const RowTile rt = row_tile<kNT>(sh.start[t.g], sh.rows[t.g], t.m);
@@ -680,6 +718,64 @@ __global__ void __cluster_dims__(kCtas, 1, 1)
           else mbar_arrive(smem_u32(&sh.tempty[buf]));
         }
       };
+      if constexpr (kSplit > 1) {
+        float v[32];
+        tmem_ld32(lane_addr + (uint32_t)(buf * kNT), v);
+        tmem_wait_ld();
+        release();
+        const uint32_t joined = smem_u32(&sh.joined), freed = smem_u32(&sh.freed);
+        const uint32_t parts = ring + (uint32_t)(C::stages * C::stage_bytes);
+        bool ok = true;
+#pragma unroll
+        for (int c = 0; c < kNT; c += C::part_rows) {
+          if (c >= rt.live) break;
+          ok = __all_sync(0xffffffffu,
+                          mbar_wait_pair<2>(freed, (chunks & 1u) ^ 1u, abort, p.status));
+          if (!ok) break;
+#pragma unroll
+          for (int j = 0; j < C::part_rows; ++j)
+            asm volatile("st.shared.f32 [%0], %1;" ::"r"(
+                             parts + (uint32_t)((j * kBM + quarter * 32 + lane) * 4)),
+                         "f"(v[c + j])
+                         : "memory");
+          __syncwarp();
+          if (lane < kSplit) mbar_arrive_release(in_cta(joined, lane));
+          ok = __all_sync(0xffffffffu, mbar_wait_pair<2>(joined, chunks & 1u, abort, p.status));
+          if (!ok) break;
+          // 8 columns of a row at a time
+          const int rows = min(C::part_rows, rt.live - c);
+          for (int i = part * 128 + quarter * 32 + lane; i < rows * (kBM / 8); i += kSplit * 128) {
+            const int row = i / (kBM / 8), col = i % (kBM / 8) * 8;
+            if (t.n * height + col >= n_end) continue;
+            float4 lo = make_float4(0.0f, 0.0f, 0.0f, 0.0f), hi = lo;
+#pragma unroll
+            for (int q = 0; q < kSplit; ++q) {
+              const uint32_t from = in_cta(parts + (uint32_t)((row * kBM + col) * 4), q);
+              const float4 a = ld_cluster_f4(from), b = ld_cluster_f4(from + 16);
+              lo.x += a.x, lo.y += a.y, lo.z += a.z, lo.w += a.w;
+              hi.x += b.x, hi.y += b.y, hi.z += b.z, hi.w += b.w;
+            }
+            uint4* const dst = reinterpret_cast<uint4*>(
+                static_cast<uint8_t*>(p.out) +
+                ((int64_t)(rt.first + c + row) * p.N + t.n * height + col) * es);
+            if (wide) {
+              reinterpret_cast<float4*>(dst)[0] = lo;
+              reinterpret_cast<float4*>(dst)[1] = hi;
+            } else if (f16) {
+              *dst = make_uint4(pack_f16x2(lo.x, lo.y), pack_f16x2(lo.z, lo.w),
+                                pack_f16x2(hi.x, hi.y), pack_f16x2(hi.z, hi.w));
+            } else {
+              *dst = make_uint4(pack_bf16x2(lo.x, lo.y), pack_bf16x2(lo.z, lo.w),
+                                pack_bf16x2(hi.x, hi.y), pack_bf16x2(hi.z, hi.w));
+            }
+          }
+          __syncwarp();
+          if (lane < kSplit) mbar_arrive_release(in_cta(freed, lane));
+          ++chunks;
+        }
+        if (!ok) break;
+        continue;
+      }
       if (first >= rt.live) release();  // nothing for this group
       for (int c = first; c < rt.live; c += 32 * kShare) {
         float v[32];
@@ -715,7 +811,7 @@ __global__ void __cluster_dims__(kCtas, 1, 1)
   }
 
   tc_fence_before();
-  if constexpr (kCtas == 2) cluster_sync();
+  if constexpr (kCtas * kSplit > 1) cluster_sync();
   else __syncthreads();
   tc_fence_after();
   if (warp == 2) dealloc16<kCtas>(tmem_base, C::tmem_cols);
@@ -1166,13 +1262,13 @@ __global__ void __cluster_dims__(kCtas, 1, 1) __launch_bounds__(kWThreads, 1)
 }
 
 // ================================================================ launches
-template <int kWay, int kCtas, int kNT, int kSub>
+template <int kWay, int kCtas, int kNT, int kSub, int kSplit>
 cudaError_t launch_mat(Args16 a, const CUtensorMap& mw, const CUtensorMap& mx,
                        const CUtensorMap& mx32, int64_t row_tiles, cudaStream_t stream, int sms) {
   using C = MatCfg<kCtas, kNT, kSub>;
   static DeviceOnce once;
   cudaError_t e = once.run([] {
-    return cudaFuncSetAttribute(grouped_matmul_kernel<kWay, kCtas, kNT, kSub>,
+    return cudaFuncSetAttribute(grouped_matmul_kernel<kWay, kCtas, kNT, kSub, kSplit>,
                                 cudaFuncAttributeMaxDynamicSharedMemorySize, (int)C::dyn_smem);
   });
   if (e != cudaSuccess) return e;
@@ -1181,8 +1277,10 @@ cudaError_t launch_mat(Args16 a, const CUtensorMap& mw, const CUtensorMap& mx,
   const int lowest = C::low ? low_step(kWay == kForward) : kBM * kCtas * kSub;
   const int64_t tiles = row_tiles * ((a.N + lowest - 1) / lowest);
   if (tiles >= (1ll << 31)) return cudaErrorInvalidValue;
-  const int64_t grid = tiles * kCtas < sms ? tiles * kCtas : sms / kCtas * kCtas;
-  grouped_matmul_kernel<kWay, kCtas, kNT, kSub><<<(unsigned)grid, C::threads, C::dyn_smem, stream>>>(mw, mx, mx32, a);
+  constexpr int kCluster = kCtas * kSplit;
+  const int64_t units = kSplit == 1 ? sms / kCtas : split_units(sms, kSplit);
+  const int64_t grid = (tiles < units ? tiles : units) * kCluster;
+  grouped_matmul_kernel<kWay, kCtas, kNT, kSub, kSplit><<<(unsigned)grid, C::threads, C::dyn_smem, stream>>>(mw, mx, mx32, a);
   return cudaGetLastError();
 }
 
@@ -1241,23 +1339,24 @@ cudaError_t launch_grouped_matmul(const Groups16& gr, bool f16, int out_type, in
   //   1 x 310, 728 x 936      15.3  10.5  11.3   9.2
   const int64_t busy = gr.rows < gr.n_groups ? gr.rows : gr.n_groups;
   const int64_t each = (gr.rows + busy - 1) / busy;
-  auto cost = [&](int ctas, int nt, int sub) {
+  auto cost = [&](int ctas, int nt, int sub, int parts) {
     const int64_t split = (each + nt - 1) / nt, rows = (each + split - 1) / split;
-    const int units = sms / ctas;
+    const int units = parts == 1 ? sms / ctas : split_units(sms, parts);
     const float x = (float)((rows + 15) / 16 * 16 / ctas * kBK * 2);
     float best = 0.0f;
     const int step = ctas == 1 ? low_step(trans_b) : kBM * ctas * sub;
     for (int h = kBM * ctas * sub; h > 0; h -= step) {
       const int64_t tiles = busy * split * ((N + h - 1) / h), rounds = (tiles + units - 1) / units;
-      const float active = (float)(tiles < units ? tiles : units) * ctas;
+      const float active = (float)(tiles < units ? tiles : units) * (float)(ctas * parts);
       float kb = block_ns((float)(h / ctas * kBK * 2), x, active, (float)split);
       const float issue = ctas == 1 ? kLowBlock : nt == 128 ? 135.0f : sub == 1 ? 210.0f : 270.0f;
       kb = kb > issue ? kb : issue;
       const float mma = 2.0f * (float)(rows * sub) / 1.4f;  // cycles at the clock under load
-      const float main = (float)p.kblocks * (kb > mma ? kb : mma);
+      const float main = (float)((p.kblocks + parts - 1) / parts) * (kb > mma ? kb : mma);
       // the epilogue, beside the next tile's MMAs unless the tile has both
       // accumulators
-      const float out = (sub == 1 && nt >= 128 ? 5.0f : 10.0f) * (float)rows + 500.0f;
+      const float out = (sub == 1 && nt >= 128 ? 5.0f : 10.0f) * (float)rows + 500.0f +
+                        (parts > 1 ? kJoin : 0.0f);
       const float t = sub == 2 ? (float)rounds * (main + out)
                                : (float)rounds * (main > out ? main : out) + out;
       if (best == 0.0f || t < best) best = t;
@@ -1265,13 +1364,15 @@ cudaError_t launch_grouped_matmul(const Groups16& gr, bool f16, int out_type, in
     return best;
   };
   struct Choice {
-    int ctas, nt, sub;
+    int ctas, nt, sub, parts;
   };
-  constexpr Choice all[] = {{2, 256, 2}, {2, 128, 1}, {2, 256, 1}, {1, 32, 1}};
+  constexpr Choice all[] = {{2, 256, 2, 1}, {2, 128, 1, 1}, {2, 256, 1, 1}, {1, 32, 1, 1},
+                            {1, 32, 1, 2},  {1, 32, 1, 4},  {1, 32, 1, 8}};
   int pick = 0;
   float least = 0.0f;
-  for (int i = 0; i < 4; ++i) {
-    const float t = cost(all[i].ctas, all[i].nt, all[i].sub);
+  for (int i = 0; i < 7; ++i) {
+    if (p.kblocks < 4 * all[i].parts && all[i].parts > 1) break;  // two stages a part
+    const float t = cost(all[i].ctas, all[i].nt, all[i].sub, all[i].parts);
     if (i == 0 || t < least) {
       least = t;
       pick = i;
@@ -1279,26 +1380,30 @@ cudaError_t launch_grouped_matmul(const Groups16& gr, bool f16, int out_type, in
   }
   CUtensorMap mw, mx, mx32;
   cudaError_t e = make_tmap_bf16(&mx, a, K, gr.rows, 1, kBK, kBM);
-  if (e == cudaSuccess) e = make_tmap_bf16(&mx32, a, K, gr.rows, 1, kBK, pick == 3 ? 16 : 32);
+  if (e == cudaSuccess) e = make_tmap_bf16(&mx32, a, K, gr.rows, 1, kBK, pick >= 3 ? 16 : 32);
   if (e == cudaSuccess)
-    e = trans_b ? make_tmap_16b_3d(&mw, b, K, N, gr.n_groups, kBK, pick == 3 ? 32 : kBM)
+    e = trans_b ? make_tmap_16b_3d(&mw, b, K, N, gr.n_groups, kBK, pick >= 3 ? 32 : kBM)
                 : make_tmap_16b_3d(&mw, b, N, K, gr.n_groups, 64, kBK);
   if (e != cudaSuccess) return e;
-  auto go = [&](auto ctas, auto nt, auto sub) {
+  auto go = [&](auto ctas, auto nt, auto sub, auto parts) {
     constexpr int kCtas = decltype(ctas)::value, kNT = decltype(nt)::value;
-    constexpr int kSub = decltype(sub)::value;
+    constexpr int kSub = decltype(sub)::value, kSplit = decltype(parts)::value;
     static_assert(MatCfg<kCtas, kNT, kSub>::x_box == (kNT == 32 ? 16 : 32), "boxes of the maps");
     const int64_t row_tiles = gr.rows / kNT + busy;
-    return trans_b ? launch_mat<kForward, kCtas, kNT, kSub>(p, mw, mx, mx32, row_tiles, stream, sms)
-                   : launch_mat<kInputGrad, kCtas, kNT, kSub>(p, mw, mx, mx32, row_tiles, stream, sms);
+    return trans_b ? launch_mat<kForward, kCtas, kNT, kSub, kSplit>(p, mw, mx, mx32, row_tiles, stream, sms)
+                   : launch_mat<kInputGrad, kCtas, kNT, kSub, kSplit>(p, mw, mx, mx32, row_tiles, stream, sms);
   };
   using std::integral_constant;
   constexpr integral_constant<int, 1> one{};
   constexpr integral_constant<int, 2> two{};
-  if (pick == 0) return go(two, integral_constant<int, 256>{}, two);
-  if (pick == 1) return go(two, integral_constant<int, 128>{}, one);
-  if (pick == 2) return go(two, integral_constant<int, 256>{}, one);
-  return go(one, integral_constant<int, 32>{}, one);
+  constexpr integral_constant<int, 32> low{};
+  if (pick == 0) return go(two, integral_constant<int, 256>{}, two, one);
+  if (pick == 1) return go(two, integral_constant<int, 128>{}, one, one);
+  if (pick == 2) return go(two, integral_constant<int, 256>{}, one, one);
+  if (pick == 3) return go(one, low, one, one);
+  if (pick == 4) return go(one, low, one, two);
+  if (pick == 5) return go(one, low, one, integral_constant<int, 4>{});
+  return go(one, low, one, integral_constant<int, 8>{});
 }
 
 cudaError_t launch_grouped_wgrad(const Groups16& gr, bool f16, int out_type, int N, int K,

@@ -329,6 +329,22 @@ def test_matmul_long_groups(capi, trans, N, out):
                  lead=2, tail=3)
 
 
+@pytest.mark.parametrize("trans", [True, False])
+@pytest.mark.parametrize("counts", [[1], [16], [17], [31, 0, 2], [40, 1, 1, 1], [0, 200] + [0] * 30,
+                                    [3] * 20])
+@pytest.mark.parametrize("K,N", [(520, 8), (1032, 264), (4104, 136), (6320, 144), (2056, 3080),
+                                 (8200, 1032)])
+def test_matmul_few_tiles_over_a_long_axis(capi, trans, counts, K, N):
+    """Sums over K split over clusters of 2, 4 and 8 CTAs; few tiles, and with
+    the wider N more than run at a time."""
+    out = FP32 if K == 4104 else None
+    dtype = FP16 if N == 264 else BF16
+    a, b, gr, gs, first = check_matmul(capi, counts, K, N, dtype, out, trans, lead=2, tail=3)
+    again = torch.full_like(first, 7.0)
+    capi.moe_grouped_matmul(a, b, gr, gs, again, trans_b=trans)
+    assert torch.equal(first, again)
+
+
 def test_matmul_each_row_count(capi):
     # every number of rows of a group from 0 to 140, all in one call and alone
     check_matmul(capi, list(range(141)), 72, 136)
