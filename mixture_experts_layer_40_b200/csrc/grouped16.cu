@@ -420,7 +420,9 @@ struct MatCfg {
 // one SM takes in, what all take in from L2 together, and HBM; and the least
 // time of a k-block, ns, that a single-CTA kernel needs from its few KB in flight.
 constexpr float kSmIn = 100.0f, kL2 = 8900.0f, kHbm = 6450.0f, kLowBlock = 225.0f;
-constexpr float kJoin = 1500.0f;  // ns, joining a split sum's parts
+// ns, joining `split` parts of up to 16 rows (measured: 1.6 us for 2, 1.8 for
+// 4, 2.8 for 8)
+inline float join_ns(int split) { return 1500.0f + 250.0f * (float)split; }
 
 // Time of a k-block of which each of `active` SMs takes in w bytes of weights,
 // which `share` tiles need at the same time, and x bytes of rows.
@@ -1328,25 +1330,33 @@ cudaError_t launch_grouped_matmul(const Groups16& gr, bool f16, int out_type, in
   p.idesc = f16 ? 0u : 1u;
   p.status = gr.status;
   // The kernel whose rounds of tiles take the least time, if the groups were
-  // alike: CTAs x rows x accumulators of 2x256x2, 2x128, 2x256 and 1x32. Over 43
-  // shapes the choice was within 3% of the best of the four in the mean. Some
-  // of them (us, K-major weights; groups x rows, N x K):
+  // alike: CTAs x rows x accumulators of 2x256x2, 2x128, 2x256 and 1x32, the
+  // last also with its sums split over 2, 4 or 8 CTAs. Over 43 shapes the
+  // choice was within 3% of the best of the first four in the mean. Some of
+  // them (us, K-major weights; groups x rows, N x K):
   //   32 x 384, 4096 x 4096    322   372   348  1669
   //   16 x 800, 1024 x 1024     31    31    28   102
   //   2 x 821, 920 x 1184     17.4  10.1  11.7  21.2
   //   1 x 1, 4096 x 7168      35.8  20.2  28.8  29.7
   //   8 x 1, 4096 x 7168      75.5  74.3  77.6  73.7
   //   1 x 310, 728 x 936      15.3  10.5  11.3   9.2
+  // and where splitting counts:
+  //   1 x 1, 144 x 6320        31.6  18.6  26.0  26.9  16.8  11.9   9.4
+  //   1 x 1, 4096 x 7168       35.7  20.1  28.9  29.8  18.2  12.3  16.3
+  //   1 x 128, 1024 x 7168     38.2  23.5  32.1  31.5  20.8  15.6  24.9
+  //   1 x 64, 2048 x 2048      14.7   9.7  12.1  13.0  11.7  11.0  20.5
+  //   8 x 1, 7168 x 2048       41.0  41.9  45.9  45.8  47.7  53.1  87.3
   const int64_t busy = gr.rows < gr.n_groups ? gr.rows : gr.n_groups;
   const int64_t each = (gr.rows + busy - 1) / busy;
   auto cost = [&](int ctas, int nt, int sub, int parts) {
     const int64_t split = (each + nt - 1) / nt, rows = (each + split - 1) / split;
     const int units = parts == 1 ? sms / ctas : split_units(sms, parts);
     const float x = (float)((rows + 15) / 16 * 16 / ctas * kBK * 2);
-    float best = 0.0f;
+    float best = 1e30f;
     const int step = ctas == 1 ? low_step(trans_b) : kBM * ctas * sub;
     for (int h = kBM * ctas * sub; h > 0; h -= step) {
       const int64_t tiles = busy * split * ((N + h - 1) / h), rounds = (tiles + units - 1) / units;
+      if (parts > 1 && rounds > 1) break;  // a join in every round costs more than it gives
       const float active = (float)(tiles < units ? tiles : units) * (float)(ctas * parts);
       float kb = block_ns((float)(h / ctas * kBK * 2), x, active, (float)split);
       const float issue = ctas == 1 ? kLowBlock : nt == 128 ? 135.0f : sub == 1 ? 210.0f : 270.0f;
@@ -1356,10 +1366,10 @@ cudaError_t launch_grouped_matmul(const Groups16& gr, bool f16, int out_type, in
       // the epilogue, beside the next tile's MMAs unless the tile has both
       // accumulators
       const float out = (sub == 1 && nt >= 128 ? 5.0f : 10.0f) * (float)rows + 500.0f +
-                        (parts > 1 ? kJoin : 0.0f);
+                        (parts > 1 ? (rows > 16 ? 2.0f : 1.0f) * join_ns(parts) : 0.0f);
       const float t = sub == 2 ? (float)rounds * (main + out)
                                : (float)rounds * (main > out ? main : out) + out;
-      if (best == 0.0f || t < best) best = t;
+      if (t < best) best = t;
     }
     return best;
   };

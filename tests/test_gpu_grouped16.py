@@ -345,6 +345,13 @@ def test_matmul_few_tiles_over_a_long_axis(capi, trans, counts, K, N):
     assert torch.equal(first, again)
 
 
+@pytest.mark.parametrize("trans", [True, False])
+@pytest.mark.parametrize("counts,N", [([33, 1], 896), ([33, 1], 2048), ([1, 0, 65, 0], 896)])
+def test_matmul_split_sums_in_rounds(capi, trans, counts, N):
+    # more row tiles than equal groups would have: clusters take several in turn
+    check_matmul(capi, counts, 8200, N, trans=trans)
+
+
 def test_matmul_each_row_count(capi):
     # every number of rows of a group from 0 to 140, all in one call and alone
     check_matmul(capi, list(range(141)), 72, 136)
