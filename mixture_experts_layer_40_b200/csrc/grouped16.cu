@@ -420,6 +420,7 @@ struct MatCfg {
 // one SM takes in, what all take in from L2 together, and HBM; and the least
 // time of a k-block, ns, that a single-CTA kernel needs from its few KB in flight.
 constexpr float kSmIn = 100.0f, kL2 = 8900.0f, kHbm = 6450.0f, kLowBlock = 225.0f;
+constexpr float kPairBlock = 370.0f;  // the same of a pair's 256 x 256 weight gradient
 // ns, joining `split` parts of up to 16 rows (measured: 1.6 us for 2, 1.8 for
 // 4, 2.8 for 8)
 inline float join_ns(int split) { return 1500.0f + 250.0f * (float)split; }
@@ -949,14 +950,89 @@ __device__ __noinline__ void add16(uint16_t* out, bool f16, const float* v, int 
   }
 }
 
+// Joins a warp's 32 rows (one a lane) x 32 columns of dw at (y, x) with those
+// of the same warp in the cluster's other CTAs, and writes this CTA's share.
+// False where a wait ran out.
+template <int kSplit>
+MOE_DEV bool join_parts(const Args16& p, Shared16& sh, const float (&v)[32], uint32_t buf, int part,
+                        int lane, uint32_t chunk, int g, int y, int x, volatile int* abort) {
+  const uint32_t joined = smem_u32(&sh.joined), freed = smem_u32(&sh.freed);
+  if (!__all_sync(0xffffffffu, mbar_wait_pair<2>(freed, (chunk & 1u) ^ 1u, abort, p.status)))
+    return false;
+#pragma unroll
+  for (int i = 0; i < 8; ++i)
+    asm volatile("st.shared.v4.f32 [%0], {%1, %2, %3, %4};" ::"r"(
+                     buf + (uint32_t)(lane * 128 + ((i ^ (lane & 7)) << 4))),
+                 "f"(v[4 * i]), "f"(v[4 * i + 1]), "f"(v[4 * i + 2]), "f"(v[4 * i + 3])
+                 : "memory");
+  __syncwarp();
+  if (lane < kSplit) mbar_arrive_release(in_cta(joined, lane));
+  if (!__all_sync(0xffffffffu, mbar_wait_pair<2>(joined, chunk & 1u, abort, p.status))) return false;
+#pragma unroll
+  for (int k = 0; k < 8 / kSplit; ++k) {
+    // 4 columns of a row
+    const int i = (part * (8 / kSplit) + k) * 32 + lane, row = i / 8, col = i % 8 * 4;
+    if (y + row >= p.M || x + col >= p.N) continue;
+    float4 s = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+#pragma unroll
+    for (int q = 0; q < kSplit; ++q) {
+      const float4 a =
+          ld_cluster_f4(in_cta(buf + (uint32_t)(row * 128 + (((col / 4) ^ (row & 7)) << 4)), q));
+      s.x += a.x, s.y += a.y, s.z += a.z, s.w += a.w;
+    }
+    const int64_t at = ((int64_t)g * p.M + y + row) * p.N + x + col;
+    if (p.out_type == MOE_FP32) {
+      float4* const dst = reinterpret_cast<float4*>(static_cast<float*>(p.out) + at);
+      if (p.accumulate) {
+        const float4 d = *dst;
+        s.x += d.x, s.y += d.y, s.z += d.z, s.w += d.w;
+      }
+      *dst = s;
+    } else {
+      const bool f16 = p.out_type == MOE_FP16;
+      uint2* const dst = reinterpret_cast<uint2*>(static_cast<uint16_t*>(p.out) + at);
+      if (p.accumulate) {
+        const uint2 d = *dst;
+        if (f16) {
+          const float2 lo = __half22float2(*reinterpret_cast<const __half2*>(&d.x));
+          const float2 hi = __half22float2(*reinterpret_cast<const __half2*>(&d.y));
+          s.x += lo.x, s.y += lo.y, s.z += hi.x, s.w += hi.y;
+        } else {
+          s.x += bf16_lo(d.x), s.y += bf16_hi(d.x), s.z += bf16_lo(d.y), s.w += bf16_hi(d.y);
+        }
+      }
+      *dst = f16 ? make_uint2(pack_f16x2(s.x, s.y), pack_f16x2(s.z, s.w))
+                 : make_uint2(pack_bf16x2(s.x, s.y), pack_bf16x2(s.z, s.w));
+    }
+  }
+  __syncwarp();
+  if (lane < kSplit) mbar_arrive_release(in_cta(freed, lane));
+  return true;
+}
+
 // whether k-block kb of a group ends inside a 16-row step
 MOE_DEV bool to_clear(int rows, int kb) {
   const int live = rows - kb * kBK;
   return live < kBK && (live & 15) != 0;
 }
 
-template <int kCtas, int kBN>
-__global__ void __cluster_dims__(kCtas, 1, 1) __launch_bounds__(kWThreads, 1)
+// this CTA's share of a group's k-blocks: all of them, or where tiles are
+// split one of kSplit shares
+struct Share {
+  int begin, end;
+};
+template <int kSplit>
+MOE_DEV Share share_of(int blocks, int part) {
+  return kSplit == 1 ? Share{0, blocks}
+                     : Share{part * blocks / kSplit, (part + 1) * blocks / kSplit};
+}
+
+// kSplit (single CTAs): a tile's rows are split over a cluster of that many
+// CTAs, for few tiles over long groups: each sums its share, leaves the fp32
+// part in shared memory, and adds its share of the tile up from all parts, in
+// the order of the ranks.
+template <int kCtas, int kBN, int kSplit>
+__global__ void __cluster_dims__(kCtas * kSplit, 1, 1) __launch_bounds__(kWThreads, 1)
     grouped_wgrad_kernel(const __grid_constant__ CUtensorMap tm_a,
                          const __grid_constant__ CUtensorMap tm_b,
                          const __grid_constant__ CUtensorMap tm_a16,
@@ -970,7 +1046,9 @@ __global__ void __cluster_dims__(kCtas, 1, 1) __launch_bounds__(kWThreads, 1)
   const uint32_t ring = (smem_u32(dyn_smem) + 1023u) & ~1023u;
   const int warp = threadIdx.x >> 5;
   const int lane = threadIdx.x & 31;
+  static_assert(kCtas == 1 || kSplit == 1, "single CTAs are split");
   const int rank = kCtas == 1 ? 0 : (int)cluster_rank();
+  const int part = kSplit == 1 ? 0 : (int)cluster_rank();
 
   if (threadIdx.x == 0) {
     for (int s = 0; s < C::stages; ++s) {
@@ -984,6 +1062,10 @@ __global__ void __cluster_dims__(kCtas, 1, 1) __launch_bounds__(kWThreads, 1)
       mbar_init(smem_u32(&sh.tempty[b]), 8 * kCtas);
     }
     mbar_init(smem_u32(&sh.drained), 1);
+    if (kSplit > 1) {
+      mbar_init(smem_u32(&sh.joined), 8 * kSplit);
+      mbar_init(smem_u32(&sh.freed), 8 * kSplit);
+    }
     sh.abort = 0;
     fence_mbar_init();
     prefetch_tensormap(&tm_a);
@@ -997,12 +1079,12 @@ __global__ void __cluster_dims__(kCtas, 1, 1) __launch_bounds__(kWThreads, 1)
     scan_groups(p, sh, lane, 0);
   }
   tc_fence_before();
-  if constexpr (kCtas == 2) cluster_sync();
+  if constexpr (kCtas * kSplit > 1) cluster_sync();
   else __syncthreads();
   tc_fence_after();
 
   const uint32_t tmem_base = sh.tmem_base;
-  const int team = blockIdx.x / kCtas, teams = gridDim.x / kCtas;
+  const int team = blockIdx.x / (kCtas * kSplit), teams = gridDim.x / (kCtas * kSplit);
   const uint32_t total = (uint32_t)sh.prefix[p.n_groups] * (uint32_t)p.n_tiles;  // checked by the host
   volatile int* abort = &sh.abort;
 
@@ -1021,8 +1103,9 @@ __global__ void __cluster_dims__(kCtas, 1, 1) __launch_bounds__(kWThreads, 1)
         const int rows = uniform(sh.rows[t.g]);
         const int kb_n = (rows + kBK - 1) / kBK;
         const int a0 = (t.m * kCtas + rank) * kBM, b0 = t.n * kBN + rank * kHalf;
-        int r = uniform(sh.start[t.g]);
-        for (int kb = 0; kb < kb_n; ++kb, ++it, at.next(), r += kBK) {
+        const Share of = share_of<kSplit>(kb_n, part);
+        int r = uniform(sh.start[t.g]) + of.begin * kBK;
+        for (int kb = of.begin; kb < of.end; ++kb, ++it, at.next(), r += kBK) {
           if (!warp_wait(at.empty, at.phase ^ 1u, abort, p.status)) {
             ok = false;
             break;
@@ -1083,8 +1166,9 @@ __global__ void __cluster_dims__(kCtas, 1, 1) __launch_bounds__(kWThreads, 1)
       const TileAt t = tile_at(tile, sh.prefix, p.n_groups, p.n_tiles);
       const int rows = sh.rows[t.g];
       const int kb_n = (rows + kBK - 1) / kBK;
-      it += kb_n;
-      if (kb_n == 0 || !to_clear(rows, kb_n - 1)) continue;
+      const Share of = share_of<kSplit>(kb_n, part);
+      it += of.end - of.begin;
+      if (of.begin == of.end || of.end < kb_n || !to_clear(rows, kb_n - 1)) continue;
       const int s = (it - 1) % C::stages;
       if (!__all_sync(0xffffffffu, mbar_wait(smem_u32(&sh.part[s]), (part_phase >> s) & 1u, abort,
                                              p.status)))
@@ -1122,8 +1206,9 @@ __global__ void __cluster_dims__(kCtas, 1, 1) __launch_bounds__(kWThreads, 1)
         const TileAt t = tile_at(tile, sh.prefix, p.n_groups, p.n_tiles);
         const int rows = uniform(sh.rows[t.g]);
         const int kb_n = (rows + kBK - 1) / kBK;
+        const Share of = share_of<kSplit>(kb_n, part);
         int in_segment = 0;
-        for (int kb = 0; kb < kb_n; ++kb, ++it, at.next()) {
+        for (int kb = of.begin; kb < of.end; ++kb, ++it, at.next()) {
           const int buf = used & 1;
           if (in_segment == 0) {
             ok = warp_wait(smem_u32(&sh.tempty[buf]), ((uint32_t)(used >> 1) & 1u) ^ 1u, abort,
@@ -1133,9 +1218,9 @@ __global__ void __cluster_dims__(kCtas, 1, 1) __launch_bounds__(kWThreads, 1)
           }
           const uint32_t d = tmem_base + (uint32_t)(buf * kBN);
           ok = warp_wait(at.full, at.phase, abort, p.status);
-          const bool last = kb == kb_n - 1;
+          const bool last = kb == of.end - 1;
           int steps = kBK / 16;
-          if (ok && last) {
+          if (ok && kb == kb_n - 1) {
             steps = (rows - kb * kBK + 15) / 16;
             if (to_clear(rows, kb)) {
               ok = __all_sync(0xffffffffu,
@@ -1176,12 +1261,14 @@ __global__ void __cluster_dims__(kCtas, 1, 1) __launch_bounds__(kWThreads, 1)
     DwOut out{&tm_out, ring + (uint32_t)(C::stages * C::stage_bytes + ew * C::buf_bytes)};
     const bool direct = p.accumulate && p.out_type != MOE_FP32;
     int used = 0;
+    uint32_t chunks = 0;  // of split tiles
     bool ok = true;
     for (uint32_t tile = team; ok && tile < total; tile += teams) {
       const TileAt t = tile_at(tile, sh.prefix, p.n_groups, p.n_tiles);
       const int kb_n = (sh.rows[t.g] + kBK - 1) / kBK;
       if (kb_n == 0 && p.accumulate) continue;
-      const int segments = (kb_n + kSegment - 1) / kSegment;
+      const Share of = share_of<kSplit>(kb_n, part);
+      const int segments = (of.end - of.begin + kSegment - 1) / kSegment;
       const int y = (t.m * kCtas + rank) * kBM + quarter * 32, x0 = t.n * kBN + c0;
       auto emit = [&](const float (&v)[32], int c) {
         const int x = x0 + c;
@@ -1215,7 +1302,7 @@ __global__ void __cluster_dims__(kCtas, 1, 1) __launch_bounds__(kWThreads, 1)
         }
         ++used;
       };
-      if (segments <= 1) {
+      if (kSplit == 1 && segments <= 1) {
         if (segments == 1 && !wait_segment()) break;
 #pragma unroll 1
         for (int c = 0; c < kEpiCols; c += 32) {
@@ -1249,15 +1336,24 @@ __global__ void __cluster_dims__(kCtas, 1, 1) __launch_bounds__(kWThreads, 1)
           release_segment();
         }
         if (!ok) break;
+        if constexpr (kSplit == 1) {
 #pragma unroll
-        for (int c = 0; c < kEpiCols / 32; ++c) emit(sum[c], 32 * c);
+          for (int c = 0; c < kEpiCols / 32; ++c) emit(sum[c], 32 * c);
+        } else {
+#pragma unroll
+          for (int c = 0; c < kEpiCols / 32; ++c) {
+            ok = join_parts<kSplit>(p, sh, sum[c], out.buf, part, lane, chunks++, t.g, y,
+                                    x0 + 32 * c, abort);
+            if (!ok) break;
+          }
+        }
       }
     }
     if (lane == 0) bulk_wait_all();
   }
 
   tc_fence_before();
-  if constexpr (kCtas == 2) cluster_sync();
+  if constexpr (kCtas * kSplit > 1) cluster_sync();
   else __syncthreads();
   tc_fence_after();
   if (warp == 2) dealloc16<kCtas>(tmem_base, 2 * kBN);
@@ -1286,7 +1382,7 @@ cudaError_t launch_mat(Args16 a, const CUtensorMap& mw, const CUtensorMap& mx,
   return cudaGetLastError();
 }
 
-template <int kCtas, int kBN>
+template <int kCtas, int kBN, int kSplit>
 cudaError_t launch_wg(Args16 a, const CUtensorMap& ma, const CUtensorMap& mb,
                       const CUtensorMap& ma16, const CUtensorMap& mb16, const CUtensorMap& mo,
                       cudaStream_t stream, int sms) {
@@ -1295,10 +1391,10 @@ cudaError_t launch_wg(Args16 a, const CUtensorMap& ma, const CUtensorMap& mb,
   cudaError_t e = once.run([] {
     // the register split is only safe if the kernel was built for it
     cudaFuncAttributes fa;
-    cudaError_t r = cudaFuncGetAttributes(&fa, grouped_wgrad_kernel<kCtas, kBN>);
+    cudaError_t r = cudaFuncGetAttributes(&fa, grouped_wgrad_kernel<kCtas, kBN, kSplit>);
     if (r != cudaSuccess) return r;
     if (fa.numRegs != kWRegsLaunch) return cudaErrorInvalidConfiguration;
-    return cudaFuncSetAttribute(grouped_wgrad_kernel<kCtas, kBN>,
+    return cudaFuncSetAttribute(grouped_wgrad_kernel<kCtas, kBN, kSplit>,
                                 cudaFuncAttributeMaxDynamicSharedMemorySize, (int)C::dyn_smem);
   });
   if (e != cudaSuccess) return e;
@@ -1307,8 +1403,9 @@ cudaError_t launch_wg(Args16 a, const CUtensorMap& ma, const CUtensorMap& mb,
   a.idesc = make_idesc(kBM * kCtas, kBN, a.idesc, a.idesc) | 1u << 15 | 1u << 16;
   const int64_t tiles = (int64_t)a.n_groups * a.m_tiles * a.n_tiles;
   if (tiles >= (1ll << 31)) return cudaErrorInvalidValue;
-  const int64_t grid = tiles * kCtas < sms ? tiles * kCtas : sms / kCtas * kCtas;
-  grouped_wgrad_kernel<kCtas, kBN><<<(unsigned)grid, kWThreads, C::dyn_smem, stream>>>(ma, mb, ma16, mb16, mo, a);
+  const int64_t units = kSplit == 1 ? sms / kCtas : split_units(sms, kSplit);
+  const int64_t grid = (tiles < units ? tiles : units) * kCtas * kSplit;
+  grouped_wgrad_kernel<kCtas, kBN, kSplit><<<(unsigned)grid, kWThreads, C::dyn_smem, stream>>>(ma, mb, ma16, mb16, mo, a);
   return cudaGetLastError();
 }
 
@@ -1441,21 +1538,47 @@ cudaError_t launch_grouped_wgrad(const Groups16& gr, bool f16, int out_type, int
     e = out_type == MOE_FP32 ? make_tmap_f32_3d(&mo, dw, K, N, gr.n_groups, 32, 32)
                              : make_tmap_16b_3d(&mo, dw, K, N, gr.n_groups, 64, 32);
   if (e != cudaSuccess) return e;
-  // Pairs of CTAs on 256 x 256 of dw, or single ones on 128 x 128, by the time
-  // of their rounds: either takes in 32 KB a k-block and SM, but the pair's
-  // covers four times as much for two SMs; dw goes out at the SM's share of
-  // HBM while the next tile's blocks come in.
-  const float blocks = (float)((gr.rows / gr.n_groups + kBK - 1) / kBK);
-  auto cost = [&](int side, int units, int bytes) {
+  // Pairs of CTAs on 256 x 256 of dw, or single ones on 128 x 128, also with
+  // the rows split over clusters of 2, 4 or 8, by the time of their rounds:
+  // each SM takes in 32 KB a k-block, but the pair's covers four times as much
+  // for two SMs; dw goes out at the SM's share of HBM while the next tile's
+  // blocks come in. Splitting is for tiles that all run at once (us, fp32 dw;
+  // groups x rows, N x K; unsplit and split):
+  //   1 x 20000, 512 x 512     93.5  33.8     4 x 3000, 1360 x 112    19.7  17.0
+  //   1 x 20000, 256 x 256     93.1  22.0     1 x 4000, 1024 x 1024   23.7  19.0
+  //   1 x 1294, 504 x 160      12.1  11.2     1 x 2000, 4096 x 128    15.0  12.7
+  const int es = out_type == MOE_FP32 ? 4 : 2;
+  const int64_t blocks = (gr.rows / gr.n_groups + kBK - 1) / kBK;
+  auto cost = [&](int side, int ctas, int split) {
+    const int units = split == 1 ? sms / ctas : split_units(sms, split);
     const int64_t tiles = (int64_t)gr.n_groups * ((N + side - 1) / side) * ((K + side - 1) / side);
     const int64_t rounds = (tiles + units - 1) / units;
-    const float in = blocks * 32768.0f * 148.0f / kL2, out = (float)bytes / (kHbm / 148.0f);
-    return (float)rounds * (in > out ? in : out) + out;
+    if (split > 1 && (rounds > 1 || blocks < 2 * split)) return 1e30f;
+    const float active = (float)((tiles < units ? tiles : units) * ctas * split);
+    float kb = block_ns(0.0f, 32768.0f, active, 1.0f);
+    if (ctas == 2 && kb < kPairBlock) kb = kPairBlock;
+    const float in = (float)((blocks + split - 1) / split) * kb;
+    const float out = (float)(side * side / ctas * es) / (kHbm / 148.0f);
+    return (float)rounds * (in > out ? in : out) + (split > 1 ? 2.0f * join_ns(split) : out);
   };
-  const int es = out_type == MOE_FP32 ? 4 : 2;
-  if (N > kBM && cost(256, sms / 2, 128 * 256 * es) < cost(128, sms, 128 * 128 * es))
-    return launch_wg<2, 256>(p, ma, mb, ma16, mb16, mo, stream, sms);
-  return launch_wg<1, 128>(p, ma, mb, ma16, mb16, mo, stream, sms);
+  struct Choice {
+    int side, ctas, split;
+  };
+  constexpr Choice all[] = {{128, 1, 1}, {128, 1, 2}, {128, 1, 4}, {128, 1, 8}, {256, 2, 1}};
+  int pick = 0;
+  float least = 1e30f;
+  for (int i = 0; i < (N > kBM ? 5 : 4); ++i) {
+    const float t = cost(all[i].side, all[i].ctas, all[i].split);
+    if (t < least) {
+      least = t;
+      pick = i;
+    }
+  }
+  if (pick == 0) return launch_wg<1, 128, 1>(p, ma, mb, ma16, mb16, mo, stream, sms);
+  if (pick == 1) return launch_wg<1, 128, 2>(p, ma, mb, ma16, mb16, mo, stream, sms);
+  if (pick == 2) return launch_wg<1, 128, 4>(p, ma, mb, ma16, mb16, mo, stream, sms);
+  if (pick == 3) return launch_wg<1, 128, 8>(p, ma, mb, ma16, mb16, mo, stream, sms);
+  return launch_wg<2, 256, 1>(p, ma, mb, ma16, mb16, mo, stream, sms);
 }
 
 }  // namespace moe

@@ -375,6 +375,26 @@ def test_wgrad_long_groups_keep_fp32(capi):
             assert float((dw[g] - ref).norm() / ref.norm()) < 2.0 ** -20
 
 
+@pytest.mark.parametrize("counts", [[300], [520, 1, 0, 33], [4000], [4013, 2, 0], [0, 3500, 70],
+                                    [64 * 70]])
+@pytest.mark.parametrize("N,K", [(8, 8), (136, 264), (512, 512), (72, 1032), (1360, 112)])
+@pytest.mark.parametrize("out,accumulate", [(FP32, False), (FP32, True), (BF16, False), (BF16, True)])
+def test_wgrad_few_tiles_over_long_groups(capi, counts, N, K, out, accumulate):
+    """Rows split over clusters of 2, 4 and 8 CTAs, some of which have no
+    share of a short group."""
+    dy, x, gr, gs, dw = check_wgrad(capi, counts, N, K, out_dtype=out, lead=2, tail=3,
+                                    accumulate=accumulate)
+    if not accumulate:
+        again = torch.full_like(dw, 7.0)
+        capi.moe_grouped_wgrad(dy, x, gr, gs, again)
+        assert torch.equal(dw, again)
+
+
+def test_wgrad_split_tiles_in_fp16(capi):
+    check_wgrad(capi, [2500, 7], 264, 136, FP16, FP16, accumulate=True)
+    check_wgrad(capi, [2500, 7], 264, 136, FP16, FP16)
+
+
 def test_calls_on_several_streams_at_once(capi):
     """Each of the kernels beside itself and the others, on streams of their
     own: the same bits as one call after another."""
