@@ -38,6 +38,9 @@
 //   warp 3     weight gradient: clears rows behind a group (below)
 //   warps 4-   epilogue: TMEM -> registers -> shared memory -> global memory,
 //              while the next tile's MMAs fill the other buffer
+// Single-CTA kernels also come with a tile's reduction split over a cluster of
+// 2, 4 or 8 CTAs: a tile by itself is bound by what one SM takes in (100 bytes
+// a ns) or by the time of a small k-block (225 ns), however idle the others.
 // Rows of a tile beyond its group are another group's rows or padding: each
 // column of out^T depends on its own row alone, so whatever they hold stays
 // in accumulator columns that are never stored. In the weight gradient the
@@ -441,9 +444,10 @@ __host__ __device__ inline float low_block_ns(int h, int x_rows, int64_t tiles, 
 // heights that the loads come in: boxes of 32 weight rows, or of 64 columns
 __host__ __device__ constexpr int low_step(bool k_major) { return k_major ? 32 : 64; }
 // clusters of `split` CTAs that run at a time: those of 4 and 8 do not fill
-// every GPC (33 and 15 of 148 SMs' 37 and 18)
+// every GPC (the occupancy query gives 33 and 15 on 148 SMs)
 inline int split_units(int sms, int split) {
-  return split <= 2 ? sms / split : sms * (split == 4 ? 33 : 15) / 148;
+  const int units = split <= 2 ? sms / split : sms * (split == 4 ? 33 : 15) / 148;
+  return units > 0 ? units : 1;
 }
 static_assert(16 * (32 * 4 + 16) <= 32 * (32 * 2 + 16), "fp32 rows in the turn buffer");
 
