@@ -27,8 +27,8 @@
 // Bound by HBM where groups are short (the weights, once): 8 rows of 64 groups
 // at 4096 x 7168 take 77 us (floor 69), 1024 rows at 7168 x 2048 take 295
 // (294). Long groups are bound by the tensor cores at the clock that the power
-// limit leaves: 32768 rows of 32 groups at 4096 x 7168 take 1468 to 1637 us,
-// 1.18 to 1.31 PFLOP/s.
+// limit leaves: 32768 rows of 32 groups at 4096 x 7168 take 1468 to 1730 us,
+// 1.11 to 1.31 PFLOP/s.
 //
 // One persistent CTA per SM:
 //   warp 0     TMA producer: 64-deep k-blocks into a ring of stages
@@ -832,7 +832,7 @@ __global__ void __cluster_dims__(kCtas * kSplit, 1, 1)
 // rows and added up in registers, rounded to nearest (one group of 512, 2048,
 // 8192, 65536 rows: off by 4.7e-7, 4.8e-7, 4.8e-7, 5.2e-7 of the result).
 //
-// Measured: 32 groups of 16384 rows in all, dw 7168 x 2048 in fp32, take 625
+// Measured: 32 groups of 16384 rows in all, dw 7168 x 2048 in fp32, take 617
 // to 889 us (floor 338). 3.8 GB of operand tiles come from L2 and 1.9 GB of dw
 // go through it, which is what bounds it.
 constexpr int kSegment = 8;  // k-blocks per TMEM sum
