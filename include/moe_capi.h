@@ -426,7 +426,8 @@ typedef enum { MOE_BF16 = 0, MOE_FP16 = 1, MOE_FP32 = 2 } moe_type;
  *
  * type: MOE_BF16 or MOE_FP16 (a and b, or dy and x, alike); out_type: the
  * same, or MOE_FP32. Sums are fp32, rounded once to out_type; their order is
- * fixed, so results are reproducible. An infinity or NaN stays in the output
+ * fixed by the sizes (and the GPU's SMs), not by timing: the same call gives
+ * the same bits. An infinity or NaN stays in the output
  * rows (for the weight gradient: in the group) it belongs to. N and K are
  * multiples of 8 up to 2^20; pointers 16-byte aligned; rows < 2^31 - 256
  * (rows = 0: the row buffers may be NULL). out and dw must not overlap the
