@@ -7,7 +7,8 @@
 //   input gradient out[r, n] = sum_k a[r, k] W_g[k, n]     W [G, K, N]
 //   weight grad    dw_g[n, k] (+)= sum_{r in g} dy[r, n] x[r, k]
 //
-// 16-bit products are exact in fp32; sums are fp32 in TMEM, rounded once.
+// 16-bit products are exact in fp32; sums are fp32 in TMEM, in segments where
+// they are long (below), rounded once.
 //
 // The tensor cores take either operand with its reduction index fastest
 // (K-major) or slowest (MN-major), so all three products read the tensors as
@@ -68,6 +69,7 @@ struct Args16 {
   const int32_t* group_start;
   int32_t n_groups;
   int32_t kblocks;   // matmul: ceil(K / 64)
+  int32_t segment;   // matmul: k-blocks of one TMEM sum, at most
   int32_t n_tiles;   // weight gradient: column tiles of dw per group
   int32_t m_tiles;   // weight gradient: row tiles of dw per group
   int64_t rows;      // rows of the row buffers
@@ -416,8 +418,21 @@ struct MatCfg {
   static constexpr bool low = kCtas == 1 && kSub == 1;
   // split sums: rows of a part that lie in the turn buffers at a time, fp32
   static constexpr int part_rows = 16;
+  // whether a tile's sum may be taken in segments, which the epilogue adds up
+  // in registers: at most 64 a thread, beside the 32 of a load
+  static constexpr bool cuts = kSub == 1 && kNT <= 128;
   static_assert(!low || part_rows * kBM * 4 <= 4 * groups * turn_bytes, "a part's rows");
 };
+
+// The tensor core's fp32 sums round towards zero at every step of 16 products:
+// 2^-24 of the sum a step where all products are positive, always downwards
+// (448 steps 2.7e-5, 4096 3.5e-4). So one TMEM sum runs only as far as that
+// stays under a sixteenth of half a step of the output's type, and the segments
+// are added up in registers, rounded to nearest: 8192 products for fp16, 65536
+// for bf16, and for fp32 outputs the 512 of the weight gradient.
+inline int segment_blocks(int out_type) {
+  return out_type == MOE_FP32 ? 8 : out_type == MOE_FP16 ? 128 : 1024;
+}
 
 // Rates for choosing tiles, in bytes per ns, measured with these kernels: what
 // one SM takes in, what all take in from L2 together, and HBM; and the least
@@ -542,6 +557,7 @@ __global__ void __cluster_dims__(kCtas * kSplit, 1, 1)
   volatile int* abort = &sh.abort;
   const int kb_all = (p.kblocks + C::depth - 1) / C::depth;  // (at least kSplit: the host)
   const int kb_0 = part * kb_all / kSplit, kb_n = (part + 1) * kb_all / kSplit - kb_0;
+  const int cut = C::cuts ? p.segment / C::depth : kb_n;  // stages of one TMEM sum
 
   if (warp == 0) {
     {
@@ -623,22 +639,24 @@ __global__ void __cluster_dims__(kCtas * kSplit, 1, 1)
       const uint64_t desc_w = kWay == kForward ? smem_desc_sw128(ring) : smem_desc_mn_sw128(ring);
       const uint64_t desc_x = smem_desc_sw128(ring + C::a_bytes);
       constexpr uint64_t step_w = kWay == kForward ? kStepK : kStepMN;
-      for (uint32_t tile = team; ok && tile < total; tile += teams, ++used) {
+      for (uint32_t tile = team; ok && tile < total; tile += teams) {
         const TileAt t = tile_at(tile, sh.prefix, p.n_groups, n_tiles);
         const RowTile rt = row_tile<kNT>(sh.start[t.g], sh.rows[t.g], t.m);
         const uint32_t idesc = p.idesc | ((uint32_t)(rt.cols >> 3) << 17);
-        // accumulators in use: tile by tile in turn, or both by each tile
-        const int buf = kSub == 1 ? used & 1 : 0;
-        const uint32_t free_phase = ((uint32_t)(kSub == 1 ? used >> 1 : used) & 1u) ^ 1u;
-        const uint32_t d0 = tmem_base + (uint32_t)(buf * kNT);
+        int in_sum = 0;  // stages in this TMEM sum
         for (int kb = 0; kb < kb_n; ++kb, ++it, at.next()) {
+          // accumulators in use: sum by sum in turn, or both by each tile
+          const int buf = kSub == 1 ? used & 1 : 0;
+          const uint32_t free_phase = ((uint32_t)(kSub == 1 ? used >> 1 : used) & 1u) ^ 1u;
+          const uint32_t d0 = tmem_base + (uint32_t)(buf * kNT);
+          const bool last = kb == kb_n - 1 || in_sum == cut - 1;
           ok = warp_wait(at.full, at.phase, abort, p.status);
           if (!ok) break;
           tc_fence_after();
           const uint64_t off = at.offset >> 4;
 #pragma unroll
           for (int u = 0; u < kSub; ++u) {
-            if (kb == 0) {
+            if (in_sum == 0) {
               ok = warp_wait(smem_u32(&sh.tempty[buf + u]), free_phase, abort, p.status);
               if (!ok) break;
               tc_fence_after();
@@ -651,12 +669,14 @@ __global__ void __cluster_dims__(kCtas * kSplit, 1, 1)
 #pragma unroll
               for (int i = 0; i < kBK / 16; ++i)
                 mma16<kCtas>(d0 + (uint32_t)(u * kNT), dw + step_w * i, dx + kStepK * i, idesc,
-                             j + i > 0 ? 1u : (uint32_t)kb);
+                             j + i > 0 ? 1u : (uint32_t)in_sum);
             }
-            if (kb == kb_n - 1) commit16<kCtas>(smem_u32(&sh.tfull[buf + u]));
+            if (last) commit16<kCtas>(smem_u32(&sh.tfull[buf + u]));
           }
           if (!ok) break;
           if (elected) commit16<kCtas>(at.empty);
+          if (last) ++used;
+          in_sum = last ? 0 : in_sum + 1;
         }
       }
       if (!ok && it > 0) {
@@ -682,14 +702,20 @@ __global__ void __cluster_dims__(kCtas * kSplit, 1, 1)
     const int piece = lane % per_row, row0 = lane / per_row, row_step = 32 / per_row;
     int used = 0;
     uint32_t chunks = 0;  // of split sums
-    for (uint32_t tile = team; tile < total; tile += teams, ++used) {
+    for (uint32_t tile = team; tile < total; tile += teams) {
       const TileAt t = tile_at(tile, sh.prefix, p.n_groups, n_tiles);
       const RowTile rt = row_tile<kNT>(sh.start[t.g], sh.rows[t.g], t.m);
-      const int buf = kSub == 1 ? used & 1 : sub;
-      const uint32_t full_phase = (uint32_t)(kSub == 1 ? used >> 1 : used) & 1u;
-      if (!__all_sync(0xffffffffu, mbar_wait(smem_u32(&sh.tfull[buf]), full_phase, abort, p.status)))
-        break;
-      tc_fence_after();
+      // the next TMEM sum is in accumulator buf
+      int buf = 0;
+      auto wait_sum = [&] {
+        buf = kSub == 1 ? used & 1 : sub;
+        const uint32_t full_phase = (uint32_t)(kSub == 1 ? used >> 1 : used) & 1u;
+        ++used;
+        const bool full = __all_sync(
+            0xffffffffu, mbar_wait(smem_u32(&sh.tfull[buf]), full_phase, abort, p.status));
+        if (full) tc_fence_after();
+        return full;
+      };
       // this tile's output columns end where the next tile's begin
       const int n0 = t.n * height + (sub * kCtas + rank) * kBM + quarter * 32;
       const int n_end = min(t.n * height + height, p.N);
@@ -725,14 +751,33 @@ __global__ void __cluster_dims__(kCtas * kSplit, 1, 1)
           else mbar_arrive(smem_u32(&sh.tempty[buf]));
         }
       };
+      // 32 rows of the sum in accumulator buf, from row c on
+      auto load_sum = [&](int c, float (&v)[32]) {
+        tmem_ld32(lane_addr + (uint32_t)(buf * kNT + c), v);
+        tmem_wait_ld();
+      };
+      // the same added to v
+      auto add_sum = [&](int c, float (&v)[32]) {
+        float more[32];
+        load_sum(c, more);
+#pragma unroll
+        for (int j = 0; j < 32; ++j) v[j] += more[j];
+      };
+      if (!wait_sum()) break;
       if constexpr (kSplit > 1) {
         float v[32];
-        tmem_ld32(lane_addr + (uint32_t)(buf * kNT), v);
-        tmem_wait_ld();
+        load_sum(0, v);
         release();
+        bool ok = true;
+        for (int done = cut; done < kb_n; done += cut) {
+          ok = wait_sum();
+          if (!ok) break;
+          add_sum(0, v);
+          release();
+        }
+        if (!ok) break;
         const uint32_t joined = smem_u32(&sh.joined), freed = smem_u32(&sh.freed);
         const uint32_t parts = ring + (uint32_t)(C::stages * C::stage_bytes);
-        bool ok = true;
 #pragma unroll
         for (int c = 0; c < kNT; c += C::part_rows) {
           if (c >= rt.live) break;
@@ -783,13 +828,9 @@ __global__ void __cluster_dims__(kCtas * kSplit, 1, 1)
         if (!ok) break;
         continue;
       }
-      if (first >= rt.live) release();  // nothing for this group
-      for (int c = first; c < rt.live; c += 32 * kShare) {
-        float v[32];
-        tmem_ld32(lane_addr + (uint32_t)(buf * kNT + c), v);
-        tmem_wait_ld();
-        if (c + 32 * kShare >= rt.live) release();
-        if (n0 >= n_end) continue;
+      // 32 rows from c on to global memory, by way of the turn buffer
+      auto put = [&](int c, const float (&v)[32]) {
+        if (n0 >= n_end) return;
         if (wide) {
 #pragma unroll
           for (int h = 0; h < 2; ++h) {
@@ -813,6 +854,37 @@ __global__ void __cluster_dims__(kCtas * kSplit, 1, 1)
           }
           copy_out(c);
         }
+      };
+      if (C::cuts && cut < kb_n) {
+        constexpr int kPieces = kNT / (32 * kShare);
+        float sum[kPieces][32];
+        bool ok = true;
+        for (int done = 0;;) {
+#pragma unroll
+          for (int i = 0; i < kPieces; ++i) {
+            const int c = first + 32 * kShare * i;
+            if (c >= rt.live) continue;
+            if (done == 0) load_sum(c, sum[i]);
+            else add_sum(c, sum[i]);
+          }
+          release();
+          done += cut;
+          if (done >= kb_n) break;
+          ok = wait_sum();
+          if (!ok) break;
+        }
+        if (!ok) break;
+#pragma unroll
+        for (int i = 0; i < kPieces; ++i)
+          if (first + 32 * kShare * i < rt.live) put(first + 32 * kShare * i, sum[i]);
+        continue;
+      }
+      if (first >= rt.live) release();  // nothing for this group
+      for (int c = first; c < rt.live; c += 32 * kShare) {
+        float v[32];
+        load_sum(c, v);
+        if (c + 32 * kShare >= rt.live) release();
+        put(c, v);
       }
     }
   }
@@ -1426,6 +1498,7 @@ cudaError_t launch_grouped_matmul(const Groups16& gr, bool f16, int out_type, in
   p.n_groups = gr.n_groups;
   p.rows = gr.rows;
   p.kblocks = (K + kBK - 1) / kBK;
+  p.segment = segment_blocks(out_type);
   p.N = N;
   p.out = out;
   p.out_type = out_type;
@@ -1480,12 +1553,14 @@ cudaError_t launch_grouped_matmul(const Groups16& gr, bool f16, int out_type, in
   };
   constexpr Choice all[] = {{2, 256, 2, 1}, {2, 128, 1, 1}, {2, 256, 1, 1}, {1, 32, 1, 1},
                             {1, 32, 1, 2},  {1, 32, 1, 4},  {1, 32, 1, 8}};
-  int pick = 0;
-  float least = 0.0f;
+  int pick = 1;
+  float least = 1e30f;
   for (int i = 0; i < 7; ++i) {
     if (p.kblocks < 4 * all[i].parts && all[i].parts > 1) break;  // two stages a part
+    // sums in segments take registers that tiles of 256 rows do not leave
+    if (p.kblocks > p.segment && all[i].nt > 128) continue;
     const float t = cost(all[i].ctas, all[i].nt, all[i].sub, all[i].parts);
-    if (i == 0 || t < least) {
+    if (t < least) {
       least = t;
       pick = i;
     }

@@ -430,3 +430,50 @@ def test_calls_on_several_streams_at_once(capi):
     torch.cuda.synchronize()
     for a, b in zip(alone, beside):
         assert all(torch.equal(p, q) for p, q in zip(a, b))
+
+
+def offset_and_error(capi, counts, K, N, dtype, out_dtype, trans, positive):
+    """(mean relative offset, error in the norm) of the product against float64."""
+    gen = torch.Generator(device="cuda").manual_seed(K + N)
+    gr, gs, starts, rows = layout(counts)
+    a, b = randn(gen, rows, K, dtype=dtype), randn(gen, len(counts), N, K, dtype=dtype)
+    if positive:
+        a, b = a.abs_(), b.abs_()
+    b.mul_(K ** -0.5)
+    out = torch.zeros(rows, N, dtype=out_dtype, device="cuda")
+    capi.moe_grouped_matmul(a, b if trans else b.transpose(1, 2).contiguous(), gr, gs, out, trans)
+    err = size = offset = 0.0
+    for g, (s, c) in enumerate(zip(starts, counts)):
+        ref = a[s:s + c].double() @ b[g].double().T
+        d = out[s:s + c].double() - ref
+        err, size = err + float(d.square().sum()), size + float(ref.square().sum())
+        offset += float((d / ref).sum())
+    return offset / out.numel(), (err / size) ** 0.5
+
+
+@pytest.mark.parametrize("trans", [True, False])
+@pytest.mark.parametrize("positive", [False, True])
+@pytest.mark.parametrize("counts,K,N", [([1], 8192, 264), ([1, 3], 65608, 136), ([40, 17], 8200, 1032),
+                                        ([300], 7168, 520), ([1000, 700], 8192, 1032),
+                                        ([257, 0, 130], 65600, 264)])
+def test_matmul_long_sums_keep_fp32(capi, counts, K, N, positive, trans):
+    """Sums over a long K with an fp32 output. A TMEM sum takes 512 products in
+    32 steps, each of which truncates by under 2^-23 of the running sum, half of
+    that on the average, and the running sum is half of the whole on the average:
+    32 x 2^-25 = 2^-20 of the segment; the segments' K / 512 <= 129 additions,
+    rounded to nearest, add at most 2^-20 where they go like a random walk.
+    2^-19 of the result's norm is allowed, however long K is."""
+    assert offset_and_error(capi, counts, K, N, BF16, FP32, trans, positive)[1] < 2.0 ** -19
+
+
+@pytest.mark.parametrize("counts,N", [([1], 136), ([40], 264), ([200, 130], 520)])
+@pytest.mark.parametrize("dtype,K", [(FP16, 65544), (BF16, 262144)])
+def test_matmul_long_sums_have_no_offset(capi, counts, N, dtype, K):
+    """All products positive, 16-bit outputs: truncated sums are too small by a
+    share that grows with their steps. A segment's (512 steps for fp16, 4096 for
+    bf16, half of 2^-23 a step at half of the sum: under 2^-16 and 2^-13) stays
+    below an eighth of half a step of the type; the roundings of the outputs have
+    no offset."""
+    offset, err = offset_and_error(capi, counts, K, N, dtype, dtype, True, True)
+    half = torch.finfo(dtype).eps / 2
+    assert abs(offset) < half / 8 and err < half, (offset, err)
