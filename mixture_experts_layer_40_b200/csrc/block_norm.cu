@@ -570,7 +570,9 @@ __global__ void __launch_bounds__(kBackThreads, 1) block_norm_backward_kernel(co
     float s[3] = {lanes_sum(sum[0]), lanes_sum(sum[1]), lanes_sum(sum[2])};
     if (p.pre || p.post) team_sum(s, at, buf, turn);
     const float R = rsqrtf(fmaf(s[0], inv_h, p.eps));
-    const float r_part = -R * R * R * (s[1] * inv_h);  // of r in dx
+    // of r in dx; the mean of du pre h first, since R to the third leaves fp32
+    // for rows of 1e14 (or, without eps, of 1e-13)
+    const float r_part = -(s[1] * inv_h * R) * R * R;
     const float Z = p.post ? rsqrtf(fmaf(s[2], inv_h, p.eps)) : 1.0f;
     F2 e[kNC][4];  // dx, then w e (times a full gate)
     F2 t2 = 0ull;
@@ -631,7 +633,7 @@ __global__ void __launch_bounds__(kBackThreads, 1) block_norm_backward_kernel(co
       team_sum(t, at, buf, turn);
       if (p.gate_kind == kGateRow && at.wid == 0 && at.lane == 0)
         static_cast<float*>(p.dgate)[row] = t[0] * Z;
-      if (p.post) z_part = -Z * Z * Z * row_gate * (t[0] * inv_h);
+      if (p.post) z_part = -(t[0] * inv_h * Z) * (Z * row_gate) * Z;
     }
     const F2 zp2 = pack2(z_part, z_part), zg2 = pack2(Z * row_gate, Z * row_gate);
 #pragma unroll

@@ -292,3 +292,35 @@ def test_binding_refuses(capi):
     with pytest.raises(capi.MoeError):
         capi.moe_block_norm_backward(x, EPS, small, du=z, pre_weight=w, dx=r,
                                      dpre=torch.empty(64, device="cuda"))
+
+
+@pytest.mark.parametrize("size,eps", [(1e13, EPS), (1e15, EPS), (1e17, EPS), (1e-8, EPS), (1e-8, 0.0),
+                                      (1e-14, 0.0), (1e-17, 0.0)])
+@pytest.mark.parametrize("dtype", [FP32, BF16])
+def test_gradients_of_large_and_small_rows(capi, size, eps, dtype):
+    """Rows far from one in size, whose squares fp32 still holds: both norms'
+    gradients by the formula, within the module's tolerances (the products of the
+    factors stay in range: at 1e17 the smallest is 1e-34 of order-one terms)."""
+    T, H = 9, 264
+    gen = torch.Generator(device="cuda").manual_seed(3)
+    rn = lambda *s: torch.randn(*s, generator=gen, device="cuda")  # noqa: E731
+    v, up, w = (rn(T, H) * size).to(dtype), rn(T, H).to(dtype), (1 + 0.2 * rn(H)).to(dtype)
+    gate = rn(T).sigmoid()
+    ws = torch.empty(capi.moe_block_norm_backward_workspace_size(H), dtype=torch.uint8, device="cuda")
+    dx, dz = torch.empty_like(v), torch.empty_like(v)
+    dpre, dpost, dgate = torch.empty(H, device="cuda"), torch.empty(H, device="cuda"), torch.empty_like(gate)
+    capi.moe_block_norm_backward(v, eps, ws, du=up, pre_weight=w, dx=dx, dpre=dpre)
+    capi.moe_block_norm_backward(up, eps, ws, dr=up, z=v, post_weight=w, gate=gate, dz=dz,
+                                 dgate=dgate, dpost=dpost)
+    a, q = v.double(), up.double() * w.double()
+    R = torch.rsqrt((a * a).mean(1, keepdim=True) + eps)
+    h = a * R
+    want = R * (q - h * (q * h).mean(1, keepdim=True))
+    mag = R * (q.abs() + h.abs() * (q * h).abs().mean(1, keepdim=True))
+    g = gate.double()[:, None]
+    close(dx, want, mag, 256, "dx")
+    close(dz, g * want, g * mag, 256, "dz")
+    close(dgate, (q * h).sum(1), (q * h).abs().sum(1), 256, "dgate")
+    t = up.double() * h
+    close(dpre, t.sum(0), t.abs().sum(0), 512, "dpre")
+    close(dpost, (g * t).sum(0), (g * t).abs().sum(0), 512, "dpost")
