@@ -324,3 +324,25 @@ def test_gradients_of_large_and_small_rows(capi, size, eps, dtype):
     t = up.double() * h
     close(dpre, t.sum(0), t.abs().sum(0), 512, "dpre")
     close(dpost, (g * t).sum(0), (g * t).abs().sum(0), 512, "dpost")
+
+
+@pytest.mark.parametrize("T,H", [(300_000, 1024), (2_000_000, 64)])
+@pytest.mark.parametrize("positive", [False, True])
+def test_column_sums_over_many_rows(capi, T, H, positive):
+    """A thread's running sum takes T / CTAs / teams rows, rounded to nearest: in
+    the worst case half of 2^-23 of it a row, as a random walk the root of that:
+    under 2^-19 of the terms' magnitudes for thousands of rows."""
+    gen = torch.Generator(device="cuda").manual_seed(5)
+    x = torch.randn(T, H, generator=gen, device="cuda").to(BF16)
+    du = torch.randn(T, H, generator=gen, device="cuda").to(BF16)
+    if positive:
+        du = du.abs() * x.sign()
+    w = torch.ones(H, dtype=BF16, device="cuda")
+    ws = torch.empty(capi.moe_block_norm_backward_workspace_size(H), dtype=torch.uint8, device="cuda")
+    dx, dpre = torch.empty_like(x), torch.empty(H, device="cuda")
+    capi.moe_block_norm_backward(x, EPS, ws, du=du, pre_weight=w, dx=dx, dpre=dpre)
+    ref = torch.zeros(2, H, dtype=torch.float64, device="cuda")
+    for a, b in zip(x.split(50_000), du.split(50_000)):
+        t = b.double() * a.double() * torch.rsqrt((a.double() ** 2).mean(1, keepdim=True) + EPS)
+        ref += torch.stack([t.sum(0), t.abs().sum(0)])
+    assert ((dpre.double() - ref[0]).abs() <= 2.0 ** -19 * ref[1]).all()
