@@ -436,7 +436,7 @@ typedef enum { MOE_BF16 = 0, MOE_FP16 = 1, MOE_FP32 = 2 } moe_type;
  * multiples of 8 up to 2^20; pointers 16-byte aligned; rows < 2^31 - 256
  * (rows = 0: the row buffers may be NULL). out and dw must not overlap the
  * inputs. status_ws: a device uint32 status word, or NULL (may be the forward
- * workspace); read by moe_get_status, which also reports a wait that ran out.
+ * workspace); it and the group arrays are 4-byte aligned; read by moe_get_status, which also reports a wait that ran out.
  */
 int moe_grouped_matmul(int32_t type, int32_t out_type, int32_t n_groups, const int32_t* group_rows,
                        const int32_t* group_start, int64_t rows, int32_t K, int32_t N,

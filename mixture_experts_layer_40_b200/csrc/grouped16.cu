@@ -1666,7 +1666,8 @@ cudaError_t launch_grouped_wgrad(const Groups16& gr, bool f16, int out_type, int
 using namespace moe;
 
 static int grouped_args(int32_t type, int32_t out_type, int32_t n_groups, const int32_t* rows_of,
-                        const int32_t* starts, int64_t rows, int32_t N, int32_t K) {
+                        const int32_t* starts, int64_t rows, int32_t N, int32_t K,
+                        const uint32_t* status) {
   if (type != MOE_BF16 && type != MOE_FP16) return MOE_ERR_SHAPE;
   if (out_type != type && out_type != MOE_FP32) return MOE_ERR_SHAPE;
   if (n_groups < 1 || n_groups > kMaxGroups16 || rows < 0 || rows >= (1ll << 31) - 256)
@@ -1674,6 +1675,8 @@ static int grouped_args(int32_t type, int32_t out_type, int32_t n_groups, const 
   if (N < 8 || N % 8 != 0 || K < 8 || K % 8 != 0) return MOE_ERR_SHAPE;
   if (N > (1 << 20) || K > (1 << 20)) return MOE_ERR_SHAPE;
   if (!rows_of || !starts) return MOE_ERR_NULL;
+  // the kernels read and write them as words
+  if (!aligned(rows_of, 4) || !aligned(starts, 4) || !aligned(status, 4)) return MOE_ERR_ALIGN;
   return MOE_OK;
 }
 
@@ -1683,7 +1686,8 @@ int moe_grouped_matmul(int32_t type, int32_t out_type, int32_t n_groups, const i
                        const int32_t* group_start, int64_t rows, int32_t K, int32_t N,
                        const void* a, const void* b, int32_t trans_b, void* out,
                        uint32_t* status_ws, void* stream) {
-  const int r = grouped_args(type, out_type, n_groups, group_rows, group_start, rows, N, K);
+  const int r =
+      grouped_args(type, out_type, n_groups, group_rows, group_start, rows, N, K, status_ws);
   if (r != MOE_OK) return r;
   if (rows == 0) return MOE_OK;  // nothing to do; empty tensors may carry NULL
   if (!a || !b || !out) return MOE_ERR_NULL;
@@ -1699,7 +1703,8 @@ int moe_grouped_wgrad(int32_t type, int32_t out_type, int32_t n_groups, const in
                       const int32_t* group_start, int64_t rows, int32_t N, int32_t K,
                       const void* dy, const void* x, void* dw, int32_t accumulate,
                       uint32_t* status_ws, void* stream) {
-  const int r = grouped_args(type, out_type, n_groups, group_rows, group_start, rows, N, K);
+  const int r =
+      grouped_args(type, out_type, n_groups, group_rows, group_start, rows, N, K, status_ws);
   if (r != MOE_OK) return r;
   if (!dw || (rows > 0 && (!dy || !x))) return MOE_ERR_NULL;
   if (!aligned(dy, 16) || !aligned(x, 16) || !aligned(dw, 16)) return MOE_ERR_ALIGN;

@@ -285,3 +285,13 @@ def test_block_backward_needs_the_forwards_x(capi, monkeypatch):
         block.forward(r, None)
     with pytest.raises(ValueError, match="forward"):
         block.backward(r, weights=False)
+
+
+@pytest.mark.parametrize("off", [1, 2, 3])
+def test_words_off_their_boundary_refused(capi, off):
+    """The group arrays and the status word are read and written as 4-byte words."""
+    lib = capi.LIB
+    for gr, gs, status in [(P + off, P, None), (P, P + off, None), (P, P, P + off)]:
+        for rows in (64, 0):
+            assert lib.moe_grouped_matmul(0, 0, 4, gr, gs, rows, 64, 64, P, P, 1, P, status, None) == ALIGN
+            assert lib.moe_grouped_wgrad(0, 2, 4, gr, gs, rows, 64, 64, P, P, P, 0, status, None) == ALIGN
