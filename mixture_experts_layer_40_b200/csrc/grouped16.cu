@@ -95,6 +95,7 @@ struct alignas(8) Shared16 {
   uint64_t freed;                // and read
   uint32_t tmem_base;
   int abort;
+  int asked;                     // weight gradient: k-blocks that the producer has asked for
   int prefix[kMaxGroups16 + 1];
   int rows[kMaxGroups16];
   int start[kMaxGroups16];
@@ -163,6 +164,29 @@ MOE_DEV bool mbar_wait_pair(uint32_t bar, uint32_t parity, volatile int* abort, 
         *abort = 1;
         return false;
       }
+    }
+  }
+}
+
+// mbar_wait for a block that the producer may ask for much later, behind tiles
+// that the waiting warp has no part in: the time limit runs from the last block
+// that was asked for.
+MOE_DEV bool mbar_wait_behind(uint32_t bar, uint32_t parity, const volatile int* asked,
+                              volatile int* abort, uint32_t* status) {
+  unsigned long long t0 = global_ns();
+  int seen = *asked;
+  for (uint32_t i = 1;; ++i) {
+    if (mbar_try_wait(bar, parity)) return true;
+    if ((i & 63u) != 0u) continue;
+    if (*abort) return false;
+    const int now = *asked;
+    if (now != seen) {
+      seen = now;
+      t0 = global_ns();
+    } else if (global_ns() - t0 > kWaitLimitNs) {
+      flag_status(status, kStatusTimeout);
+      *abort = 1;
+      return false;
     }
   }
 }
@@ -1144,6 +1168,7 @@ __global__ void __cluster_dims__(kCtas * kSplit, 1, 1) __launch_bounds__(kWThrea
       mbar_init(smem_u32(&sh.freed), 8 * kSplit);
     }
     sh.abort = 0;
+    sh.asked = 0;
     fence_mbar_init();
     prefetch_tensormap(&tm_a);
     prefetch_tensormap(&tm_b);
@@ -1194,6 +1219,7 @@ __global__ void __cluster_dims__(kCtas * kSplit, 1, 1) __launch_bounds__(kWThrea
           const bool clear = kb == kb_n - 1 && to_clear(rows, kb);
           if (clear) part_phase ^= 1u << at.stage();
           if (!elected) continue;
+          *static_cast<volatile int*>(&sh.asked) = it + 1;
           // the last block only as far as its 16-row steps go
           const int steps = min((rows - kb * kBK + 15) / 16, kBK / 16);
           const uint32_t bytes = (uint32_t)(C::stage_bytes / (kBK / 16) * steps);
@@ -1247,8 +1273,8 @@ __global__ void __cluster_dims__(kCtas * kSplit, 1, 1) __launch_bounds__(kWThrea
       it += of.end - of.begin;
       if (of.begin == of.end || of.end < kb_n || !to_clear(rows, kb_n - 1)) continue;
       const int s = (it - 1) % C::stages;
-      if (!__all_sync(0xffffffffu, mbar_wait(smem_u32(&sh.part[s]), (part_phase >> s) & 1u, abort,
-                                             p.status)))
+      if (!__all_sync(0xffffffffu, mbar_wait_behind(smem_u32(&sh.part[s]), (part_phase >> s) & 1u,
+                                                    &sh.asked, abort, p.status)))
         break;
       part_phase ^= 1u << s;
       // up to the next 16-row step, in every 64-column box (a swizzled row

@@ -477,3 +477,25 @@ def test_matmul_long_sums_have_no_offset(capi, counts, N, dtype, K):
     offset, err = offset_and_error(capi, counts, K, N, dtype, dtype, True, True)
     half = torch.finfo(dtype).eps / 2
     assert abs(offset) < half / 8 and err < half, (offset, err)
+
+
+def test_wgrad_short_group_behind_seconds_of_others(capi):
+    """A CTA works for longer than the kernel's wait limit (2 s) on a group whose
+    rows need no clearing before it comes to one whose rows do. 149 groups of one
+    tile go round 148 CTAs, so the first and the last share one; the first has a
+    billion rows, at a quarter of a microsecond for 64. Sums of ones are exact."""
+    from mixture_experts_layer_40_b200 import capi as c
+    sms = c.LIB.moe_device_sm_count()
+    long = 1_000_000_000 // 64 * 64
+    x = torch.zeros(long + 5, 8, dtype=BF16, device="cuda")
+    x[::1 << 20] = 1.0
+    x[long:] = 2.0
+    counts = torch.zeros(sms + 1, dtype=torch.int32)
+    counts[0], counts[sms] = long, 5
+    starts = torch.cumsum(counts, 0, dtype=torch.int32) - counts
+    dw = torch.full((sms + 1, 8, 8), 7.0, device="cuda")
+    status = torch.zeros(4, dtype=torch.int32, device="cuda")
+    capi.moe_grouped_wgrad(x, x, counts.cuda(), starts.cuda(), dw, status=status)
+    assert capi.moe_get_status(status) == 0
+    assert (dw[0] == -(-long // (1 << 20))).all()
+    assert (dw[sms] == 20.0).all() and not dw[1:sms].any()
