@@ -16,7 +16,7 @@ class MoEBlock:
     gate and residual. post_weight, scale (weights [H], bf16 or float32 alike)
     and gate (float32 [T], or bf16 [T, H]) are optional. x is bf16 or float32;
     the layer runs on bf16. The block keeps the last forward's x, u and the
-    layer's output for the backward."""
+    layer's output (with next_weight also r) for the backward."""
 
     def __init__(self, layer: MoELayer, pre_weight: torch.Tensor,
                  post_weight: torch.Tensor | None = None, scale: torch.Tensor | None = None,
@@ -26,15 +26,17 @@ class MoEBlock:
         shape = (layer.T, layer.H)
         self.u = torch.empty(shape, dtype=torch.bfloat16, device=layer.device)
         self.z = torch.empty(shape, dtype=torch.bfloat16, device=layer.device)
-        self.x = self.gate = self._ws = None
+        self.x = self.gate = self.r = self.next_weight = self._ws = None
 
     def forward(self, x: torch.Tensor, bias: torch.Tensor, gate: torch.Tensor | None = None,
                 r: torch.Tensor | None = None, next_weight: torch.Tensor | None = None,
                 stream=None):
         """r [T, H] like x; with next_weight also u = N(r; next_weight), the
-        next block's input, from the same pass: (r, u). r may be x, in place;
-        there is no backward then, which reads x."""
-        self.x = self.gate = None  # the layer's state is a new forward's from here on
+        normed input of what follows the block (an MoEBlock norms its own x),
+        from the same pass: (r, u). r may be x, in place; there is no backward
+        then, which reads x."""
+        # the layer's state is a new forward's from here on
+        self.x = self.gate = self.r = self.next_weight = None
         with torch.cuda.stream(stream):  # None: the current one
             capi.moe_block_norm(x, self.eps, pre_weight=self.pre_weight, u=self.u, stream=stream)
             self.layer.forward(self.u, bias, self.z, stream)
@@ -46,16 +48,23 @@ class MoEBlock:
                                 alpha=self.alpha, r=r, stream=stream)
             if r.data_ptr() != x.data_ptr():
                 self.x, self.gate = x, gate
+                if next_weight is not None:
+                    self.r, self.next_weight = r, next_weight
             return r if next_weight is None else (r, u)
 
-    def backward(self, dr: torch.Tensor, weights: bool = True, stream=None) -> dict:
-        """Gradients of the last forward for the upstream gradient dr of r, with
-        the routing held fixed: a dict of dx (through the residual and the
-        experts), gates (the layer's gate gradients, [T, K]), pre_weight, and
-        as they were given post_weight, scale and gate; with `weights` also w13
-        and w2."""
+    def backward(self, dr: torch.Tensor, weights: bool = True, stream=None,
+                 du: torch.Tensor | None = None) -> dict:
+        """Gradients of the last forward for the upstream gradients dr of r and,
+        of a forward with next_weight, du of u (None: u was used for nothing
+        that has a gradient), with the routing held fixed: a dict of dx (through
+        the residual and the experts), gates (the layer's gate gradients,
+        [T, K]), pre_weight, and as they were given post_weight, scale and gate;
+        with du also next_weight; with `weights` also w13 and w2. With du the
+        forward's r is read and must be as it was left."""
         if self.x is None:
             raise ValueError("backward needs a forward before it, and not one in place")
+        if du is not None and self.next_weight is None:
+            raise ValueError("du needs a forward with next_weight before it")
         with torch.cuda.stream(stream):  # None: the current one
             dev, H = self.layer.device, self.layer.H
             if self._ws is None:
@@ -69,15 +78,20 @@ class MoEBlock:
                    "scale": column(self.scale),
                    "gate": None if self.gate is None else torch.empty_like(self.gate)}
             dz = torch.empty_like(self.z)
-            # r itself is only read with a norm of r, which this half has not
-            capi.moe_block_norm_backward(dr, self.eps, self._ws, dr=dr, z=self.z,
+            # with du the norm of r joins in, and e is the whole gradient of r (to
+            # dz unrounded, to dx rounded to x's type); without it r is not read
+            e, r, norm = dr, dr, {}
+            if du is not None:
+                e, r, out["next_weight"] = torch.empty_like(dr), self.r, column(self.next_weight)
+                norm = {"du": du, "pre_weight": self.next_weight, "dx": e, "dpre": out["next_weight"]}
+            capi.moe_block_norm_backward(r, self.eps, self._ws, dr=dr, z=self.z,
                                          post_weight=self.post_weight, gate=self.gate,
                                          scale=self.scale, alpha=self.alpha, dz=dz,
                                          dgate=out["gate"], dscale=out["scale"],
-                                         dpost=out["post_weight"], stream=stream)
+                                         dpost=out["post_weight"], stream=stream, **norm)
             grads = self.layer.backward(dz, self.u if weights else None, stream)
             dx = torch.empty_like(self.x)
-            capi.moe_block_norm_backward(self.x, self.eps, self._ws, dr=dr, du=grads[0],
+            capi.moe_block_norm_backward(self.x, self.eps, self._ws, dr=e, du=grads[0],
                                          pre_weight=self.pre_weight, dx=dx, dpre=out["pre_weight"],
                                          stream=stream)
             out.update(dx=dx, gates=grads[1])

@@ -161,3 +161,87 @@ def test_step_in_a_graph():
     assert torch.equal(got_r, eager_r)
     for k in eager:
         assert torch.equal(got[k], eager[k]), k
+
+
+def norm64(v, w):
+    return v * torch.rsqrt((v * v).mean(1, keepdim=True) + 1e-6) * w
+
+
+@pytest.mark.parametrize("res", [BF16, torch.float32])
+@pytest.mark.parametrize("gate_kind", ["row", "full", "none"])
+@pytest.mark.parametrize("with_du", [False, True])
+def test_every_gradient_of_the_block(res, gate_kind, with_du):
+    """All of the backward's gradients: bit for bit what the norms' two backwards
+    and the layer's give one by one, and against float64 around the layer, with
+    and without a gradient of the second output u = N(r; next_weight).
+
+    The norms' sums are off by at most 2^-15 of their terms' magnitudes (512 units
+    of 2^-24), which for sums of 64 random terms are about 8 times the result:
+    2^-12 in the norm. dx in bf16 is rounded once, with du also half-way: 2^-7."""
+    from mixture_experts_layer_40_b200 import capi
+    from mixture_experts_layer_40_b200.block import MoEBlock
+    case, layer, bias = a_layer()
+    T, Hs = layer.T, layer.H
+    gen = torch.Generator(device="cuda").manual_seed(2)
+    rn = lambda *s: torch.randn(*s, generator=gen, device="cuda")  # noqa: E731
+    pre, post, scale = 1 + 0.2 * rn(Hs), 1 + 0.2 * rn(Hs), 0.5 + 0.1 * rn(Hs)
+    nxt = 1 + 0.2 * rn(Hs)
+    x = H.x_to_device(case.x_bits).to(res)
+    gate = {"row": rn(T).sigmoid(), "full": rn(T, Hs).sigmoid().to(BF16), "none": None}[gate_kind]
+    block = MoEBlock(layer, pre, post, scale, alpha=0.5)
+    r, u = block.forward(x, bias, gate, next_weight=nxt)
+    dr, du = rn(T, Hs).to(res), rn(T, Hs).to(BF16) if with_du else None
+    got = block.backward(dr, du=du)
+    assert layer.status() == 0
+    names = {"dx", "gates", "pre_weight", "post_weight", "scale", "w13", "w2"}
+    names |= {"gate"} if gate is not None else set()
+    assert set(got) == names | ({"next_weight"} if with_du else set())
+
+    # the parts one by one
+    ws = torch.empty(capi.moe_block_norm_backward_workspace_size(Hs), dtype=torch.uint8, device="cuda")
+    col = lambda: torch.empty(Hs, device="cuda")  # noqa: E731
+    e, dz, dpost, dscale = torch.empty_like(dr), torch.empty_like(block.z), col(), col()
+    dgate = None if gate is None else torch.empty_like(gate)
+    more = {"du": du, "pre_weight": nxt, "dx": e, "dpre": col()} if with_du else {}
+    capi.moe_block_norm_backward(r, 1e-6, ws, dr=dr, z=block.z, post_weight=post, gate=gate,
+                                 scale=scale, alpha=0.5, dz=dz, dgate=dgate, dscale=dscale,
+                                 dpost=dpost, **more)
+    d_in, dgates, dw13, dw2 = layer.backward(dz, block.u)
+    dx, dpre = torch.empty_like(x), col()
+    capi.moe_block_norm_backward(x, 1e-6, ws, dr=e if with_du else dr, du=d_in, pre_weight=pre,
+                                 dx=dx, dpre=dpre)
+    want = {"dx": dx, "gates": dgates, "pre_weight": dpre, "post_weight": dpost, "scale": dscale,
+            "gate": dgate, "w13": dw13, "w2": dw2, "next_weight": more.get("dpre")}
+    for k in got:
+        assert torch.equal(got[k], want[k]), k
+
+    # around the layer in float64
+    leaf = lambda t: None if t is None else t.double().requires_grad_()  # noqa: E731
+    near = lambda a, b, t: (a.double() - b).norm() <= t * b.norm()  # noqa: E731
+    rl, nl, zl, pl, sl, gl, xl, wl = map(leaf, (r, nxt, block.z, post, scale, gate, x, pre))
+    up = dr.double()
+    if with_du:
+        (norm64(rl, nl) * du.double()).sum().backward()
+        up = up + rl.grad
+        assert near(got["next_weight"], nl.grad, 2.0 ** -12)
+    branch = 0.5 * sl * norm64(zl, pl)
+    if gate is not None:
+        branch = branch * (gl[:, None] if gate_kind == "row" else gl)
+    (branch * up).sum().backward()
+    assert near(got["post_weight"], pl.grad, 2.0 ** -12) and near(got["scale"], sl.grad, 2.0 ** -12)
+    assert near(dz, zl.grad, 2.0 ** -8)
+    if gate is not None:
+        assert near(got["gate"], gl.grad, 2.0 ** -12 if gate_kind == "row" else 2.0 ** -8)
+    (norm64(xl, wl) * d_in.double()).sum().backward()
+    assert near(got["pre_weight"], wl.grad, 2.0 ** -12)
+    assert near(got["dx"], up + xl.grad, 2.0 ** -12 if res != BF16 else 2.0 ** -7)
+
+
+def test_gradient_of_u_needs_its_weight():
+    from mixture_experts_layer_40_b200.block import MoEBlock
+    case, layer, bias = a_layer()
+    x = H.x_to_device(case.x_bits)
+    block = MoEBlock(layer, torch.ones(layer.H, device="cuda"))
+    block.forward(x, bias)
+    with pytest.raises(ValueError, match="next_weight"):
+        block.backward(x, du=x)
