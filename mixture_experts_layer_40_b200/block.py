@@ -104,12 +104,20 @@ class GroupedLinear:
     """y[r] = x[r] W_g^T for the rows of each expert's group: weight [G, N, K],
     bf16 or fp16. The groups are device arrays (rows and first row of each),
     packed or with gaps, as MoELayer's workspace views "group_rows" and
-    "row_start" hold them after a forward."""
+    "row_start" hold them after a forward. A group table that fails the kernels'
+    checks, or a wait that ran out, shows in status(), or in the status word
+    that a call was given."""
 
     def __init__(self, weight: torch.Tensor):
         if weight.dim() != 3:
             raise ValueError("weight must be [groups, N, K]")
         self.weight = weight
+        self._status = torch.zeros(1, dtype=torch.int32, device=weight.device)
+
+    def status(self, stream=None) -> int:
+        """MOE_OK, or the error code of the calls since the last status();
+        waits for the stream."""
+        return capi.moe_get_status(self._status, stream)
 
     def forward(self, x, group_rows, group_start, y=None, status=None, stream=None):
         """y [R, N] like x; rows outside the groups stay as they are (zero in a
@@ -117,7 +125,8 @@ class GroupedLinear:
         with torch.cuda.stream(stream):  # None: the current one
             if y is None:
                 y = torch.zeros((x.shape[0], self.weight.shape[1]), dtype=x.dtype, device=x.device)
-            capi.moe_grouped_matmul(x, self.weight, group_rows, group_start, y, True, status, stream)
+            capi.moe_grouped_matmul(x, self.weight, group_rows, group_start, y, True,
+                                    self._status if status is None else status, stream)
             return y
 
     def backward(self, dy, x, group_rows, group_start, dw=None, accumulate=False, dx=None,
@@ -126,6 +135,8 @@ class GroupedLinear:
         gradient is added to the dw given."""
         if accumulate and dw is None:
             raise ValueError("accumulate needs the dw to add to")
+        if status is None:
+            status = self._status
         with torch.cuda.stream(stream):  # None: the current one
             if dx is None:
                 dx = torch.zeros((dy.shape[0], self.weight.shape[2]), dtype=dy.dtype, device=dy.device)

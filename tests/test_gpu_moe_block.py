@@ -245,3 +245,25 @@ def test_gradient_of_u_needs_its_weight():
     block.forward(x, bias)
     with pytest.raises(ValueError, match="next_weight"):
         block.backward(x, du=x)
+
+
+def test_grouped_linear_reports_bad_groups():
+    """Without a status word of the caller's, the holder's own tells of group
+    tables that fail the checks, in the forward and in the backward."""
+    from mixture_experts_layer_40_b200.block import GroupedLinear
+    gen = torch.Generator(device="cuda").manual_seed(3)
+    lin = GroupedLinear(torch.randn(2, 32, 64, generator=gen, device="cuda").to(BF16))
+    x = torch.randn(20, 64, generator=gen, device="cuda").to(BF16)
+    dy = torch.randn(20, 32, generator=gen, device="cuda").to(BF16)
+    ints = lambda *v: torch.tensor(v, dtype=torch.int32, device="cuda")  # noqa: E731
+    good, bad = (ints(10, 10), ints(0, 10)), (ints(10, 11), ints(0, 10))
+    lin.forward(x, *good)
+    lin.backward(dy, x, *good)
+    assert lin.status() == 0
+    lin.forward(x, *bad)
+    assert lin.status() == -5 and lin.status() == 0  # MOE_ERR_BOUNDS, told once
+    lin.backward(dy, x, *bad)
+    assert lin.status() == -5
+    word = torch.zeros(1, dtype=torch.int32, device="cuda")
+    lin.forward(x, *bad, status=word)
+    assert lin.status() == 0 and int(word) != 0
