@@ -170,4 +170,5 @@ class GradClip:
         the next call)."""
         capi.moe_grad_sumsq(self.list, self.partials, stream)
         capi.moe_grad_clip(self.list, self.partials, max_norm, self.norm, stream)
+        capi.keep_until_done(self.list.device, stream, self.partials, self.norm)
         return self.norm

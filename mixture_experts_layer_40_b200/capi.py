@@ -368,6 +368,16 @@ def _run(name: str, device: int, stream, *args) -> None:
         raise MoeError(name, code)
 
 
+def keep_until_done(device: int, stream, *tensors) -> None:
+    """The tensors' memory is not given to others before `stream` (None: the
+    device's current one) is done with what it holds now, even if they are
+    dropped; for tensors that a holder made on one stream and uses on another."""
+    at = torch.cuda.current_stream(device) if stream is None else stream
+    for t in tensors:
+        if t is not None:
+            t.record_stream(at)
+
+
 def _sums_type(t: torch.Tensor, of: torch.Tensor, name: str) -> int:
     if t.dtype not in (of.dtype, torch.float32):
         raise ValueError(f"{name} must be {of.dtype} or float32, got {t.dtype}")
@@ -553,6 +563,7 @@ class GradList:
                                     cast(s, ctypes.POINTER(ctypes.c_int64)),
                                     cast(t, ctypes.POINTER(ctypes.c_int32)), None)
         # longer lists read their table from device memory
+        self._table = None
         nbytes = int(LIB.moe_grad_table_size(ctypes.byref(self.struct)))
         if nbytes:
             host = torch.empty(nbytes, dtype=torch.uint8)
@@ -600,6 +611,8 @@ def moe_grad_sumsq(gl: GradList, partials, stream=None):
     experts, add the ranks' partials (an all-reduce) before moe_grad_clip."""
     dev, p = _partials(gl, partials)
     _run("moe_grad_sumsq", dev, stream, ctypes.byref(gl.struct), p)
+    if gl._table is not None:
+        keep_until_done(dev, stream, gl._table)
 
 
 def moe_grad_clip(gl: GradList, partials, max_norm: float, norm, stream=None):
@@ -608,6 +621,8 @@ def moe_grad_clip(gl: GradList, partials, max_norm: float, norm, stream=None):
     dev, p = _partials(gl, partials)
     _run("moe_grad_clip", dev, stream, ctypes.byref(gl.struct), p, float(max_norm),
          _need(norm, torch.float32, (1,), dev, "norm"))
+    if gl._table is not None:
+        keep_until_done(dev, stream, gl._table)
 
 
 def moe_ep_row_bytes(sh: moe_shape) -> int:

@@ -228,3 +228,36 @@ def test_binding_refuses(capi):
         capi.make_grad_list([a.view(8, 8).T])
     with pytest.raises(ValueError):
         capi.moe_grad_sumsq(capi.make_grad_list([a]), a)
+
+
+@pytest.mark.parametrize("n", [3, 40])
+def test_dropped_holders_keep_their_memory_until_done(capi, n):
+    """A GradClip, and a list with its table, used on another stream than the one
+    they were made on and dropped at once: their memory goes to nobody else while
+    that stream still has their work before it."""
+    from mixture_experts_layer_40_b200.block import GradClip
+    g = grads_of([500] * n, [FP32, BF16])
+    total = math.sqrt(sum(float((x.double() ** 2).sum()) for x in g))
+    side = torch.cuda.Stream()
+    for explicit in (True, False):
+        clip = GradClip(g)
+        table = clip.list._table
+        places = [(clip.partials.data_ptr(), 8192)]
+        places += [(table.data_ptr(), table.numel())] if table is not None else []
+        torch.cuda.synchronize()
+        with torch.cuda.stream(side):
+            torch.cuda._sleep(200_000_000)
+        if explicit:
+            norm = clip(math.inf, stream=side)
+        else:
+            with torch.cuda.stream(side):
+                norm = clip(math.inf)
+        del clip, table
+        held = [torch.full((size,), 255, dtype=torch.uint8, device="cuda")
+                for _ in range(300) for _, size in places]
+        taken = {t.data_ptr() for t in held}
+        assert not side.query()
+        assert not any(at in taken for at, _ in places)
+        torch.cuda.synchronize()
+        assert abs(float(norm) - total) <= 6 * U * total
+        del held
