@@ -50,6 +50,7 @@ class MoEBlock:
                 self.x, self.gate = x, gate
                 if next_weight is not None:
                     self.r, self.next_weight = r, next_weight
+            self._keep(stream)
             return r if next_weight is None else (r, u)
 
     def backward(self, dr: torch.Tensor, weights: bool = True, stream=None,
@@ -94,10 +95,15 @@ class MoEBlock:
             capi.moe_block_norm_backward(self.x, self.eps, self._ws, dr=e, du=grads[0],
                                          pre_weight=self.pre_weight, dx=dx, dpre=out["pre_weight"],
                                          stream=stream)
+            self._keep(stream)
             out.update(dx=dx, gates=grads[1])
             if weights:
                 out.update(w13=grads[2], w2=grads[3])
             return {k: v for k, v in out.items() if v is not None}
+
+    def _keep(self, stream):
+        if self.u.is_cuda:
+            capi.keep_until_done(self.u.device.index, stream, self.u, self.z, self._ws)
 
 
 class GroupedLinear:
@@ -119,6 +125,9 @@ class GroupedLinear:
         waits for the stream."""
         return capi.moe_get_status(self._status, stream)
 
+    def _keep(self, stream):
+        capi.keep_until_done(self._status.device.index, stream, self._status)
+
     def forward(self, x, group_rows, group_start, y=None, status=None, stream=None):
         """y [R, N] like x; rows outside the groups stay as they are (zero in a
         new y)."""
@@ -127,6 +136,7 @@ class GroupedLinear:
                 y = torch.zeros((x.shape[0], self.weight.shape[1]), dtype=x.dtype, device=x.device)
             capi.moe_grouped_matmul(x, self.weight, group_rows, group_start, y, True,
                                     self._status if status is None else status, stream)
+            self._keep(stream)
             return y
 
     def backward(self, dy, x, group_rows, group_start, dw=None, accumulate=False, dx=None,
@@ -144,6 +154,7 @@ class GroupedLinear:
                 dw = torch.empty(self.weight.shape, dtype=torch.float32, device=dy.device)
             capi.moe_grouped_matmul(dy, self.weight, group_rows, group_start, dx, False, status, stream)
             capi.moe_grouped_wgrad(dy, x, group_rows, group_start, dw, accumulate, status, stream)
+            self._keep(stream)
             return dx, dw
 
 

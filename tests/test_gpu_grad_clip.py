@@ -239,6 +239,10 @@ def test_dropped_holders_keep_their_memory_until_done(capi, n):
     g = grads_of([500] * n, [FP32, BF16])
     total = math.sqrt(sum(float((x.double() ** 2).sum()) for x in g))
     side = torch.cuda.Stream()
+    # every kernel once: loading one waits for the GPU
+    GradClip(g)(math.inf)
+    torch.cuda._sleep(1)
+    torch.full((8,), 255, dtype=torch.uint8, device="cuda")
     for explicit in (True, False):
         clip = GradClip(g)
         table = clip.list._table
@@ -246,7 +250,7 @@ def test_dropped_holders_keep_their_memory_until_done(capi, n):
         places += [(table.data_ptr(), table.numel())] if table is not None else []
         torch.cuda.synchronize()
         with torch.cuda.stream(side):
-            torch.cuda._sleep(200_000_000)
+            torch.cuda._sleep(1_000_000_000)  # half a second
         if explicit:
             norm = clip(math.inf, stream=side)
         else:

@@ -267,3 +267,38 @@ def test_grouped_linear_reports_bad_groups():
     word = torch.zeros(1, dtype=torch.int32, device="cuda")
     lin.forward(x, *bad, status=word)
     assert lin.status() == 0 and int(word) != 0
+
+
+def test_dropped_holders_keep_their_memory_until_done():
+    """A block and a grouped map used on another stream than the one they were
+    made on and dropped at once: the memory they made goes to nobody else while
+    that stream still has their work before it."""
+    from mixture_experts_layer_40_b200.block import GroupedLinear, MoEBlock
+    case, layer, bias = a_layer()
+    x = H.x_to_device(case.x_bits)
+    w = torch.ones(layer.H, device="cuda")
+    rows = torch.tensor([layer.T], dtype=torch.int32, device="cuda")
+    start = torch.zeros_like(rows)
+    maps = torch.randn(1, 64, layer.H, device="cuda").to(BF16)
+    # every kernel once: loading one waits for the GPU
+    MoEBlock(layer, w).forward(x, bias)
+    GroupedLinear(maps).forward(x, rows, start)
+    torch.cuda._sleep(1)
+    torch.full((8,), 255, dtype=torch.uint8, device="cuda")
+    side = torch.cuda.Stream()
+    block, lin = MoEBlock(layer, w), GroupedLinear(maps)
+    places = [(t.data_ptr(), t.numel() * t.element_size()) for t in (block.u, block.z, lin._status)]
+    torch.cuda.synchronize()
+    with torch.cuda.stream(side):
+        torch.cuda._sleep(1_000_000_000)  # half a second
+    r = block.forward(x, bias, stream=side)
+    y = lin.forward(x, rows, start, stream=side)
+    del block, lin
+    held = [torch.full((size,), 255, dtype=torch.uint8, device="cuda")
+            for _ in range(300) for _, size in places]
+    taken = {t.data_ptr() for t in held}
+    assert not side.query()
+    assert not any(at in taken for at, _ in places)
+    torch.cuda.synchronize()
+    assert torch.equal(r, MoEBlock(layer, w).forward(x, bias))
+    assert torch.equal(y, GroupedLinear(maps).forward(x, rows, start))
