@@ -25,6 +25,8 @@ class MoEBlock:
         self.pre_weight, self.post_weight, self.scale = pre_weight, post_weight, scale
         shape = (layer.T, layer.H)
         self.u = torch.empty(shape, dtype=torch.bfloat16, device=layer.device)
+        # the layer runs on the current device: made so in every call
+        self._index = self.u.device.index if self.u.is_cuda else -1
         self.z = torch.empty(shape, dtype=torch.bfloat16, device=layer.device)
         self.x = self.gate = self.r = self.next_weight = self._ws = None
 
@@ -37,7 +39,7 @@ class MoEBlock:
         then, which reads x."""
         # the layer's state is a new forward's from here on
         self.x = self.gate = self.r = self.next_weight = None
-        with torch.cuda.stream(stream):  # None: the current one
+        with torch.cuda.device(self._index), torch.cuda.stream(stream):  # None: the current one
             capi.moe_block_norm(x, self.eps, pre_weight=self.pre_weight, u=self.u, stream=stream)
             self.layer.forward(self.u, bias, self.z, stream)
             if r is None:
@@ -66,7 +68,7 @@ class MoEBlock:
             raise ValueError("backward needs a forward before it, and not one in place")
         if du is not None and self.next_weight is None:
             raise ValueError("du needs a forward with next_weight before it")
-        with torch.cuda.stream(stream):  # None: the current one
+        with torch.cuda.device(self._index), torch.cuda.stream(stream):  # None: the current one
             dev, H = self.layer.device, self.layer.H
             if self._ws is None:
                 nbytes = capi.moe_block_norm_backward_workspace_size(H)

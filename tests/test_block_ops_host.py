@@ -295,3 +295,43 @@ def test_words_off_their_boundary_refused(capi, off):
         for rows in (64, 0):
             assert lib.moe_grouped_matmul(0, 0, 4, gr, gs, rows, 64, 64, P, P, 1, P, status, None) == ALIGN
             assert lib.moe_grouped_wgrad(0, 2, 4, gr, gs, rows, 64, 64, P, P, P, 0, status, None) == ALIGN
+
+
+def test_block_makes_its_device_the_current_one(capi, monkeypatch):
+    """The layer launches on the current device, the norms on their tensors': a
+    block on another device than the current one makes it current for both."""
+    from mixture_experts_layer_40_b200.block import MoEBlock
+
+    now = [0]
+
+    class Device:
+        def __init__(self, index):
+            self.index = index
+
+        def __enter__(self):
+            now.append(self.index)
+
+        def __exit__(self, *exc):
+            now.pop()
+
+    class Layer(FakeLayer):
+        seen = []
+
+        def forward(self, u, bias, z, stream):
+            self.seen.append(now[-1])
+
+        def backward(self, dz, u, stream):
+            self.seen.append(now[-1])
+            return super().backward(dz, u, stream)
+
+    monkeypatch.setattr(torch.cuda, "device", Device)
+    for name in ("moe_block_norm", "moe_block_norm_backward", "keep_until_done"):
+        monkeypatch.setattr(capi, name, lambda *a, **k: None)
+    monkeypatch.setattr(capi, "moe_block_norm_backward_workspace_size", lambda H: 16)
+    block = MoEBlock(Layer(), torch.ones(64))
+    assert block._index == -1  # host memory: no device
+    block._index = 1
+    x = torch.zeros(4, 64)
+    block.forward(x, None)
+    block.backward(x, weights=False)
+    assert Layer.seen == [1, 1] and now == [0]
