@@ -16,7 +16,9 @@ class MoEBlock:
     gate and residual. post_weight, scale (weights [H], bf16 or float32 alike)
     and gate (float32 [T], or bf16 [T, H]) are optional. x is bf16 or float32;
     the layer runs on bf16. The block keeps the last forward's x, u and the
-    layer's output (with next_weight also r) for the backward."""
+    layer's output (with next_weight also r) for the backward, and the layer its
+    routing and rows: a backward after another pass of the same layer is refused
+    (one inside a graph of the caller's cannot be seen)."""
 
     def __init__(self, layer: MoELayer, pre_weight: torch.Tensor,
                  post_weight: torch.Tensor | None = None, scale: torch.Tensor | None = None,
@@ -42,6 +44,7 @@ class MoEBlock:
         with torch.cuda.device(self._index), torch.cuda.stream(stream):  # None: the current one
             capi.moe_block_norm(x, self.eps, pre_weight=self.pre_weight, u=self.u, stream=stream)
             self.layer.forward(self.u, bias, self.z, stream)
+            self._pass = getattr(self.layer, "passes", None)
             if r is None:
                 r = torch.empty_like(x)
             u = None if next_weight is None else torch.empty_like(self.z)
@@ -66,6 +69,8 @@ class MoEBlock:
         forward's r is read and must be as it was left."""
         if self.x is None:
             raise ValueError("backward needs a forward before it, and not one in place")
+        if getattr(self.layer, "passes", None) != self._pass:
+            raise ValueError("the layer has run since this block's forward; its state is another's")
         if du is not None and self.next_weight is None:
             raise ValueError("du needs a forward with next_weight before it")
         with torch.cuda.device(self._index), torch.cuda.stream(stream):  # None: the current one

@@ -94,11 +94,14 @@ class MoELayer:
         self.ids = torch.empty((T, K), dtype=torch.int32, device=self.device)
         self.gates = torch.empty((T, K), dtype=torch.float32, device=self.device)
         self.counts = torch.empty((N,), dtype=torch.int32, device=self.device)
+        # forwards, routings and replays so far: whose state the workspace holds
+        self.passes = 0
 
     def forward(self, x: torch.Tensor, bias: torch.Tensor, y: torch.Tensor | None = None,
                 stream=None) -> torch.Tensor:
         if y is None:
             y = torch.empty((self.T, self.H), dtype=torch.bfloat16, device=self.device)
+        self.passes += 1
         capi.moe_forward(self.shape, self._cw, x, bias, y, self.ids, self.gates, self.counts,
                          self.ws, stream)
         return y
@@ -117,6 +120,7 @@ class MoELayer:
             capi.moe_transpose_weights(self.shape, self._cw, *self._wt_bufs, stream)
 
     def route(self, x: torch.Tensor, bias: torch.Tensor, stream=None):
+        self.passes += 1
         capi.moe_route(self.shape, self.weights.gate_w, x, bias, self.ids, self.gates,
                        self.counts, self.ws, stream)
         return self.ids, self.gates, self.counts
@@ -211,6 +215,7 @@ class GraphedStep:
 
     def replay(self) -> torch.Tensor:
         """Runs the step on the current stream; returns y (the same tensor)."""
+        self.layer.passes += 1
         self.graph.replay()
         return self.y
 

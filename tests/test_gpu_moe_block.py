@@ -302,3 +302,26 @@ def test_dropped_holders_keep_their_memory_until_done():
     torch.cuda.synchronize()
     assert torch.equal(r, MoEBlock(layer, w).forward(x, bias))
     assert torch.equal(y, GroupedLinear(maps).forward(x, rows, start))
+
+
+def test_backward_after_another_pass_of_the_layer_is_refused():
+    """Two blocks around one layer, or a call of the layer itself between a block's
+    forward and its backward: the layer's routing and rows are another pass's."""
+    from mixture_experts_layer_40_b200.block import MoEBlock
+    case, layer, bias = a_layer()
+    x = H.x_to_device(case.x_bits)
+    w = torch.ones(layer.H, device="cuda")
+    first, second = MoEBlock(layer, w), MoEBlock(layer, w)
+    step = layer.graphed_step(x, bias)
+    first.forward(x, bias)
+    want = first.backward(x)
+    for between in (lambda: second.forward(x, bias), lambda: layer.forward(x, bias),
+                    lambda: layer.route(x, bias), step.replay):
+        first.forward(x, bias)
+        between()
+        with pytest.raises(ValueError, match="another"):
+            first.backward(x)
+    second.forward(x, bias)
+    got = second.backward(x)
+    assert all(torch.equal(got[k], want[k]) for k in want)
+    second.backward(x)  # twice after one forward
