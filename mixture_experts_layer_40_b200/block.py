@@ -51,7 +51,7 @@ class MoEBlock:
             capi.moe_block_norm(x, self.eps, pre_weight=next_weight, u=u, z=self.z,
                                 post_weight=self.post_weight, gate=gate, scale=self.scale,
                                 alpha=self.alpha, r=r, stream=stream)
-            if r.data_ptr() != x.data_ptr():
+            if x.numel() == 0 or r.data_ptr() != x.data_ptr():  # (empty: both addresses are 0)
                 self.x, self.gate = x, gate
                 if next_weight is not None:
                     self.r, self.next_weight = r, next_weight

@@ -335,3 +335,19 @@ def test_block_makes_its_device_the_current_one(capi, monkeypatch):
     block.forward(x, None)
     block.backward(x, weights=False)
     assert Layer.seen == [1, 1] and now == [0]
+
+
+def test_block_of_no_rows_has_a_backward(capi, monkeypatch):
+    """Empty tensors all have the address 0: no forward in place."""
+    from mixture_experts_layer_40_b200.block import MoEBlock
+
+    for name in ("moe_block_norm", "moe_block_norm_backward"):
+        monkeypatch.setattr(capi, name, lambda *a, **k: None)
+    monkeypatch.setattr(capi, "moe_block_norm_backward_workspace_size", lambda H: 16)
+
+    class Layer(FakeLayer):
+        T = 0
+
+    block = MoEBlock(Layer(), torch.ones(64))
+    x = torch.zeros(0, 64)
+    assert "dx" in (block.forward(x, None), block.backward(x, weights=False))[1]
