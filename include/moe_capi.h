@@ -283,7 +283,7 @@ size_t moe_backward_workspace_size(moe_shape sh);
  *   topk_ids, topk_gates: the forward's [T, K] outputs; x: its bf16 input
  *   (only read for the weight gradients; may be NULL without them)
  *   dy, dx: bf16 [T, H], 16-byte aligned; dgates: float [T, K]
- *   dw13, dw2: the weight gradients, or both NULL to skip them
+ *   dw13, dw2: the weight gradients, or both NULL to skip them (T = 0: zero)
  *   ws: the forward's workspace (read only, apart from its status word);
  *   bws: moe_backward_workspace_size(sh) bytes, 256-byte aligned.
  * Errors: MOE_ERR_SHAPE, MOE_ERR_NULL, MOE_ERR_ALIGN, MOE_ERR_WORKSPACE; device

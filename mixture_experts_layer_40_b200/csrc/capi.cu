@@ -504,7 +504,13 @@ int moe_backward(moe_shape sh, const moe_weights* w, const moe_weights* wt,
   if (!aligned(ws, 256) || !aligned(bws, 256)) return MOE_ERR_ALIGN;
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   uint32_t* status = at<uint32_t>(ws, L.status);
-  if (sh.T == 0) return cuda_status(cudaMemsetAsync(status, 0, 4, s));
+  if (sh.T == 0) {  // an empty batch: zero weight gradients
+    const size_t weights = (size_t)(sh.N + 1) * sh.H * sh.I;
+    cudaError_t e = cudaMemsetAsync(status, 0, 4, s);
+    if (e == cudaSuccess && dw13) e = cudaMemsetAsync(dw13, 0, weights * 2 * sizeof(float), s);
+    if (e == cudaSuccess && dw2) e = cudaMemsetAsync(dw2, 0, weights * sizeof(float), s);
+    return cuda_status(e);
+  }
   if (!topk_ids || !topk_gates || !dy || !dx || !dgates) return MOE_ERR_NULL;
   if (!w->w13 || !w->s13 || !wt->w13 || !wt->s13 || !wt->w2 || !wt->s2) return MOE_ERR_NULL;
   if (!aligned(dy, 16) || !aligned(dx, 16) || !aligned(w->w13, 16) || !aligned(wt->w13, 16) ||

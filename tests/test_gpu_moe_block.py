@@ -325,3 +325,21 @@ def test_backward_after_another_pass_of_the_layer_is_refused():
     got = second.backward(x)
     assert all(torch.equal(got[k], want[k]) for k in want)
     second.backward(x)  # twice after one forward
+
+
+def test_block_of_no_rows():
+    """An empty batch: empty outputs, and zero weight gradients to the last one."""
+    from mixture_experts_layer_40_b200.block import MoEBlock
+    from mixture_experts_layer_40_b200.layer import MoELayer
+    case, layer, bias = a_layer()
+    empty = MoELayer(0, layer.H, layer.N, layer.K, layer.I, layer.weights)
+    w = torch.ones(layer.H, device="cuda")
+    block = MoEBlock(empty, w, w, w)
+    x = torch.empty(0, layer.H, dtype=BF16, device="cuda")
+    filler = [torch.full((17, 512, 256), 7.0, device="cuda") for _ in range(4)]
+    del filler  # memory that is not zero for the gradients
+    r, u = block.forward(x, bias, torch.empty(0, device="cuda"), next_weight=w)
+    g = block.backward(r, du=u)
+    assert r.shape == u.shape == g["dx"].shape == (0, layer.H) and empty.status() == 0
+    for k in ("pre_weight", "post_weight", "scale", "next_weight", "w13", "w2"):
+        assert not g[k].any(), k
