@@ -346,3 +346,50 @@ def test_column_sums_over_many_rows(capi, T, H, positive):
         t = b.double() * a.double() * torch.rsqrt((a.double() ** 2).mean(1, keepdim=True) + EPS)
         ref += torch.stack([t.sum(0), t.abs().sum(0)])
     assert ((dpre.double() - ref[0]).abs() <= 2.0 ** -19 * ref[1]).all()
+
+
+@pytest.mark.parametrize("T,H", [(2000, 512), (700, 1409), (1500, 7168), (40, 16384), (33, 331), (5, 8)])
+@pytest.mark.parametrize("act,res", [(BF16, FP32), (BF16, BF16), (FP32, FP32)])
+@pytest.mark.parametrize("gate", ["row", "full"])
+def test_backward_in_place(capi, T, H, act, res, gate):
+    """dx may be dr, and dz may be z or du: bit for bit the results of outputs of
+    their own, in the vector and the element-wise form, several rows a team."""
+    d = make(T, H, act, res, act, gate, True, True, True, True, seed=T)
+    want = backward(capi, d, d["x"])
+    ws = torch.empty(capi.moe_block_norm_backward_workspace_size(H), dtype=torch.uint8, device="cuda")
+    for on in ("z", "du"):
+        e = {k: v.clone() if isinstance(v, torch.Tensor) else v for k, v in d.items()}
+        col = lambda: torch.empty(H, device="cuda")  # noqa: E731
+        got = {"dx": e["dr"], "dz": e[on], "dgate": torch.empty_like(e["gate"]), "dscale": col(),
+               "dpost": col(), "dpre": col()}
+        capi.moe_block_norm_backward(e["x"], EPS, ws, dr=e["dr"], du=e["du"], pre_weight=e["pre"],
+                                     z=e["z"], post_weight=e["post"], gate=e["gate"],
+                                     scale=e["scale"], alpha=e["alpha"], **got)
+        for k in want:
+            assert torch.equal(got[k], want[k]), (on, k)
+
+
+@pytest.mark.parametrize("gate", ["none", "row", "full"])
+def test_misaligned_rows_backward(capi, gate):
+    """Views that start off a 16-byte boundary take the element-wise path, whose
+    gradients are within the tolerances of the formula as well."""
+    T, H = 300, 512
+    d = make(T, H, BF16, FP32, BF16, gate, True, True, True, True)
+    shift = lambda t: torch.cat([t.new_zeros(1), t.flatten()])[1:].view(t.shape)  # noqa: E731
+    m = {k: shift(v) if isinstance(v, torch.Tensor) else v for k, v in d.items()}
+    assert m["z"].data_ptr() % 16 == 2 and m["x"].data_ptr() % 16 == 4
+    o, e = backward(capi, m, m["x"]), dbl(d)
+    inv = lambda v: torch.rsqrt((v * v).mean(1, keepdim=True) + EPS)  # noqa: E731
+    R, Z = inv(e["x"]), inv(e["z"])
+    h, y, w = e["x"] * R, e["z"] * Z, e["du"] * e["pre"]
+    up = e["dr"] + R * (w - h * (w * h).mean(1, keepdim=True))
+    mag = e["dr"].abs() + R * (w.abs() + h.abs() * (w * h).abs().mean(1, keepdim=True))
+    k = e["alpha"] * e["s"] * e["p"] * e["g"]
+    q, mq = k * up, k.abs() * mag
+    close(o["dx"], up, mag, 256, "dx")
+    close(o["dz"], Z * (q - y * (q * y).mean(1, keepdim=True)),
+          Z * (mq + y.abs() * (mq * y.abs()).mean(1, keepdim=True)), 256, "dz")
+    close(o["dpre"], (e["du"] * h).sum(0), (e["du"] * h).abs().sum(0), 512, "dpre")
+    t, mt = e["alpha"] * e["g"] * up * y, e["alpha"] * e["g"] * mag * y.abs()
+    close(o["dpost"], (t * e["s"]).sum(0), (mt * e["s"].abs()).sum(0), 512, "dpost")
+    close(o["dscale"], (t * e["p"]).sum(0), (mt * e["p"].abs()).sum(0), 512, "dscale")

@@ -265,3 +265,26 @@ def test_dropped_holders_keep_their_memory_until_done(capi, n):
         torch.cuda.synchronize()
         assert abs(float(norm) - total) <= 6 * U * total
         del held
+
+
+def test_long_list_in_a_graph(capi):
+    """A list with a table, made before a capture: the graph clips what its
+    gradients hold at each replay."""
+    from mixture_experts_layer_40_b200.block import GradClip
+    g = grads_of([(i * 91) % 3000 + 1 for i in range(50)], [FP32, BF16])
+    clip = GradClip(g)
+    clip(math.inf)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        norm = clip(1.0)
+    for scale in (3.0, 0.25):
+        fresh = grads_of([t.numel() for t in g], [FP32, BF16], seed=9, std=scale)
+        for a, b in zip(g, fresh):
+            a.copy_(b)
+        graph.replay()
+        total = math.sqrt(sum(float((x.double() ** 2).sum()) for x in fresh))
+        assert abs(float(norm) - total) <= 6 * U * total
+        for a, b in zip(g, fresh):
+            want = b.double() / (total + 1e-6)
+            tol = (9 * U + (0 if a.dtype == FP32 else torch.finfo(a.dtype).eps / 2 * 1.001)) * want.abs()
+            assert ((a.double() - want).abs() <= tol + 1e-40).all()
