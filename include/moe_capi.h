@@ -523,7 +523,8 @@ int moe_block_norm_backward(int64_t T, int32_t H, int32_t res_type, int32_t act_
  * moe_grad_clip adds the partials, writes the norm (float [1]) and scales.
  *   max_norm >= 0, infinity allowed. In place nothing is touched when c = 1.
  *   An infinite norm under an infinite max_norm makes c NaN.
- * Squares are summed in fp64, in a fixed order. A NaN in any gradient makes
+ * Squares are summed 4 or 8 at a time in fp32 (in fp64 where fp32 cannot hold
+ * them) and from there in fp64, in a fixed order. A NaN in any gradient makes
  * the norm and every gradient NaN; an infinity makes the norm infinite, the
  * infinite gradients NaN and the others zero.
  */

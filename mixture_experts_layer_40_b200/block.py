@@ -1,6 +1,10 @@
 """The Transformer block around an MoE layer, per-expert linear maps in 16
 bits, and gradient clipping: thin holders of device memory over the C ABI, as
 layer.MoELayer is. All compute is in the CUDA library.
+
+A holder's buffers serve one call at a time: calls on several streams at once,
+or two captured graphs replayed side by side, need holders of their own. A graph
+that holds a call uses the holder's memory: keep the holder as long as the graph.
 """
 from __future__ import annotations
 

@@ -16,9 +16,9 @@
 // latency of the row sums (two in the forward, which takes two rows a step;
 // three phases in the backward, one row a team at a time). 4096 rows of 7168
 // in bf16, x and z to r and u: 47 us, 77% of the copy rate; backward of
-// 16384 rows with an fp32 residual stream: 493 to 498 us, 66%. Odd widths go
+// 16384 rows with an fp32 residual stream: 492 to 498 us, 66%. Odd widths go
 // element by element and are bound by instructions: 777 rows of 1409 in fp16,
-// backward, 16.7 us (floor 2.7).
+// backward, 17 us (floor 2.7).
 #include <type_traits>
 
 #include "kernels.cuh"
@@ -743,8 +743,10 @@ struct Plan {
 };
 
 // 8 columns a thread up to 7168 columns (the backward: 4096), 16 up to 8192
-// and 32 above: the weights and column sums of so many fit in registers
-// beside the row's. One CTA per SM, with fewer teams where there are not rows
+// and 32 above. The weights and column sums of 8 and 16 columns fit in registers
+// beside the row's (but for 4 to 52 bytes in some backwards of 16); of 32 they
+// do not: those backwards spill 550 to 670 bytes a thread, the forwards 40 to
+// 190. One CTA per SM, with fewer teams where there are not rows
 // enough for every SM's; the forward takes two rows a step where every team
 // has more. per_column: bytes of the row tensors per column.
 Plan plan_of(int64_t T, int H, int per_column, bool vec, int sms, bool backward) {

@@ -28,8 +28,9 @@
 // Bound by HBM where groups are short (the weights, once): 8 rows of 64 groups
 // at 4096 x 7168 take 77 us (floor 69), 1024 rows at 7168 x 2048 take 295
 // (294). Long groups are bound by the tensor cores at the clock that the power
-// limit leaves: 32768 rows of 32 groups at 4096 x 7168 take 1468 to 1730 us,
-// 1.11 to 1.31 PFLOP/s.
+// limit leaves: 32768 rows of 32 groups at 4096 x 7168 take 1402 us in short
+// bursts (1.37 PFLOP/s) and 1830 in a run of seconds (1.05), where the clock
+// falls to 1000 MHz and the MMAs of the groups' rows fill 87% of its cycles.
 //
 // One persistent CTA per SM:
 //   warp 0     TMA producer: 64-deep k-blocks into a ring of stages
@@ -929,7 +930,7 @@ __global__ void __cluster_dims__(kCtas * kSplit, 1, 1)
 // 8192, 65536 rows: off by 4.7e-7, 4.8e-7, 4.8e-7, 5.2e-7 of the result).
 //
 // Measured: 32 groups of 16384 rows in all, dw 7168 x 2048 in fp32, take 617
-// to 889 us (floor 338). What bounds it is what SMs and L2 exchange: 3.8 GB of
+// to 1033 us from process to process (floor 338). What bounds it is what SMs and L2 exchange: 3.8 GB of
 // operand tiles in and 1.9 GB of dw out, 9.1 TB/s in 617 us; without the
 // stores it takes 438 (8.6 TB/s), with a stage less 639.
 constexpr int kSegment = 8;  // k-blocks per TMEM sum
