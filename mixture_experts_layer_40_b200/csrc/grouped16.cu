@@ -450,11 +450,11 @@ struct MatCfg {
 };
 
 // The tensor core's fp32 sums round towards zero at every step of 16 products:
-// 2^-24 of the sum a step where all products are positive, always downwards
-// (448 steps 2.7e-5, 4096 3.5e-4). So one TMEM sum runs only as far as that
-// stays under a sixteenth of half a step of the output's type, and the segments
-// are added up in registers, rounded to nearest: 8192 products for fp16, 65536
-// for bf16, and for fp32 outputs the 512 of the weight gradient.
+// where all products are positive they are too small by about 2^-24 a step (448
+// steps 2.7e-5, 4096 3.5e-4). So one TMEM sum runs only as far as that stays
+// under a tenth of half a step of the output's type, and the segments are added
+// up in registers, rounded to nearest: 8192 products for fp16, 65536 for bf16,
+// and for fp32 outputs the 512 of the weight gradient.
 inline int segment_blocks(int out_type) {
   return out_type == MOE_FP32 ? 8 : out_type == MOE_FP16 ? 128 : 1024;
 }

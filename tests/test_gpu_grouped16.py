@@ -470,10 +470,10 @@ def test_matmul_long_sums_keep_fp32(capi, counts, K, N, positive, trans):
 @pytest.mark.parametrize("dtype,K", [(FP16, 65544), (BF16, 262144)])
 def test_matmul_long_sums_have_no_offset(capi, counts, N, dtype, K):
     """All products positive, 16-bit outputs: truncated sums are too small by a
-    share that grows with their steps. A segment's (512 steps for fp16, 4096 for
-    bf16, half of 2^-23 a step at half of the sum: under 2^-16 and 2^-13) stays
-    below an eighth of half a step of the type; the roundings of the outputs have
-    no offset."""
+    share that grows with their steps. A segment has 512 steps for fp16 and 4096
+    for bf16, each off by at most 2^-22 of the running sum, which is half of the
+    whole on the average: 2^-14 and 2^-11, an eighth of half a step of the type.
+    The roundings of the outputs have no offset."""
     offset, err = offset_and_error(capi, counts, K, N, dtype, dtype, True, True)
     half = torch.finfo(dtype).eps / 2
     assert abs(offset) < half / 8 and err < half, (offset, err)
@@ -482,7 +482,7 @@ def test_matmul_long_sums_have_no_offset(capi, counts, N, dtype, K):
 def test_wgrad_short_group_behind_seconds_of_others(capi):
     """A CTA works for longer than the kernel's wait limit (2 s) on a group whose
     rows need no clearing before it comes to one whose rows do. 149 groups of one
-    tile go round 148 CTAs, so the first and the last share one; the first has a
+    tile are spread over 148 CTAs, so the first and the last share one; the first has a
     billion rows, at a quarter of a microsecond for 64. Sums of ones are exact."""
     from mixture_experts_layer_40_b200 import capi as c
     sms = c.LIB.moe_device_sm_count()
